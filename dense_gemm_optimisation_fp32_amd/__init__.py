@@ -385,3 +385,9 @@ def linear(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor | None = None, a
     plan = get_plan(m, n, k, layout_b, lda, ldb, ldc, None, A.device.index, layout_a, 1, stream=stream)
     plan.run_ex(A.data_ptr(), B.data_ptr(), out.data_ptr(), alpha, beta, bias_ptr, act, stream)
     return out
+
+
+# The expert-layer operators (include/expert_ops.h).
+from .expert_ops import (  # noqa: E402
+    EXPERT_BF16, EXPERT_F32, EXPERT_FUNCTIONS, Mx4Tensor, Routing, grouped_linear, grouped_weight_grad,
+    mx4_dequantize, mx4_linear, mx4_quantize, route, route_grad)

@@ -5,8 +5,9 @@ Usage: ``python -m dense_gemm_optimisation_fp32_amd.build`` (or call
 
 The kernels are compiled in several translation units in parallel
 (``csrc/k_*.hip``, explicit instantiations of the lists in
-``csrc/kernel_list.hpp``); the host unit ``csrc/gemm_f32.hip`` holds the C ABI
-and only takes the kernels' handles.  The compiler's per-kernel resource
+``csrc/kernel_list.hpp``, and the expert-layer kernels with their launches);
+the host units ``csrc/gemm_f32.hip`` and ``csrc/expert_ops.hip`` hold the C ABI
+and only take the kernels' handles.  The compiler's per-kernel resource
 report (VGPRs, AGPRs, SGPRs, LDS, scratch, occupancy) is kept in
 ``_build/kernel_resources.txt`` for the tile/occupancy sweep and compiled into
 the library as a table (``_build/kernel_resources.cpp``), which
@@ -26,7 +27,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libgemm_f32.so")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
-HOST_SOURCE = os.path.join(CSRC, "gemm_f32.hip")
+HOST_SOURCES = [os.path.join(CSRC, "gemm_f32.hip"), os.path.join(CSRC, "expert_ops.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 HIPCC_FLAGS = [
@@ -99,7 +100,7 @@ def build(verbose: bool = False) -> str:
     inc = ["-I", INCLUDE, "-I", CSRC]
     jobs = []
     objs = []
-    for src in kernel_sources() + [HOST_SOURCE]:
+    for src in kernel_sources() + HOST_SOURCES:
         obj = os.path.join(BUILD_DIR, os.path.basename(src).replace(".hip", ".o"))
         objs.append(obj)
         jobs.append(([HIPCC, *HIPCC_FLAGS, *inc, REMARKS, "-c", "-o", obj, src], src))
@@ -107,14 +108,14 @@ def build(verbose: bool = False) -> str:
 
     report = []
     entries = []
-    for src in kernel_sources() + [HOST_SOURCE]:
+    for src in kernel_sources() + HOST_SOURCES:
         rc, err = results[src]
         report.append(err)
         if rc != 0:
             _fail(f"hipcc {os.path.basename(src)}", err)
         found = parse_resources(err)
-        if src == HOST_SOURCE and found:
-            raise RuntimeError("kernels instantiated in the host unit (add them to csrc/kernel_list.hpp): "
+        if src in HOST_SOURCES and found:
+            raise RuntimeError("kernels instantiated in a host unit (instantiate them in a kernel unit): "
                                + ", ".join(n for n, _ in found[:5]))
         entries.extend(found)
     with open(os.path.join(BUILD_DIR, "kernel_resources.txt"), "w") as f:

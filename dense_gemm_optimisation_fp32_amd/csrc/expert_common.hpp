@@ -1,0 +1,149 @@
+// Device helpers shared by the expert-layer kernels (products grouped by
+// expert, 4-bit products, routing): the launch arguments, the search for the
+// rows that a workgroup's tile covers, and 16-bit conversions.
+#pragma once
+
+#include "device_common.hpp"
+
+namespace gemmf32 {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef unsigned char u8;
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// Launch arguments of the grouped kernels.  Strides and extents in bytes.
+struct GroupedArgs {
+    const char *A;             // rows of A, sorted by expert
+    const char *B;             // the experts' matrices (weight gradient: the rows of G)
+    char *C;                   // rows of C (weight gradient: the experts' matrices)
+    const u8 *a_scales;        // 4-bit products: scales of A and B, (k / 128, rows, 4)
+    const u8 *b_scales;
+    const float *bias;         // (groups, n) or NULL
+    const int *offsets;        // groups + 1 row offsets, or NULL: one expert with every row
+    int m, n, k;               // rows of A, columns of C, contraction (weight gradient: rows of dB)
+    int groups;
+    long long lda, ldb, ldc;   // bytes from row to row (B: from k-row to k-row, or column to column)
+    long long expert_stride;   // bytes from expert to expert (B; weight gradient: C)
+    long long bias_stride;     // floats from expert to expert
+    int tiles_m, tiles_n;      // tiles_m: bound on the row tiles of all experts
+    int group_m;               // row tiles per rasterisation group
+    int num_xcd;
+    int act;                   // 0 none, 1 ReLU, 2 GELU
+    int a_kblocks;             // 4-bit products: 128-column blocks of a row
+};
+
+// The rows of one tile: expert (-1: rows of no expert, which become zero),
+// its first row, and the expert's rows from there on.
+struct RowTile {
+    int expert, row, rows;
+};
+
+// Rows of entry e: an expert, or (the two entries after the experts) the rows
+// after the last expert's and before the first's.  Offsets are read from
+// device memory that the host has not seen, so they are clamped to the rows
+// there are: a wrong list gives wrong rows, never an access outside A and C.
+__device__ __forceinline__ void entry_rows(const GroupedArgs &g, int e, int &lo, int &hi)
+{
+    if (!g.offsets) {
+        lo = 0;
+        hi = e == 0 ? g.m : 0;
+        return;
+    }
+    lo = hi = 0;
+    if (e < g.groups) {
+        lo = g.offsets[e];
+        hi = g.offsets[e + 1];
+    } else if (e == g.groups) {
+        lo = g.offsets[g.groups];
+        hi = g.m;
+    } else if (e == g.groups + 1) {
+        hi = g.offsets[0];
+    }
+    lo = min(max(lo, 0), g.m);
+    hi = min(max(hi, lo), g.m);
+}
+
+__device__ __forceinline__ int wave_inclusive_sum(int x, int lane)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    return x;
+}
+
+// Workgroup id -> (row tile, column tile), and the rows of that row tile.
+// Every wavefront does it for itself, 64 experts at a time: the experts' row
+// tiles are counted and summed over the lanes (the number of row tiles is
+// only known on the device), the workgroup's place is taken from the actual
+// number of tiles, so that the XCDs share the real work evenly, and the
+// expert is found by ballot.  False: the workgroup is past the last tile.
+template <int BM>
+__device__ __forceinline__ bool find_tile(const GroupedArgs &g, int wg, int lane, RowTile &rt, int &tn)
+{
+    const int entries = g.offsets ? g.groups + 2 : 1;
+    auto tiles_of = [](int lo, int hi) { return (hi - lo + BM - 1) / BM; };
+    int total = 0, base = (entries - 1) / 64 * 64;
+    int lo, hi, sum;
+    for (int b = 0; b <= base; b += 64) {
+        entry_rows(g, b + lane, lo, hi);
+        sum = wave_inclusive_sum(tiles_of(lo, hi), lane);
+        total += __builtin_amdgcn_readlane(sum, 63);
+    }
+    const int all = min(total, g.tiles_m);
+    if (wg >= all * g.tiles_n) return false;
+    const int logical = xcd_contiguous(wg, all * g.tiles_n, g.num_xcd);
+    const int width = g.group_m * g.tiles_n;
+    const int first = logical / width * g.group_m;
+    const int size = min(all - first, g.group_m);
+    const int r = logical % width;
+    const int tm = first + r % size;
+    tn = r / size;
+    // Back from the last 64 entries to those that hold row tile tm.
+    int before = total - __builtin_amdgcn_readlane(sum, 63);
+    while (before > tm) {
+        base -= 64;
+        entry_rows(g, base + lane, lo, hi);
+        sum = wave_inclusive_sum(tiles_of(lo, hi), lane);
+        before -= __builtin_amdgcn_readlane(sum, 63);
+    }
+    // The first lane whose running sum passes tm.
+    const int at = __builtin_ctzll(__ballot(before + sum > tm));
+    const int inside = tm - before - (__builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(tiles_of(lo, hi), at));
+    rt.row = __builtin_amdgcn_readlane(lo, at) + inside * BM;
+    rt.rows = __builtin_amdgcn_readlane(hi, at) - rt.row;
+    rt.expert = base + at < g.groups ? base + at : -1;
+    return true;
+}
+
+// 16 bytes of a row at p, elements at or past `left` zero.  Any alignment that
+// the elements have: unaligned wide loads are in order on this target.
+template <class E>
+__device__ __forceinline__ i32x4 load_chunk(const E *p, int left)
+{
+    constexpr int N = 16 / sizeof(E);
+    struct __attribute__((packed, aligned(sizeof(E)))) Chunk {
+        i32x4 v;
+    };
+    if (left >= N) return reinterpret_cast<const Chunk *>(p)->v;
+    i32x4 r = {};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < left) {
+            if constexpr (sizeof(E) == 4) r[i] = reinterpret_cast<const int *>(p)[i];
+            else r[i / 2] |= (int)reinterpret_cast<const unsigned short *>(p)[i] << (16 * (i & 1));
+        }
+    return r;
+}
+
+// (Compared so that a NaN stays one.)
+__device__ __forceinline__ float activate(float x, int act)
+{
+    if (act == 1) x = x < 0.0f ? 0.0f : x;
+    return act == 2 ? gelu_erf(x) : x;
+}
+
+}  // namespace gemmf32

@@ -1,0 +1,44 @@
+// Launches of the expert-layer kernels, defined in their translation units
+// and called by the C entry points in expert_ops.hip.
+#pragma once
+
+#include "expert_common.hpp"
+
+namespace gemmf32 {
+
+struct Mx4Args;
+struct RouteArgs;
+
+// Bound on the row tiles of bm rows: each run of rows (the experts' and the
+// two of no expert) has at most one tile that is not full.
+inline int grouped_row_tiles(const GroupedArgs &a, int bm)
+{
+    const long long tiles = (long long)a.m / bm + (a.offsets ? a.groups + 2 : 1);
+    return (int)(tiles < a.m ? tiles : a.m);
+}
+
+// Which of a tile shape's kernels a call takes.
+struct LpCall {
+    bool fp4, bf16;         // 4-bit operands; 16-bit results
+    bool b_contiguous;      // B's columns contiguous along k
+    bool weight_grad;
+    bool wide;              // 16-byte stores of C
+};
+
+// Status of the current device (a gemm_f32_status) and its facts; a failed
+// HIP call's status, recorded for gemm_f32_last_hip_error.  In gemm_f32.hip.
+int current_device(int *cu_count, int *num_xcd);
+int record_hip_error(hipError_t e);
+
+void launch_mx4_quantize(const Mx4Args &a, bool bf16, bool columns, hipStream_t s);
+void launch_mx4_dequantize(const Mx4Args &a, bool bf16, hipStream_t s);
+void launch_f32_grouped(GroupedArgs a, bool b_contiguous, hipStream_t s);
+void launch_f32_weight_grad(GroupedArgs a, hipStream_t s);
+void launch_lp256(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+void launch_lp128(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+void launch_lp128_unaligned(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+// At most 16 or 32 rows a tile (row_tiles 1 or 2).
+void launch_few(const GroupedArgs &a, bool bf16, bool fp4, bool b_contiguous, int row_tiles, hipStream_t s);
+void launch_route(const RouteArgs &a, bool bf16, bool grad, hipStream_t s);
+
+}  // namespace gemmf32

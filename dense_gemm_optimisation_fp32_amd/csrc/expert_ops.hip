@@ -1,0 +1,316 @@
+// C entry points of include/expert_ops.h: argument checks, the choice of a
+// kernel, and its launch.  No kernel is compiled in this unit.
+#include "expert_ops.h"
+
+#include "expert_launch.hpp"
+#include "mx4.hpp"
+#include "route.hpp"
+
+using namespace gemmf32;
+
+namespace {
+
+constexpr int64_t kMaxInt = 0x7fffffff;
+constexpr int64_t kMaxRowBytes = (int64_t)8 << 20;
+
+bool size_ok(int64_t v, int64_t least) { return v >= least && v <= kMaxInt; }
+bool dtype_ok(int d) { return d == EXPERT_F32 || d == EXPERT_BF16; }
+bool layout_ok(int l) { return l == GEMM_F32_ROW_MAJOR || l == GEMM_F32_COL_MAJOR; }
+int64_t elem(int dtype) { return dtype == EXPERT_BF16 ? 2 : 4; }
+bool aligned(const void *p, int64_t to) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)to == 0; }
+bool here(const void *p, int64_t to) { return p && aligned(p, to); }
+int64_t padded(int64_t k) { return (k + 127) / 128 * 128; }
+
+hipStream_t stream_of(void *s) { return reinterpret_cast<hipStream_t>(s); }
+
+int launched()
+{
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? GEMM_F32_SUCCESS : record_hip_error(e);
+}
+
+// Whether rows of C can be stored 16 bytes at a time.
+bool wide_rows(const void *c, int64_t row_bytes, int64_t n, int64_t size)
+{
+    return aligned(c, 16) && row_bytes % 16 == 0 && n * size % 16 == 0;
+}
+
+// The tiles' workgroups are counted in 32 bits.
+bool grid_ok(int64_t rows, int64_t cols, int64_t row_tile, int64_t col_tile, int64_t more)
+{
+    return (rows / row_tile + more) <= kMaxInt / ((cols + col_tile - 1) / col_tile);
+}
+
+// Rows an expert has on average.
+int64_t mean_rows(int64_t m, int64_t groups) { return (m + groups - 1) / groups; }
+
+// Up to this many rows an expert on average, the few-row kernels.
+constexpr int64_t kFewRows = 16;
+
+}  // namespace
+
+extern "C" {
+
+int expert_grouped_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups, const void *A, int64_t lda,
+                          const void *B, int layout_b, int64_t ldb, int64_t expert_stride, const int *offsets,
+                          const float *bias, int activation, void *C, int64_t ldc, void *stream)
+{
+    const bool col = layout_b == GEMM_F32_COL_MAJOR;
+    if (!dtype_ok(dtype) || !layout_ok(layout_b) || !size_ok(m, 0) || !size_ok(n, 1) || !size_ok(k, 1) ||
+        !size_ok(groups, 1) || lda < k || ldb < (col ? k : n) || ldc < n || expert_stride < 0 || activation < 0 ||
+        activation > 2)
+        return GEMM_F32_ERR_INVALID_VALUE;
+    const int64_t size = elem(dtype);
+    if (lda * size >= kMaxRowBytes || ldb * size >= kMaxRowBytes || ldc * size >= kMaxRowBytes)
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (!here(offsets, 4) || !here(B, size) || (bias && !aligned(bias, 4)) || (m > 0 && (!here(A, size) || !here(C, size))))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (dtype == EXPERT_F32 && (col ? (n - 1) * ldb + k : (k - 1) * ldb + n) * size > kMaxInt - 3)
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (!grid_ok(m, n, 16, 32, groups + 2)) return GEMM_F32_ERR_INVALID_VALUE;
+    GroupedArgs a{};
+    const int st = current_device(nullptr, &a.num_xcd);
+    if (st != GEMM_F32_SUCCESS) return st;
+    if (m == 0) return GEMM_F32_SUCCESS;
+    a.A = static_cast<const char *>(A);
+    a.B = static_cast<const char *>(B);
+    a.C = static_cast<char *>(C);
+    a.bias = bias;
+    a.offsets = offsets;
+    a.m = (int)m;
+    a.n = (int)n;
+    a.k = (int)k;
+    a.groups = (int)groups;
+    a.lda = lda * size;
+    a.ldb = ldb * size;
+    a.ldc = ldc * size;
+    a.expert_stride = expert_stride * size;
+    a.bias_stride = n;
+    a.group_m = 8;
+    a.act = activation;
+    const hipStream_t s = stream_of(stream);
+    const int64_t rows = mean_rows(m, groups);
+    // The copies of the bfloat16 tiles need 4-byte aligned rows.
+    const bool copies = dtype == EXPERT_F32 || (aligned(A, 4) && aligned(B, 4) && a.lda % 4 == 0 && a.ldb % 4 == 0 &&
+                                                a.expert_stride % 4 == 0);
+    if (rows <= kFewRows) {
+        launch_few(a, dtype == EXPERT_BF16, false, col, rows <= 16 ? 1 : 2, s);
+    } else if (dtype == EXPERT_F32) {
+        launch_f32_grouped(a, col, s);
+    } else {
+        const LpCall c{false, true, col, false, wide_rows(C, a.ldc, n, size)};
+        if (!copies) launch_lp128_unaligned(a, c, s);
+        else if (rows >= 256) launch_lp256(a, c, s);
+        else launch_lp128(a, c, s);
+    }
+    return launched();
+}
+
+int expert_grouped_weight_grad(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups, const void *A, int64_t lda,
+                               const void *G, int64_t ldg, const int *offsets, void *dB, int64_t ldd,
+                               int64_t expert_stride, void *stream)
+{
+    if (!dtype_ok(dtype) || !size_ok(m, 0) || !size_ok(n, 1) || !size_ok(k, 1) || !size_ok(groups, 1) || lda < k ||
+        ldg < n || ldd < n || expert_stride < 0)
+        return GEMM_F32_ERR_INVALID_VALUE;
+    const int64_t size = elem(dtype);
+    if (lda * size >= kMaxRowBytes || ldg * size >= kMaxRowBytes || ldd * size >= kMaxRowBytes)
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (!here(offsets, 4) || !here(dB, size) || (m > 0 && (!here(A, size) || !here(G, size))))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (dtype == EXPERT_F32 && ((k - 1) * ldd + n) * size > kMaxInt - 3) return GEMM_F32_ERR_INVALID_VALUE;
+    if ((k + 63) / 64 * ((n + 63) / 64) > kMaxInt / groups) return GEMM_F32_ERR_INVALID_VALUE;
+    GroupedArgs a{};
+    const int st = current_device(nullptr, &a.num_xcd);
+    if (st != GEMM_F32_SUCCESS) return st;
+    a.A = static_cast<const char *>(A);
+    a.B = static_cast<const char *>(G);
+    a.C = static_cast<char *>(dB);
+    a.offsets = offsets;
+    a.m = (int)m;
+    a.n = (int)n;
+    a.k = (int)k;
+    a.groups = (int)groups;
+    a.lda = lda * size;
+    a.ldb = ldg * size;
+    a.ldc = ldd * size;
+    a.expert_stride = expert_stride * size;
+    a.group_m = 8;
+    const hipStream_t s = stream_of(stream);
+    if (dtype == EXPERT_F32) {
+        launch_f32_weight_grad(a, s);
+    } else {
+        const LpCall c{false, true, false, true, wide_rows(dB, a.ldc, n, size) && a.expert_stride % 16 == 0};
+        const bool copies = aligned(A, 4) && aligned(G, 4) && a.lda % 4 == 0 && a.ldb % 4 == 0;
+        if (!copies) launch_lp128_unaligned(a, c, s);
+        else if (k >= 256 && n >= 256) launch_lp256(a, c, s);
+        else launch_lp128(a, c, s);
+    }
+    return launched();
+}
+
+int expert_mx4_quantize(int dtype, int64_t rows, int64_t k, const void *X, int layout, int64_t ld, void *codes,
+                        void *scales, void *stream)
+{
+    if (!dtype_ok(dtype) || !layout_ok(layout) || !size_ok(rows, 0) || !size_ok(k, 1) || k > kMaxInt - 1024 ||
+        ld < (layout == GEMM_F32_COL_MAJOR ? rows : k))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (rows > 0 && (!here(X, elem(dtype)) || !here(codes, 16) || !here(scales, 4))) return GEMM_F32_ERR_INVALID_VALUE;
+    if (rows > (kMaxInt - 3) / ((k + 31) / 32)) return GEMM_F32_ERR_INVALID_VALUE;
+    const int st = current_device(nullptr, nullptr);
+    if (st != GEMM_F32_SUCCESS) return st;
+    if (rows == 0) return GEMM_F32_SUCCESS;
+    const Mx4Args a{static_cast<const char *>(X), static_cast<u8 *>(codes), static_cast<u8 *>(scales), ld, (int)rows,
+                    (int)k, (int)padded(k)};
+    launch_mx4_quantize(a, dtype == EXPERT_BF16, layout == GEMM_F32_COL_MAJOR, stream_of(stream));
+    return launched();
+}
+
+int expert_mx4_dequantize(int dtype, int64_t rows, int64_t k, const void *codes, const void *scales, void *X,
+                          int64_t ld, void *stream)
+{
+    if (!dtype_ok(dtype) || !size_ok(rows, 0) || !size_ok(k, 1) || k > kMaxInt - 1024 || ld < k)
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (rows > 0 && (!here(X, elem(dtype)) || !here(codes, 16) || !here(scales, 4))) return GEMM_F32_ERR_INVALID_VALUE;
+    if (rows > (kMaxInt - 3) / ((k + 31) / 32)) return GEMM_F32_ERR_INVALID_VALUE;
+    const int st = current_device(nullptr, nullptr);
+    if (st != GEMM_F32_SUCCESS) return st;
+    if (rows == 0) return GEMM_F32_SUCCESS;
+    const Mx4Args a{static_cast<const char *>(X), static_cast<u8 *>(const_cast<void *>(codes)),
+                    static_cast<u8 *>(const_cast<void *>(scales)), ld, (int)rows, (int)k, (int)padded(k)};
+    launch_mx4_dequantize(a, dtype == EXPERT_BF16, stream_of(stream));
+    return launched();
+}
+
+int64_t expert_mx4_workspace(int64_t m, int64_t n, int64_t k, int64_t groups)
+{
+    if (!size_ok(m, 1) || !size_ok(n, 1) || !size_ok(k, 1) || !size_ok(groups, 1)) return 0;
+    if (mean_rows(m, groups) <= kFewRows) return 0;
+    // X's codes and scales.
+    return m * (padded(k) / 2 + padded(k) / 32);
+}
+
+int expert_mx4_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups, const void *X, int64_t ldx,
+                      const void *codes, const void *scales, const int *offsets, const float *bias, int activation,
+                      void *Y, int64_t ldy, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (!dtype_ok(dtype) || !size_ok(m, 0) || !size_ok(n, 1) || !size_ok(k, 1) || !size_ok(groups, 1) || ldx < k ||
+        ldy < n || activation < 0 || activation > 2 || (!offsets && groups != 1))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    const int64_t size = elem(dtype), kp = padded(k);
+    if (ldx * size >= kMaxRowBytes || ldy * size >= kMaxRowBytes || kp > kMaxRowBytes) return GEMM_F32_ERR_INVALID_VALUE;
+    if ((offsets && !aligned(offsets, 4)) || !here(codes, 16) || !here(scales, 4) || (bias && !aligned(bias, 4)) ||
+        (m > 0 && (!here(X, size) || !here(Y, size))))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (!grid_ok(m, n, 16, 32, groups + 2) || m > (kMaxInt - 3) / ((k + 31) / 32)) return GEMM_F32_ERR_INVALID_VALUE;
+    const int64_t need = expert_mx4_workspace(m, n, k, groups);
+    if (need > 0 && !here(workspace, 16)) return GEMM_F32_ERR_INVALID_VALUE;
+    if (workspace_bytes < need) return GEMM_F32_ERR_SCRATCH_TOO_SMALL;
+    GroupedArgs a{};
+    const int st = current_device(nullptr, &a.num_xcd);
+    if (st != GEMM_F32_SUCCESS) return st;
+    if (m == 0) return GEMM_F32_SUCCESS;
+    a.A = static_cast<const char *>(X);
+    a.B = static_cast<const char *>(codes);
+    a.C = static_cast<char *>(Y);
+    a.b_scales = static_cast<const u8 *>(scales);
+    a.bias = bias;
+    a.offsets = offsets;
+    a.m = (int)m;
+    a.n = (int)n;
+    a.k = (int)k;
+    a.groups = (int)groups;
+    a.lda = ldx * size;
+    a.ldb = kp / 2;
+    a.ldc = ldy * size;
+    a.expert_stride = n * (kp / 2);
+    a.bias_stride = n;
+    a.group_m = 8;
+    a.act = activation;
+    a.a_kblocks = (int)(kp / 128);
+    const hipStream_t s = stream_of(stream);
+    const bool bf16 = dtype == EXPERT_BF16;
+    const int64_t rows = mean_rows(m, groups);
+    if (need == 0) {
+        launch_few(a, bf16, true, true, 1, s);
+        return launched();
+    }
+    u8 *const xc = static_cast<u8 *>(workspace), *const xs = xc + m * (kp / 2);
+    launch_mx4_quantize(Mx4Args{static_cast<const char *>(X), xc, xs, ldx, (int)m, (int)k, (int)kp}, bf16, false, s);
+    a.A = reinterpret_cast<const char *>(xc);
+    a.a_scales = xs;
+    a.lda = kp / 2;
+    const LpCall c{true, bf16, true, false, wide_rows(Y, a.ldc, n, size)};
+    if (rows >= 256) launch_lp256(a, c, s);
+    else launch_lp128(a, c, s);
+    return launched();
+}
+
+int64_t expert_route_workspace(int64_t tokens, int64_t groups)
+{
+    if (!size_ok(tokens, 1) || !size_ok(groups, 1) || tokens <= kRouteTokens) return 0;
+    return (tokens + kRouteTokens - 1) / kRouteTokens * groups * 4;
+}
+
+int expert_route(int dtype, int64_t tokens, int64_t groups, int64_t choices, int normalize, const void *logits,
+                 int64_t ld, float *weights, int *experts, int *offsets, int *order, void *workspace,
+                 int64_t workspace_bytes, void *stream)
+{
+    if (!dtype_ok(dtype) || !size_ok(tokens, 0) || groups < 1 || groups > kRouteMaxExperts || choices < 1 ||
+        choices > groups || choices > kRouteMaxChoices || tokens * choices > kMaxInt || ld < groups ||
+        (normalize != 0 && normalize != 1) || !here(offsets, 4))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (tokens > 0 && (!here(logits, elem(dtype)) || !here(weights, 4) || !here(experts, 4) || !here(order, 4)))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    const int64_t need = expert_route_workspace(tokens, groups);
+    if (need > 0 && !here(workspace, 4)) return GEMM_F32_ERR_INVALID_VALUE;
+    if (workspace_bytes < need) return GEMM_F32_ERR_SCRATCH_TOO_SMALL;
+    const int st = current_device(nullptr, nullptr);
+    if (st != GEMM_F32_SUCCESS) return st;
+    RouteArgs a{};
+    a.logits = logits;
+    a.ld = ld;
+    a.weights = weights;
+    a.experts = experts;
+    a.offsets = offsets;
+    a.order = order;
+    a.counts = static_cast<int *>(workspace);
+    a.tokens = (int)tokens;
+    a.groups = (int)groups;
+    a.choices = (int)choices;
+    a.normalize = normalize;
+    launch_route(a, dtype == EXPERT_BF16, false, stream_of(stream));
+    return launched();
+}
+
+int expert_route_grad(int dtype, int64_t tokens, int64_t groups, int64_t choices, int normalize, const void *logits,
+                      int64_t ld, const float *weights, const int *experts, const float *grad, void *dlogits,
+                      int64_t ldd, void *stream)
+{
+    if (!dtype_ok(dtype) || !size_ok(tokens, 0) || groups < 1 || groups > kRouteMaxExperts || choices < 1 ||
+        choices > groups || choices > kRouteMaxChoices || tokens * choices > kMaxInt || ld < groups || ldd < groups ||
+        (normalize != 0 && normalize != 1))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (tokens > 0 && (!here(logits, elem(dtype)) || !here(weights, 4) || !here(experts, 4) || !here(grad, 4) ||
+                       !here(dlogits, elem(dtype))))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    const int st = current_device(nullptr, nullptr);
+    if (st != GEMM_F32_SUCCESS) return st;
+    if (tokens == 0) return GEMM_F32_SUCCESS;
+    RouteArgs a{};
+    a.logits = logits;
+    a.ld = ld;
+    a.weights = const_cast<float *>(weights);
+    a.experts = const_cast<int *>(experts);
+    a.tokens = (int)tokens;
+    a.groups = (int)groups;
+    a.choices = (int)choices;
+    a.normalize = normalize;
+    a.grad = grad;
+    a.dlogits = dlogits;
+    a.ldd = ldd;
+    launch_route(a, dtype == EXPERT_BF16, true, stream_of(stream));
+    return launched();
+}
+
+}  // extern "C"

@@ -1388,6 +1388,24 @@ bool pointers_ok(const float *A, const float *B, const float *C)
 
 }  // namespace
 
+namespace gemmf32 {
+
+// For the other host units.
+int current_device(int *cu_count, int *num_xcd)
+{
+    int device = 0;
+    DeviceFacts f;
+    const int st = device_facts(&device, &f);
+    if (st != GEMM_F32_SUCCESS) return st;
+    if (cu_count) *cu_count = f.cu_count;
+    if (num_xcd) *num_xcd = f.num_xcd;
+    return GEMM_F32_SUCCESS;
+}
+
+int record_hip_error(hipError_t e) { return hip_fail(e); }
+
+}  // namespace gemmf32
+
 extern "C" {
 
 int gemm_f32_run(gemm_f32_plan p, const float *A, const float *B, float *C, void *stream)

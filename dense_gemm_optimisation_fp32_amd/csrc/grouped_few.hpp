@@ -1,0 +1,259 @@
+// Products grouped by expert where an expert has few rows (decoding): bound
+// by the bytes of the experts' matrices, each read once.
+//
+// A workgroup takes 16 MT rows of one expert and a strip of columns, and its
+// wavefronts split k.  B goes straight from memory into registers, 16 bytes
+// a lane, one iteration's loads ahead of the products; the products run on
+// 16-row matrix instructions whose rows past the expert's are wasted, which
+// costs nothing that the memory does not cover.  The order of k inside an
+// instruction is free as long as A and B agree, which the layouts use:
+//   k contiguous  a lane holds 16 bytes of one column: four neighbouring k
+//                 (32 bits), eight (bfloat16) or a block of 32 (4-bit).  Four
+//                 lanes share a column, so an iteration's four loads cover
+//                 256 bytes of each column.
+//   k strided     32 bits: a lane's 16 bytes are four columns of one k, and
+//                 load s of lane group g takes k-row 4 g + s; bfloat16: eight
+//                 columns of k-row 8 g + j, turned by one byte permute a
+//                 register into pairs along k.
+// The wavefronts' sums meet in LDS and are added in the order of k's parts:
+// the result is the same in every run.  4-bit products quantise the rows of
+// X on the way: a lane's operand is one block of 32, so the largest
+// magnitude, the scale and the codes need no other lane.
+#pragma once
+
+#include "lp_gemm.hpp"
+#include "mx4.hpp"
+
+namespace gemmf32 {
+
+enum FewKind { kFewF32 = 0, kFewBf16 = 1, kFewFp4 = 2 };
+
+template <int KIND, bool B_KS, class X>
+struct FewTile {
+    using E = X;                                     // elements of A and C
+    static constexpr int WAVES = 4, THREADS = WAVES * 64;
+    // Columns of a workgroup, and of the k that one wavefront's iteration covers.
+    static constexpr int NB = B_KS ? (KIND == kFewF32 ? 4 : 8) : 2;       // 16-column blocks
+    static constexpr int BN = 16 * NB;
+    static constexpr int KI = KIND == kFewFp4 ? 512 : KIND == kFewF32 ? (B_KS ? 32 : 64) : (B_KS ? 32 : 128);
+    static constexpr int LOADS = B_KS ? 8 : 4 * NB;  // 16-byte loads of B a lane and iteration
+    static constexpr int A_LOADS = KIND == kFewF32 ? KI / 16 : KI / 32;   // of A (not 4-bit)
+};
+
+template <class T, int KIND, bool B_KS>
+struct FewRegs {
+    i32x4 b[T::LOADS];
+    int s[KIND == kFewFp4 ? T::LOADS : 1];
+};
+
+template <int KIND, bool B_KS, class X, int MT>
+__global__ __launch_bounds__(256) void few_grouped_kernel(GroupedArgs g)
+{
+    using T = FewTile<KIND, B_KS, X>;
+    using E = typename T::E;
+    constexpr int BM = 16 * MT, BN = T::BN, ROW = BN + 4;
+    __shared__ float red[T::WAVES][BM * ROW];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    RowTile rt;
+    int tn;
+    if (!find_tile<BM>(g, blockIdx.x, lane, rt, tn)) return;
+    const int col0 = tn * BN;
+    const int l16 = lane & 15, grp = lane >> 4;
+    const int rows = min(rt.rows, BM);
+
+    f32x4 acc[MT][T::NB];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb) acc[mt][nb] = f32x4{};
+
+    if (rt.expert >= 0) {
+        const char *const bx = g.B + rt.expert * g.expert_stride;
+        const E *pa[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+            pa[mt] = reinterpret_cast<const E *>(g.A + (rt.row + min(mt * 16 + l16, rows - 1)) * g.lda);
+        // 4-bit: codes of 128 columns are 64 bytes; counted in k-blocks.
+        const int blocks = g.a_kblocks;
+        const u8 *sb = nullptr;
+        const char *pb[B_KS ? 1 : T::NB];
+        if constexpr (B_KS) {
+            pb[0] = bx + (KIND == kFewF32 ? grp * 4 : grp * 8) * g.ldb +
+                    (long long)(col0 + l16 * (KIND == kFewF32 ? 4 : 8)) * sizeof(E);
+        } else {
+#pragma unroll
+            for (int nb = 0; nb < T::NB; ++nb)
+                pb[nb] = bx + min(col0 + nb * 16 + l16, g.n - 1) * g.ldb + grp * 16;
+            if constexpr (KIND == kFewFp4) sb = g.b_scales + (long long)rt.expert * blocks * g.n * 4 + grp;
+        }
+        const int cols_left = g.n - (col0 + l16 * (KIND == kFewF32 ? 4 : 8));   // (k strided)
+
+        auto load_b = [&](int it, FewRegs<T, KIND, B_KS> &r) {
+            const int k0 = it * T::KI;
+            if constexpr (B_KS) {
+                constexpr int PER = KIND == kFewF32 ? 4 : 8;
+#pragma unroll
+                for (int j = 0; j < T::LOADS; ++j) {
+                    // (32 bits: two runs of 16 k-rows)
+                    const int kr = KIND == kFewF32 ? (j / 4) * 16 + j % 4 : j;
+                    const int kk = k0 + kr + grp * PER;
+                    r.b[j] = load_chunk(reinterpret_cast<const E *>(pb[0] + (long long)(k0 + kr) * g.ldb),
+                                      kk < g.k ? cols_left : 0);
+                }
+            } else if constexpr (KIND == kFewFp4) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int kb = min(it * 4 + s, blocks - 1);
+#pragma unroll
+                    for (int nb = 0; nb < T::NB; ++nb) {
+                        struct __attribute__((packed, aligned(1))) Chunk {
+                            i32x4 v;
+                        };
+                        r.b[s * T::NB + nb] = reinterpret_cast<const Chunk *>(pb[nb] + (long long)kb * 64)->v;
+                        r.s[s * T::NB + nb] = sb[((long long)kb * g.n + min(col0 + nb * 16 + l16, g.n - 1)) * 4];
+                    }
+                }
+            } else {
+                constexpr int N = 16 / sizeof(E);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int kk = k0 + (s * 4 + grp) * N;
+#pragma unroll
+                    for (int nb = 0; nb < T::NB; ++nb)
+                        r.b[s * T::NB + nb] =
+                            load_chunk(reinterpret_cast<const E *>(pb[nb] + (long long)(k0 + s * 4 * N) * sizeof(E)), g.k - kk);
+                }
+            }
+        };
+        auto multiply = [&](int it, const FewRegs<T, KIND, B_KS> &r) {
+            const int k0 = it * T::KI;
+            if constexpr (KIND == kFewFp4) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int kb = it * 4 + s;
+                    if (kb >= blocks) break;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const int k = kb * 128 + grp * 32;
+                        float v[4][8];
+                        unsigned largest = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            load8(pa[mt] + k + 8 * i, g.k - k - 8 * i, v[i]);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) largest = max(largest, magnitude(v[i][c]));
+                        }
+                        const MxBlock m = mx_block(largest);
+                        i32x8 a = {};
+                        if (m.byte != 255)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) a[i] = (int)mx_codes(v[i], m.factor);
+#pragma unroll
+                        for (int nb = 0; nb < T::NB; ++nb) {
+                            const i32x4 w = r.b[s * T::NB + nb];
+                            const i32x8 b = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+                            acc[mt][nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                b, a, acc[mt][nb], 4, 4, 0, r.s[s * T::NB + nb], 0, (int)m.byte);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int s = 0; s < T::A_LOADS; ++s) {
+                        constexpr int N = 16 / sizeof(E);
+                        const int kk = k0 + (s * 4 + grp) * N;
+                        const i32x4 a = load_chunk(pa[mt] + kk, g.k - kk);
+                        if constexpr (KIND == kFewF32) {
+                            const f32x4 af = __builtin_bit_cast(f32x4, a);
+                            if constexpr (B_KS) {
+                                // k-rows 4 grp + j of the run; set c: columns 4 i + c.
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const f32x4 bf = __builtin_bit_cast(f32x4, r.b[s * 4 + j]);
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c)
+                                        acc[mt][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(bf[c], af[j], acc[mt][c], 0, 0, 0);
+                                }
+                            } else {
+#pragma unroll
+                                for (int nb = 0; nb < T::NB; ++nb) {
+                                    const f32x4 bf = __builtin_bit_cast(f32x4, r.b[s * T::NB + nb]);
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j)
+                                        acc[mt][nb] = __builtin_amdgcn_mfma_f32_16x16x4f32(bf[j], af[j], acc[mt][nb], 0, 0, 0);
+                                }
+                            }
+                        } else {
+                            const bf16x8 af = __builtin_bit_cast(bf16x8, a);
+#pragma unroll
+                            for (int nb = 0; nb < T::NB; ++nb) {
+                                i32x4 b;
+                                if constexpr (B_KS) {
+                                    // Column nb of the lane's eight, its k-rows in pairs.
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        b[i] = (int)__builtin_amdgcn_perm((unsigned)r.b[2 * i + 1][nb / 2],
+                                                                          (unsigned)r.b[2 * i][nb / 2],
+                                                                          nb & 1 ? 0x07060302u : 0x05040100u);
+                                } else {
+                                    b = r.b[s * T::NB + nb];
+                                }
+                                acc[mt][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), af,
+                                                                                      acc[mt][nb], 0, 0, 0);
+                            }
+                        }
+                    }
+            }
+        };
+
+        const int its = KIND == kFewFp4 ? (blocks + 3) / 4 : (g.k + T::KI - 1) / T::KI;
+        if (wave < its) {
+            FewRegs<T, KIND, B_KS> r[2];
+            load_b(wave, r[0]);
+            int it = wave;
+            while (true) {
+                if (it + T::WAVES < its) load_b(it + T::WAVES, r[1]);
+                multiply(it, r[0]);
+                it += T::WAVES;
+                if (it >= its) break;
+                if (it + T::WAVES < its) load_b(it + T::WAVES, r[0]);
+                multiply(it, r[1]);
+                it += T::WAVES;
+                if (it >= its) break;
+            }
+        }
+    }
+
+    // Lane (l16, grp) holds row l16 and columns 4 grp + v of each block:
+    // column 16 nb + i (k contiguous) or NB i + nb (k strided) of the strip.
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int i = 4 * grp + v;
+                red[wave][(mt * 16 + l16) * ROW + (B_KS ? T::NB * i + nb : nb * 16 + i)] = acc[mt][nb][v];
+            }
+    __syncthreads();
+    const float *const bias = g.bias && rt.expert >= 0 ? g.bias + rt.expert * g.bias_stride + col0 : nullptr;
+    for (int e = tid; e < rows * BN; e += T::THREADS) {
+        const int row = e / BN, col = e % BN;
+        if (col0 + col >= g.n) continue;
+        float x = 0.0f;
+#pragma unroll
+        for (int w = 0; w < T::WAVES; ++w) x += red[w][row * ROW + col];
+        if (rt.expert < 0) {
+            x = 0.0f;
+        } else {
+            if (bias) x += bias[col];
+            x = activate(x, g.act);
+        }
+        *(reinterpret_cast<E *>(g.C + (rt.row + row) * g.ldc) + col0 + col) = (E)x;
+    }
+}
+
+}  // namespace gemmf32

@@ -1,0 +1,173 @@
+// Microscaled 4-bit floating point: quantisation and its inverse.
+//
+// Blocks of 32 values along k share a power of two, 2^e; each value is the
+// nearest of {0, .5, 1, 1.5, 2, 3, 4, 6} times the scale (ties to the even
+// code) with its sign.  e = floor(log2(largest magnitude)) - 2, at least -127,
+// so the largest magnitude lands in [4, 8) and saturates at 6.  A block that
+// holds an infinity or a NaN has no such e: its scale byte is 255, which
+// stands for NaN, so that it shows in every result that uses the block.
+//
+// Both kernels are bound by memory: one pass, 16 bytes a lane and load.
+// Measured on one MI355X, 14336 x 4096 bf16 along rows: see the host's
+// launch functions.
+#pragma once
+
+#include "expert_common.hpp"
+
+namespace gemmf32 {
+
+struct Mx4Args {
+    const char *x;          // values (quantise: in, dequantise: out)
+    u8 *codes;              // (rows, kp / 2): two codes a byte, the even column in the low half
+    u8 *scales;             // (kp / 128, rows, 4)
+    long long ld;           // elements from row to row (columns layout: from column to column)
+    int rows, k, kp;
+};
+
+struct MxBlock {
+    float factor;           // 2^-e: x * factor is in [0, 8)
+    unsigned byte;          // 127 + e, or 255
+};
+
+// From the largest magnitude's bits (as an unsigned number a NaN is larger
+// than an infinity, which is larger than any finite value).
+__device__ __forceinline__ MxBlock mx_block(unsigned largest)
+{
+    const int field = (int)(largest >> 23);
+    const int biased = max(field - 2, 0);                 // 127 + e
+    MxBlock b;
+    b.byte = field == 255 ? 255u : (unsigned)biased;
+    // 2^(127 - biased): its exponent field is 254 - biased, from 254 down to 2.
+    b.factor = field == 255 ? 0.0f : __uint_as_float((unsigned)(254 - biased) << 23);
+    return b;
+}
+
+// Eight values -> eight codes.  The conversion rounds to nearest, ties to
+// the even code, and saturates at 6 (checked value by value in the tests).
+__device__ __forceinline__ unsigned mx_codes(const float (&v)[8], float factor)
+{
+    unsigned w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0] * factor, v[1] * factor, 1.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2] * factor, v[3] * factor, 1.0f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4] * factor, v[5] * factor, 1.0f, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6] * factor, v[7] * factor, 1.0f, 3);
+    return w;
+}
+
+__device__ __forceinline__ unsigned magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__bf16 x) { return (float)x; }
+
+// Eight values from p on, those at or past `left` zero.  Unaligned wide
+// loads are in order here: rows of odd length start anywhere.
+template <class E>
+__device__ __forceinline__ void load8(const E *p, int left, float (&v)[8])
+{
+    struct __attribute__((packed, aligned(sizeof(E)))) Eight {
+        E e[8];
+    };
+    if (left >= 8) {
+        const Eight t = *reinterpret_cast<const Eight *>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f32(t.e[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f32(p[i]) : 0.0f;
+    }
+}
+
+// Rows contiguous along k: four lanes hold a block, eight values each, and
+// sixteen lanes the four blocks of a scale word.
+template <class E>
+__global__ __launch_bounds__(256) void mx4_quantize_rows_kernel(Mx4Args a)
+{
+    const int lane = threadIdx.x & 63;
+    const int segments = (a.kp + 511) / 512;              // 512 columns a wavefront
+    const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const long long row = unit / segments;
+    if (row >= a.rows) return;
+    const int col = (int)(unit % segments) * 512 + lane * 8;
+    float v[8] = {};
+    if (col < a.k) load8(reinterpret_cast<const E *>(a.x) + row * a.ld + col, a.k - col, v);
+    unsigned largest = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) largest = max(largest, magnitude(v[i]));
+    largest = max(largest, (unsigned)__shfl_xor((int)largest, 1));
+    largest = max(largest, (unsigned)__shfl_xor((int)largest, 2));
+    const MxBlock b = mx_block(largest);
+    const unsigned codes = b.byte == 255 ? 0u : mx_codes(v, b.factor);
+    unsigned word = b.byte << (8 * ((lane >> 2) & 3));
+    word |= (unsigned)__shfl_xor((int)word, 4);
+    word |= (unsigned)__shfl_xor((int)word, 8);
+    if (col < a.kp) {
+        *reinterpret_cast<unsigned *>(a.codes + row * (a.kp / 2) + col / 2) = codes;
+        if ((lane & 15) == 0)
+            *reinterpret_cast<unsigned *>(a.scales + ((long long)(col / 128) * a.rows + row) * 4) = word;
+    }
+}
+
+// Rows contiguous along the other axis (x(r, c) = x[c * ld + r]): a lane
+// takes one row's block, neighbouring lanes neighbouring rows; the four
+// wavefronts take the four blocks of a scale word.
+template <class E>
+__global__ __launch_bounds__(256) void mx4_quantize_columns_kernel(Mx4Args a)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int strips = (a.rows + 63) / 64;
+    const int kb = blockIdx.x / strips;
+    const int row = blockIdx.x % strips * 64 + lane;
+    if (row >= a.rows) return;
+    const int col = kb * 128 + wave * 32;
+    float v[4][8];
+    const E *p = reinterpret_cast<const E *>(a.x) + (long long)col * a.ld + row;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i / 8][i % 8] = col + i < a.k ? to_f32(p[(long long)i * a.ld]) : 0.0f;
+    unsigned largest = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) largest = max(largest, magnitude(v[i / 8][i % 8]));
+    const MxBlock b = mx_block(largest);
+    u32x4 codes = {};
+    if (b.byte != 255)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) codes[i] = mx_codes(v[i], b.factor);
+    *reinterpret_cast<u32x4 *>(a.codes + (long long)row * (a.kp / 2) + col / 2) = codes;
+    a.scales[((long long)kb * a.rows + row) * 4 + wave] = (u8)b.byte;
+}
+
+// Codes and scales back to values: eight columns a lane.  The scale byte 0
+// is 2^-127, below the normal numbers: set by its mantissa bit.
+template <class E>
+__global__ __launch_bounds__(256) void mx4_dequantize_kernel(Mx4Args a)
+{
+    const int lane = threadIdx.x & 63;
+    const int segments = (a.k + 511) / 512;
+    const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const long long row = unit / segments;
+    if (row >= a.rows) return;
+    const int col = (int)(unit % segments) * 512 + lane * 8;
+    if (col >= a.k) return;
+    const unsigned codes = *reinterpret_cast<const unsigned *>(a.codes + row * (a.kp / 2) + col / 2);
+    const unsigned byte = a.scales[((long long)(col / 128) * a.rows + row) * 4 + ((col >> 5) & 3)];
+    const float scale = byte == 255 ? __builtin_nanf("") : __uint_as_float(byte ? byte << 23 : 0x00400000u);
+    struct __attribute__((packed, aligned(sizeof(E)))) Eight {
+        E e[8];
+    } t;
+    const f32x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0);
+    const f32x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1);
+    const f32x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2);
+    const f32x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
+    // A code times a power of two is exact in 32 and in 16 bits.
+    t.e[0] = (E)(v0.x * scale), t.e[1] = (E)(v0.y * scale), t.e[2] = (E)(v1.x * scale), t.e[3] = (E)(v1.y * scale);
+    t.e[4] = (E)(v2.x * scale), t.e[5] = (E)(v2.y * scale), t.e[6] = (E)(v3.x * scale), t.e[7] = (E)(v3.y * scale);
+    E *p = reinterpret_cast<E *>(const_cast<char *>(a.x)) + row * a.ld + col;
+    if (col + 8 <= a.k) {
+        *reinterpret_cast<Eight *>(p) = t;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i < a.k) p[i] = t.e[i];
+    }
+}
+
+}  // namespace gemmf32

@@ -1,0 +1,558 @@
+"""The expert-layer operators against plain 64-bit forms, on the GPU.
+
+Tolerances, per element.  A product's sum over k of 32-bit terms with S = sum
+|a b|: the library's bar for 32-bit products, 1e-5 S + 1e-6 (products of two
+bfloat16 or 4-bit values are exact in 32 bits, so their sums meet the same
+bar); with an activation 1.2e-5 S' + 1.2e-6, S' with |bias|.  A bfloat16
+result adds its one rounding, 2^-8 |y| (the bar's own error, rounded with it, by
+a factor 1 + 2^-8).  Routing weights are a few 32-bit operations: exp of a difference d
+rounded at 2^-24 |d| with |d| <= 30 here, and at most 1024 terms in a sum:
+1e-5 relative."""
+import pytest
+import torch
+
+import dense_gemm_optimisation_fp32_amd as g
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+DEV = "cuda"
+
+
+def normal(shape, dtype, seed, scale=1.0):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
+    return (torch.randn(shape, generator=gen, device=DEV) * scale).to(dtype)
+
+
+def offsets_of(sizes, first=0):
+    ends = [first]
+    for s in sizes:
+        ends.append(ends[-1] + s)
+    return torch.tensor(ends, dtype=torch.int32, device=DEV)
+
+
+def padded_rows(x, extra, fill=float("nan")):
+    """x with rows `extra` elements longer, those set to `fill`, as a view."""
+    full = torch.full((x.shape[0], x.shape[1] + extra), fill, dtype=x.dtype, device=x.device)
+    full[:, : x.shape[1]] = x
+    return full[:, : x.shape[1]]
+
+
+def close(y, ref, s, act=False):
+    ref, s = ref.double(), s.double()
+    bar = 1.2e-5 * s + 1.2e-6 if act else 1e-5 * s + 1e-6
+    if y.dtype == BF16:
+        bar = bar * (1 + 2 ** -8) + ref.abs() * 2 ** -8
+    err = (y.double() - ref).abs()
+    assert y.shape == ref.shape
+    assert not torch.isnan(y).any(), "NaN in the result"
+    worst = (err / bar).max().item() if err.numel() else 0.0
+    assert worst <= 1, f"max error ratio {worst:.3g}"
+
+
+# Rows of each expert; experts without rows, one row, tiles that end inside,
+# more experts than lanes, and averages on both sides of every dispatch rule.
+SIZES = {
+    "one": [1],
+    "few": [2, 0, 1, 5],
+    "decode": [3] * 8,
+    "long_few": [0, 70, 1, 0, 0, 0, 0, 9],
+    "ragged": [33, 0, 129, 64, 1],
+    "many": [i % 5 for i in range(150)],
+    "many_large": [(7 * i) % 50 for i in range(130)],
+    "large": [300, 511, 0, 257],
+}
+
+
+def grouped_case(dtype, layout, sizes, n, k, seed, tail=0, pad_a=0, pad_b=0):
+    m, e = sum(sizes) + tail, len(sizes)
+    a = normal((m, k), dtype, seed)
+    if pad_a:
+        a = padded_rows(a, pad_a)
+    b = normal((e, k, n) if layout == "row" else (e, n, k), dtype, seed + 1, k ** -0.5)
+    if pad_b:
+        wide = torch.full((*b.shape[:2], b.shape[2] + pad_b), float("nan"), dtype=dtype, device=DEV)
+        wide[..., : b.shape[2]] = b
+        b = wide[..., : b.shape[2]]
+    if layout == "col":
+        b = b.transpose(1, 2)
+    return a, b, offsets_of(sizes)
+
+
+def grouped_reference(a, b, sizes, bias=None, act=None):
+    m, n = a.shape[0], b.shape[2]
+    ref = torch.zeros((m, n), dtype=torch.float64, device=DEV)
+    s = torch.zeros_like(ref)
+    at = 0
+    for e, r in enumerate(sizes):
+        x, w = a[at:at + r].double(), b[e].double().contiguous()
+        ref[at:at + r], s[at:at + r] = x @ w, x.abs() @ w.abs()
+        if bias is not None:
+            ref[at:at + r] += bias[e].double()
+            s[at:at + r] += bias[e].double().abs()
+        at += r
+    if act == "relu":
+        ref = ref.clamp(min=0)
+    elif act == "gelu":
+        ref = ref * torch.special.ndtr(ref)
+    return ref, s
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("n,k", [(1, 1), (64, 128), (130, 70), (257, 67), (300, 1000), (513, 192)])
+@pytest.mark.parametrize("sizes", list(SIZES))
+def test_grouped_linear(dtype, layout, n, k, sizes):
+    a, b, off = grouped_case(dtype, layout, SIZES[sizes], n, k, 1)
+    ref, s = grouped_reference(a, b, SIZES[sizes])
+    close(g.grouped_linear(a, b, off), ref, s)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("sizes", ["few", "ragged", "large"])
+@pytest.mark.parametrize("act", [None, "relu", "gelu"])
+@pytest.mark.parametrize("n", [136, 67])
+def test_grouped_linear_epilogue_strides_and_unowned_rows(dtype, layout, sizes, act, n):
+    """Bias and activation; rows and matrices with NaN between them; rows of no
+    expert become zero; `out` with a row stride keeps what is between."""
+    k, tail = 150, 37
+    a, b, off = grouped_case(dtype, layout, SIZES[sizes], n, k, 2, tail=tail, pad_a=10, pad_b=6)
+    a[sum(SIZES[sizes]):] = float("nan")
+    bias = normal((len(SIZES[sizes]), n), F32, 3)
+    ref, s = grouped_reference(torch.nan_to_num(a), b, SIZES[sizes], bias, act)
+    ref[sum(SIZES[sizes]):] = 0
+    full = torch.full((a.shape[0], n + 5), 7.0, dtype=dtype, device=DEV)
+    out = g.grouped_linear(a, b, off, bias=bias, activation=act, out=full[:, :n])
+    close(out, ref, s, act=True)
+    assert (full[:, n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_before_the_first_expert(dtype):
+    sizes = [40, 0, 90]
+    a, b, _ = grouped_case(dtype, "col", [25] + sizes, 96, 128, 4)
+    b = b[1:]
+    ref, s = grouped_reference(a[25:], b, sizes)
+    y = g.grouped_linear(a, b, offsets_of(sizes, 25))
+    assert (y[:25] == 0).all()
+    close(y[25:], ref, s)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n,k", [(1, 1), (128, 256), (130, 70), (257, 67), (512, 300)])
+@pytest.mark.parametrize("sizes", list(SIZES))
+def test_grouped_weight_grad(dtype, n, k, sizes):
+    rows, tail = SIZES[sizes], 5
+    m = sum(rows) + tail
+    a, grad = normal((m, k), dtype, 5), normal((m, n), dtype, 6)
+    a[m - tail:], grad[m - tail:] = float("nan"), float("nan")
+    out = g.grouped_weight_grad(a, grad, offsets_of(rows))
+    assert tuple(out.shape) == (len(rows), k, n)
+    at = 0
+    for e, r in enumerate(rows):
+        x, y = a[at:at + r].double().t().contiguous(), grad[at:at + r].double()
+        close(out[e], x @ y, x.abs() @ y.abs())
+        at += r
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradients_against_differences(dtype):
+    """The two gradients of sum(C * G) against central differences of the
+    64-bit product: linear in each operand, so the difference is exact but for
+    the 64-bit rounding, and the bars are those of the products."""
+    sizes, n, k = [20, 0, 45], 40, 56
+    a, b, off = grouped_case(dtype, "row", sizes, n, k, 7)
+    grad = normal((sum(sizes), n), dtype, 8)
+    da = g.grouped_linear(grad, b.transpose(1, 2), off)
+    db = g.grouped_weight_grad(a, grad, off)
+
+    def loss(x, w):
+        total, at = 0.0, 0
+        for e, r in enumerate(sizes):
+            total = total + (x[at:at + r] @ w[e] * grad[at:at + r].double()).sum()
+            at += r
+        return total
+
+    x, w = a.double(), b.double()
+    for i, j in [(0, 0), (19, 55), (20, 3), (64, 30)]:
+        d = torch.zeros_like(x)
+        d[i, j] = 0.5
+        slope = loss(x + d, w) - loss(x - d, w)
+        bar = 1e-5 * (grad[i].double().abs() * w[0 if i < 20 else 2][j].abs()).sum() + 1e-6 + 2 ** -8 * slope.abs()
+        assert (da[i, j].double() - slope).abs() <= bar
+    for e, i, j in [(0, 0, 0), (2, 55, 39), (1, 4, 4), (2, 11, 7)]:
+        d = torch.zeros_like(w)
+        d[e, i, j] = 0.5
+        slope = loss(x, w + d) - loss(x, w - d)
+        rows = slice(0, 20) if e == 0 else slice(20, 20) if e == 1 else slice(20, 65)
+        bar = 1e-5 * (x[rows, i].abs() * grad[rows, j].double().abs()).sum() + 1e-6 + 2 ** -8 * slope.abs()
+        assert (db[e, i, j].double() - slope).abs() <= bar
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("act", [None, "relu", "gelu"])
+@pytest.mark.parametrize("rows", [5, 200, 300])
+def test_grouped_nan_and_infinity_stay_in_their_row(dtype, act, rows):
+    a, b, off = grouped_case(dtype, "col", [rows, rows], 96, 128, 14)
+    a[1, 3] = float("nan")
+    a[rows, 100] = float("inf")
+    y = g.grouped_linear(a, b, off, activation=act)
+    assert y[1].isnan().all()
+    keep = [i for i in range(2 * rows) if i not in (1, rows)]
+    assert y[keep].isfinite().all() and not y[rows].isfinite().all()
+
+
+def test_grouped_no_rows():
+    off = offsets_of([0, 0, 0])
+    for dtype in (F32, BF16):
+        a, b = torch.empty((0, 64), dtype=dtype, device=DEV), normal((3, 64, 32), dtype, 9)
+        assert g.grouped_linear(a, b, off).shape == (0, 32)
+        assert (g.grouped_weight_grad(a, torch.empty((0, 32), dtype=dtype, device=DEV), off) == 0).all()
+
+
+def test_nonsense_offsets_stay_inside():
+    """Offsets that are not sorted or point outside give some result, and touch
+    nothing outside the operands."""
+    a, b = normal((100, 64), BF16, 10), normal((4, 64, 64), BF16, 11)
+    for bad in ([0, 500, -3, 1000, 100], [90, 10, 80, 20, 70], [-5, -5, -5, -5, -5]):
+        off = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        for dtype in (F32, BF16):
+            assert g.grouped_linear(a.to(dtype), b.to(dtype), off).shape == (100, 64)
+            assert g.grouped_weight_grad(a.to(dtype), a.to(dtype), off).shape == (4, 64, 64)
+
+
+# --- 4-bit ---------------------------------------------------------------------
+
+GRID = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64)
+
+
+def quantised(x):
+    """The values of x's 4-bit form in 64 bits: nearest of the grid by search, ties to the even code."""
+    r, k = x.shape
+    grid = GRID.to(x.device)
+    out = torch.zeros((r, k), dtype=torch.float64, device=x.device)
+    for c in range(0, k, 32):
+        v = x[:, c:c + 32].double()
+        top = v.abs().amax(1, keepdim=True)
+        e = (torch.frexp(top)[1] - 3).clamp(min=-127).double()
+        scale = torch.where(top > 0, torch.exp2(e), torch.full_like(e, 2.0 ** -127))
+        d = ((v.abs() / scale).unsqueeze(-1) - grid).abs()
+        # of two as near, the even code: it gets the smaller of two tiny handicaps that never beat a distance
+        best = d.amin(-1, keepdim=True)
+        near = d == best
+        even = near & (torch.arange(8, device=x.device) % 2 == 0)
+        pick = torch.where(even.any(-1, keepdim=True), even, near).double().argmax(-1)
+        out[:, c:c + 32] = torch.sign(v) * grid[pick] * scale
+    return out
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,k", [(1, 1), (3, 31), (5, 32), (7, 33), (64, 128), (65, 129), (130, 700), (257, 1025)])
+@pytest.mark.parametrize("along", ["rows", "columns", "padded"])
+def test_quantize_and_back(dtype, rows, k, along):
+    x = normal((rows, k), F32, 12) * torch.exp(normal((rows, 1), F32, 13) * 3)
+    x = x.to(dtype)
+    if along == "columns":
+        x = x.t().contiguous().t()
+    elif along == "padded":
+        x = padded_rows(x, 3)
+    q = g.mx4_quantize(x)
+    assert tuple(q.shape) == (rows, k)
+    for out in (F32, BF16):
+        assert torch.equal(g.mx4_dequantize(q, out).double(), quantised(x))
+    kp = -(-k // 128) * 128
+    codes = torch.stack((q.codes & 15, q.codes >> 4), -1).reshape(rows, kp)
+    assert (codes[:, k:] == 0).all()
+
+
+def test_every_code_border():
+    """Values at, just under and just over each border between two codes, both signs, in one scale."""
+    borders = torch.tensor([0.0, 0.25, 0.5, 0.75, 1.0, 1.25, 1.5, 1.75, 2.0, 2.5, 3.0, 3.5, 4.0, 5.0, 6.0, 7.0])
+    v = torch.cat([borders, torch.nextafter(borders, borders + 1), torch.nextafter(borders, borders - 1)])
+    v = torch.cat([v, -v]).cuda()
+    for power in (-126, -60, 0, 60, 124):
+        x = torch.zeros((v.numel(), 32), device=DEV)
+        x[:, 0] = 4.0
+        x[:, 5] = v
+        x = x * 2.0 ** power
+        assert torch.equal(g.mx4_dequantize(g.mx4_quantize(x)).double(), quantised(x))
+
+
+def test_extreme_magnitudes():
+    """Zero blocks, subnormal blocks (scale 2^-127), the largest finite value; a
+    block with an infinity or a NaN becomes NaN and leaves its neighbours."""
+    x = torch.zeros((6, 128), device=DEV)
+    x[0, 0] = 2.0 ** -149
+    x[1, :32] = torch.arange(32, device=DEV) * 2.0 ** -130
+    x[2, 40] = torch.finfo(F32).max
+    x[3, 64:96] = -torch.finfo(F32).tiny
+    x[4, 70] = float("inf")
+    x[5, 3] = float("nan")
+    for y in (x, x.t().contiguous().t()):
+        q = g.mx4_quantize(y)
+        back = g.mx4_dequantize(q)
+        assert torch.equal(back[:4].double(), quantised(x[:4]))
+        assert back[4, 64:96].isnan().all() and back[5, :32].isnan().all()
+        back[4, 64:96] = 0
+        back[5, :32] = 0
+        assert (back[4:] == 0).all()
+        assert q.scales[0, 4, 2] == 255 and q.scales[0, 5, 0] == 255 and q.scales[0, 0, 0] == 0
+
+
+def packed(e, n, k, seed):
+    q = [g.mx4_quantize(normal((n, k), F32, seed + i, k ** -0.5)) for i in range(e)]
+    w = g.Mx4Tensor(torch.stack([t.codes for t in q]), torch.stack([t.scales for t in q]), k)
+    return w, [g.mx4_dequantize(t).double() for t in q]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("m", [1, 4, 16, 17, 100, 300])
+@pytest.mark.parametrize("n,k", [(1, 1), (64, 128), (130, 70), (257, 300), (512, 640)])
+def test_mx4_linear(dtype, m, n, k):
+    w, values = packed(1, n, k, 20)
+    w = g.Mx4Tensor(w.codes[0], w.scales[0], k)
+    x = padded_rows(normal((m, k), dtype, 21), 3)
+    xq = quantised(x)
+    close(g.mx4_linear(x, w), xq @ values[0].t(), xq.abs() @ values[0].t().abs())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n,k", [(96, 128), (257, 300)])
+@pytest.mark.parametrize("sizes", list(SIZES))
+def test_mx4_linear_grouped(dtype, n, k, sizes):
+    rows = SIZES[sizes]
+    w, values = packed(len(rows), n, k, 30)
+    m = sum(rows) + 3
+    x, bias = normal((m, k), dtype, 31), normal((len(rows), n), F32, 32)
+    x[m - 3:] = float("nan")
+    y = g.mx4_linear(x, w, offsets=offsets_of(rows), bias=bias, activation="relu")
+    at = 0
+    for e, r in enumerate(rows):
+        xq = quantised(x[at:at + r])
+        ref = xq @ values[e].t() + bias[e].double()
+        close(y[at:at + r], ref.clamp(min=0), xq.abs() @ values[e].t().abs() + bias[e].double().abs(), act=True)
+        at += r
+    assert (y[m - 3:] == 0).all()
+
+
+@pytest.mark.parametrize("m", [3, 200])
+def test_mx4_linear_shows_infinities_and_nan(m):
+    w, values = packed(1, 64, 256, 40)
+    w = g.Mx4Tensor(w.codes[0], w.scales[0], 256)
+    x = normal((m, 256), F32, 41)
+    x[1, 100], x[2, 7] = float("inf"), float("nan")
+    y = g.mx4_linear(x, w)
+    assert y[1:3].isnan().all()
+    keep = [i for i in range(m) if i not in (1, 2)]
+    assert not y[keep].isnan().any()
+
+
+# --- routing ---------------------------------------------------------------------
+
+def route_reference(logits, choices, normalize):
+    x = logits.double()
+    x = torch.where(x.isnan(), torch.full_like(x, -torch.inf), x)
+    t, e = x.shape
+    ordered, which = torch.sort(x, dim=1, descending=True, stable=True)
+    top, which = ordered[:, :choices], which[:, :choices]
+    used = top > -torch.inf
+    first = torch.where(used[:, :1], top[:, :1], torch.zeros_like(top[:, :1]))
+    p = torch.exp((top if normalize else x) - first).sum(1, keepdim=True)
+    weights = torch.where(used, torch.exp(top - first) / torch.where(p > 0, p, torch.ones_like(p)), 0.0)
+    experts = torch.where(used, which, torch.full_like(which, -1))
+    flat = torch.where(used, which, torch.full_like(which, e)).reshape(-1)
+    order = torch.sort(flat, stable=True)[1]
+    counts = torch.bincount(flat, minlength=e + 1)[:e]
+    offsets = torch.cat((counts.new_zeros(1), counts.cumsum(0)))
+    order[offsets[-1]:] = -1
+    return weights, experts, offsets, order
+
+
+ROUTES = [(1, 1, 1), (1, 2, 1), (3, 5, 5), (16, 64, 4), (128, 8, 2), (129, 8, 2), (200, 17, 3), (300, 33, 8),
+          (700, 100, 6), (515, 129, 8), (1000, 256, 8), (260, 300, 16), (150, 600, 17), (140, 1024, 32)]
+
+
+def logits_of(t, e, dtype, masked, seed):
+    x = normal((t, e), dtype, seed, 2.0)
+    if masked:
+        off = normal((t, e), F32, seed + 1) < 0.3
+        off[::7] = True                                  # tokens that no expert may take
+        x = x.masked_fill(off, float("-inf"))
+    return x
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("t,e,c", ROUTES)
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("masked", [False, True])
+def test_route(dtype, t, e, c, normalize, masked):
+    x = logits_of(t, e, dtype, masked, 50)
+    r = g.route(x, c, normalize=normalize)
+    weights, experts, offsets, order = route_reference(x, c, normalize)
+    assert torch.equal(r.experts.long(), experts)
+    assert torch.equal(r.offsets.long(), offsets)
+    assert torch.equal(r.order.long(), order)
+    assert ((r.weights.double() - weights).abs() <= 1e-5 * weights).all()
+
+
+@pytest.mark.parametrize("t", [40, 400])
+def test_route_ties_nan_and_stride(t):
+    """Equal logits go to the lower expert, NaN to none; rows with NaN between them."""
+    x = (normal((t, 40), F32, 60) * 2).round() / 2
+    x[3] = 0.0
+    x[5, 7] = float("nan")
+    x[6] = float("nan")
+    x[8] = -0.0
+    x[8, ::2] = 0.0                                      # zeros of both signs are equal
+    view = padded_rows(x, 9)
+    r = g.route(view, 6)
+    weights, experts, offsets, order = route_reference(x, 6, True)
+    assert torch.equal(r.experts.long(), experts)
+    assert torch.equal(r.offsets.long(), offsets) and torch.equal(r.order.long(), order)
+    assert ((r.weights.double() - weights).abs() <= 1e-5 * weights).all()
+
+
+def test_route_no_tokens():
+    r = g.route(torch.empty((0, 8), device=DEV), 2)
+    assert r.weights.shape == (0, 2) and r.order.numel() == 0 and (r.offsets == 0).all()
+    assert g.route_grad(torch.empty((0, 8), device=DEV), r, torch.empty((0, 2), device=DEV)).shape == (0, 8)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("t,e,c", ROUTES)
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("masked", [False, True])
+def test_route_grad(dtype, t, e, c, normalize, masked):
+    """Against w (g - sum w g), by 64-bit differentiation of the plain softmax.
+    Bar: the weights' 1e-5, on the terms of the difference, and the rounding of
+    the result."""
+    x = logits_of(t, e, dtype, masked, 70)
+    r = g.route(x, c, normalize=normalize)
+    grad = normal((t, c), F32, 71)
+    d = g.route_grad(x, r, grad)
+    assert d.dtype == dtype
+    _, experts, _, _ = route_reference(x, c, normalize)
+    used = experts >= 0
+    leaf = x.double().requires_grad_()
+    index = experts.clamp(min=0)
+    chosen = torch.zeros_like(x, dtype=torch.bool).scatter(1, index, used) if c else None
+    chosen |= torch.zeros_like(chosen).scatter(1, index.where(used, index[:, :1]), True) & used.any(1, keepdim=True)
+    over = torch.where(chosen if normalize else x > -torch.inf, leaf, torch.full_like(leaf, -torch.inf))
+    live = used.any(1)
+    p = torch.softmax(over[live], 1)
+    (p.gather(1, index[live]) * used[live] * grad[live].double()).sum().backward()
+    ref = torch.nan_to_num(leaf.grad, nan=0.0)
+    gu = torch.where(used, grad.double().abs(), 0.0)
+    share = torch.zeros_like(ref)
+    share[live] = p.detach()
+    spread = torch.zeros_like(ref).scatter_add_(1, index, gu)
+    dot = (share.gather(1, index) * gu).sum(1, keepdim=True)
+    bar = 4e-5 * share * (spread + dot) + 1e-30
+    if dtype == BF16:
+        bar = bar * (1 + 2 ** -8) + 2 ** -8 * ref.abs()
+    assert ((d.double() - ref).abs() <= bar).all()
+
+
+def test_route_grad_against_differences():
+    x = logits_of(6, 9, F32, False, 80).double()
+    grad = normal((6, 3), F32, 81)
+    for normalize in (True, False):
+        r = g.route(x.float(), 3, normalize=normalize)
+        d = g.route_grad(x.float(), r, grad)
+        index = r.experts.long()
+
+        def loss(z):
+            over = z.gather(1, index) if normalize else z
+            p = torch.exp(z.gather(1, index)) / torch.exp(over).sum(1, keepdim=True)
+            return (p * grad.double()).sum()
+
+        h = 1e-4                                        # central: error h^2 / 6 times a third derivative below 10
+        for i, j in [(0, 0), (1, 8), (5, 4), (2, int(index[2, 0]))]:
+            step = torch.zeros_like(x)
+            step[i, j] = h
+            slope = (loss(x + step) - loss(x - step)) / (2 * h)
+            assert (d[i, j].double() - slope).abs() <= 1e-5
+
+
+# --- streams and graphs ------------------------------------------------------------
+
+def all_operators(x, w, wq, w4, grad):
+    r = g.route(x[:, :16].contiguous(), 2)
+    rows = x[r.order.clamp(min=0) // 2]
+    y = g.grouped_linear(rows, w, r.offsets, activation="gelu")
+    dx = g.grouped_linear(grad, w.transpose(1, 2), r.offsets)
+    dw = g.grouped_weight_grad(rows, grad, r.offsets)
+    y4 = g.mx4_linear(rows, w4, offsets=r.offsets)
+    back = g.mx4_dequantize(g.mx4_quantize(x))
+    dl = g.route_grad(x[:, :16].contiguous(), r, r.weights)
+    one = g.mx4_linear(x[:3].contiguous(), wq)
+    return [r.weights, r.experts, r.offsets, r.order, y, dx, dw, y4, back, dl, one]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_streams_and_graph(dtype):
+    """The same bits on another stream and from a graph replayed on new inputs,
+    with eager work in between."""
+    t, d, n = 300, 192, 160
+    w = normal((16, d, n), dtype, 91, d ** -0.5)
+    w4, _ = packed(16, n, d, 92)
+    wq = g.Mx4Tensor(w4.codes[0], w4.scales[0], d)
+    grad = normal((2 * t, n), dtype, 93)
+    x = normal((t, d), dtype, 94)
+    want = all_operators(x, w, wq, w4, grad)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = all_operators(x, w, wq, w4, grad)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+
+    static = x.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = all_operators(static, w, wq, w4, grad)
+    for seed in range(95, 99):
+        fresh = normal((t, d), dtype, seed)
+        static.copy_(fresh)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = all_operators(fresh, w, wq, w4, grad)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(want, captured)), f"replay on seed {seed}"
+
+
+def test_binding_refusals_on_the_gpu():
+    a, b, off = grouped_case(BF16, "row", [4, 4], 32, 64, 1)
+    with pytest.raises(ValueError):
+        g.grouped_linear(a, b[:, :32], off)
+    with pytest.raises(TypeError):
+        g.grouped_linear(a.float(), b, off)
+    with pytest.raises(ValueError):
+        g.grouped_linear(a, b, off.long())
+    with pytest.raises(ValueError):
+        g.grouped_linear(a, b, off[:2])
+    with pytest.raises(ValueError):
+        g.grouped_linear(a, b, off.cpu())
+    with pytest.raises(ValueError):
+        g.grouped_linear(a, b[:, ::2, ::2], off)
+    with pytest.raises(ValueError):
+        g.grouped_linear(a, b, off, bias=torch.zeros((2, 32), dtype=BF16, device=DEV))
+    with pytest.raises(KeyError):
+        g.grouped_linear(a, b, off, activation="tanh")
+    with pytest.raises(ValueError):
+        g.grouped_weight_grad(a, a[:4], off)
+    with pytest.raises(ValueError):
+        g.route(a, 65)
+    with pytest.raises(g.GemmF32Error):
+        g.route(a, 33)
+    with pytest.raises(ValueError):
+        g.mx4_quantize(a.expand(2, 8, 64))
+    q = g.mx4_quantize(a)
+    with pytest.raises(ValueError):
+        g.mx4_linear(a[:, :32].contiguous(), q)
+    with pytest.raises(ValueError):
+        g.mx4_linear(a, q, offsets=off)
+    with pytest.raises(TypeError):
+        g.mx4_dequantize(q, torch.float16)
