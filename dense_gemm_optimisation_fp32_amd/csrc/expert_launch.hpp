@@ -23,6 +23,7 @@ struct LpCall {
     bool b_contiguous;      // B's columns contiguous along k
     bool weight_grad;
     bool wide;              // 16-byte stores of C
+    int cu_count;
 };
 
 // Status of the current device (a gemm_f32_status) and its facts; a failed
@@ -34,7 +35,7 @@ void launch_mx4_quantize(const Mx4Args &a, bool bf16, bool columns, hipStream_t 
 void launch_mx4_dequantize(const Mx4Args &a, bool bf16, hipStream_t s);
 void launch_f32_grouped(GroupedArgs a, bool b_contiguous, hipStream_t s);
 void launch_f32_weight_grad(GroupedArgs a, hipStream_t s);
-void launch_lp256(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+void launch_lp256(GroupedArgs a, const LpCall &c, hipStream_t s);
 void launch_lp128(const GroupedArgs &a, const LpCall &c, hipStream_t s);
 void launch_lp128_unaligned(const GroupedArgs &a, const LpCall &c, hipStream_t s);
 // At most 16 or 32 rows a tile (row_tiles 1 or 2).

@@ -44,6 +44,19 @@ bool grid_ok(int64_t rows, int64_t cols, int64_t row_tile, int64_t col_tile, int
 // Rows an expert has on average.
 int64_t mean_rows(int64_t m, int64_t groups) { return (m + groups - 1) / groups; }
 
+// Most experts of the 256 x 256 tiles' kernels.
+constexpr int64_t kPipeGroups = 1022;
+
+// Whether the products of `rows` rows an expert take 256 x 256 tiles (one
+// workgroup a CU) rather than 128 x 128 (two): where a tile is mostly full and
+// there is a tile for every CU.  Measured, us, 16 experts, k = 2048, n = 4096,
+// 256 / 128: 128 rows 69 / 56, 256 rows 76 / 101, 1024 rows 259 / 334; 512
+// rows, k = n = 1024 (160 tiles) 32 / 24.
+bool large_tiles(int64_t rows, int64_t m, int64_t n, int64_t groups, int cus)
+{
+    return rows >= 192 && groups <= kPipeGroups && (m / 256 + groups / 2 + 1) * ((n + 255) / 256) >= cus;
+}
+
 // Up to this many rows an expert on average, the few-row kernels.
 constexpr int64_t kFewRows = 16;
 
@@ -69,7 +82,8 @@ int expert_grouped_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t gr
         return GEMM_F32_ERR_INVALID_VALUE;
     if (!grid_ok(m, n, 16, 32, groups + 2)) return GEMM_F32_ERR_INVALID_VALUE;
     GroupedArgs a{};
-    const int st = current_device(nullptr, &a.num_xcd);
+    int cus = 0;
+    const int st = current_device(&cus, &a.num_xcd);
     if (st != GEMM_F32_SUCCESS) return st;
     if (m == 0) return GEMM_F32_SUCCESS;
     a.A = static_cast<const char *>(A);
@@ -98,9 +112,9 @@ int expert_grouped_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t gr
     } else if (dtype == EXPERT_F32) {
         launch_f32_grouped(a, col, s);
     } else {
-        const LpCall c{false, true, col, false, wide_rows(C, a.ldc, n, size)};
+        const LpCall c{false, true, col, false, wide_rows(C, a.ldc, n, size), cus};
         if (!copies) launch_lp128_unaligned(a, c, s);
-        else if (rows >= 256) launch_lp256(a, c, s);
+        else if (large_tiles(rows, m, n, groups, cus)) launch_lp256(a, c, s);
         else launch_lp128(a, c, s);
     }
     return launched();
@@ -121,7 +135,8 @@ int expert_grouped_weight_grad(int dtype, int64_t m, int64_t n, int64_t k, int64
     if (dtype == EXPERT_F32 && ((k - 1) * ldd + n) * size > kMaxInt - 3) return GEMM_F32_ERR_INVALID_VALUE;
     if ((k + 63) / 64 * ((n + 63) / 64) > kMaxInt / groups) return GEMM_F32_ERR_INVALID_VALUE;
     GroupedArgs a{};
-    const int st = current_device(nullptr, &a.num_xcd);
+    int cus = 0;
+    const int st = current_device(&cus, &a.num_xcd);
     if (st != GEMM_F32_SUCCESS) return st;
     a.A = static_cast<const char *>(A);
     a.B = static_cast<const char *>(G);
@@ -140,10 +155,14 @@ int expert_grouped_weight_grad(int dtype, int64_t m, int64_t n, int64_t k, int64
     if (dtype == EXPERT_F32) {
         launch_f32_weight_grad(a, s);
     } else {
-        const LpCall c{false, true, false, true, wide_rows(dB, a.ldc, n, size) && a.expert_stride % 16 == 0};
+        const LpCall c{false, true, false, true, wide_rows(dB, a.ldc, n, size) && a.expert_stride % 16 == 0, cus};
         const bool copies = aligned(A, 4) && aligned(G, 4) && a.lda % 4 == 0 && a.ldb % 4 == 0;
         if (!copies) launch_lp128_unaligned(a, c, s);
-        else if (k >= 256 && n >= 256) launch_lp256(a, c, s);
+        // The larger tiles from 384 rows on, the length of the contraction, where there
+        // is one for every CU (k = 2048, n = 4096, 256 / 128: 256 rows 139 / 128 us, 512
+        // rows 194 / 208, 1024 rows 287 / 346).
+        else if (mean_rows(m, groups) >= 384 && groups * ((k + 255) / 256) * ((n + 255) / 256) >= cus)
+            launch_lp256(a, c, s);
         else launch_lp128(a, c, s);
     }
     return launched();
@@ -207,7 +226,8 @@ int expert_mx4_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups
     if (need > 0 && !here(workspace, 16)) return GEMM_F32_ERR_INVALID_VALUE;
     if (workspace_bytes < need) return GEMM_F32_ERR_SCRATCH_TOO_SMALL;
     GroupedArgs a{};
-    const int st = current_device(nullptr, &a.num_xcd);
+    int cus = 0;
+    const int st = current_device(&cus, &a.num_xcd);
     if (st != GEMM_F32_SUCCESS) return st;
     if (m == 0) return GEMM_F32_SUCCESS;
     a.A = static_cast<const char *>(X);
@@ -240,8 +260,8 @@ int expert_mx4_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups
     a.A = reinterpret_cast<const char *>(xc);
     a.a_scales = xs;
     a.lda = kp / 2;
-    const LpCall c{true, bf16, true, false, wide_rows(Y, a.ldc, n, size)};
-    if (rows >= 256) launch_lp256(a, c, s);
+    const LpCall c{true, bf16, true, false, wide_rows(Y, a.ldc, n, size), cus};
+    if (large_tiles(rows, m, n, groups, cus)) launch_lp256(a, c, s);
     else launch_lp128(a, c, s);
     return launched();
 }

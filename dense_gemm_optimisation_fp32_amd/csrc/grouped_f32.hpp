@@ -104,10 +104,9 @@ __global__ __launch_bounds__(T::THREADS) void f32_weight_grad_kernel(GroupedArgs
     const int width = a.group_m * a.tiles_n;
     const int first = r / width * a.group_m, size = min(a.tiles_m - first, a.group_m);
     const int row0 = (first + r % width % size) * T::BM, col0 = r % width / size * T::BN;
-    int lo, hi;
-    entry_rows(a, expert, lo, hi);
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    hi = __builtin_amdgcn_readfirstlane(hi);
+    const Rows rows = entry_rows(a, expert);
+    int lo = __builtin_amdgcn_readfirstlane(rows.lo);
+    const int hi = __builtin_amdgcn_readfirstlane(rows.hi);
     GemmArgs g{};
     g.m = a.k;
     g.n = a.n;

@@ -1,10 +1,35 @@
 // Kernel translation unit: grouped bfloat16 and 4-bit products, 256 x 256 tiles.
-#include "lp_launch.hpp"
+#include "expert_launch.hpp"
+#include "lp_pipe.hpp"
 
 namespace gemmf32 {
 
-using Tile = LpTile<256, 256, 2, 4, 2>;
+namespace {
 
-void launch_lp256(const GroupedArgs &a, const LpCall &c, hipStream_t s) { launch_lp<Tile>(a, c, s); }
+using Tile = LpTile<256, 256, 2, 4, 8, 2>;
+
+template <int KIND, bool GRAD, bool B_KS, class E>
+void launch_pipe(const GroupedArgs &a, bool wide, unsigned grid, hipStream_t s)
+{
+    if (wide) lp_pipe_kernel<Tile, KIND, GRAD, B_KS, E, true><<<grid, Tile::THREADS, 0, s>>>(a);
+    else lp_pipe_kernel<Tile, KIND, GRAD, B_KS, E, false><<<grid, Tile::THREADS, 0, s>>>(a);
+}
+
+}  // namespace
+
+void launch_lp256(GroupedArgs a, const LpCall &c, hipStream_t s)
+{
+    a.tiles_m = c.weight_grad ? (a.k + Tile::BM - 1) / Tile::BM : grouped_row_tiles(a, Tile::BM);
+    a.tiles_n = (a.n + Tile::BN - 1) / Tile::BN;
+    // A workgroup a CU, as many on each XCD.
+    const long long tiles = (long long)a.tiles_m * a.tiles_n * (c.weight_grad ? a.groups : 1);
+    const long long most = c.cu_count / a.num_xcd * a.num_xcd;
+    const unsigned grid = (unsigned)(tiles < most ? (tiles + a.num_xcd - 1) / a.num_xcd * a.num_xcd : most);
+    if (c.weight_grad) launch_pipe<kBf16, true, true, __bf16>(a, c.wide, grid, s);
+    else if (c.fp4 && c.bf16) launch_pipe<kFp4, false, false, __bf16>(a, c.wide, grid, s);
+    else if (c.fp4) launch_pipe<kFp4, false, false, float>(a, c.wide, grid, s);
+    else if (c.b_contiguous) launch_pipe<kBf16, false, false, __bf16>(a, c.wide, grid, s);
+    else launch_pipe<kBf16, false, true, __bf16>(a, c.wide, grid, s);
+}
 
 }  // namespace gemmf32

@@ -28,10 +28,10 @@
 //                  with the transposing LDS read (ds_read_b64_tr_b16), which
 //                  hands lane i of 16 column i of four k-rows: the four rows'
 //                  64-byte pieces fall on distinct quarters of the banks.
-// The rows of B (columns of C) of a block of 32 are read in the order
-// 16 ((i / 4) % 2) + 4 (i / 8) + i % 4, which gives each lane 16 neighbouring
-// columns of one row of C: 16-byte stores.  Contiguous B is put in that order
-// by the copy, strided B by the addresses of the transposing read.
+// The rows of B (columns of C) of a block of 32 are read in an order
+// (lp_column) that gives each lane runs of 16 bytes of C, two lanes' side by
+// side.  Contiguous B is put in that order by the copy, strided B by the
+// addresses of the transposing read.
 //
 // Rows past an expert's end are another expert's (or, past the matrix, its
 // last row again): they only feed rows of C that are not stored.  Elements
@@ -50,18 +50,29 @@ typedef __attribute__((address_space(3))) void *lds_void_t;
 
 enum LpKind { kBf16 = 0, kFp4 = 1 };
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_>
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int CPR_, int STAGES_>
 struct LpTile {
+    static constexpr int CPR = CPR_;                      // 16-byte chunks of a row and slab: 4 or 8
+    static constexpr int STEPS = CPR / 2;                 // k-steps of a slab
     static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, STAGES = STAGES_;
     static constexpr int THREADS = WAVES_M * WAVES_N * 64;
     static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
     static constexpr int MB = WM / 32, NB = WN / 32;      // 32 x 32 blocks of a wavefront
-    static constexpr int A_CHUNKS = BM * 8, B_CHUNKS = BN * 8;
+    static constexpr int A_CHUNKS = BM * CPR, B_CHUNKS = BN * CPR;
     static constexpr int A_PER_T = A_CHUNKS / THREADS, B_PER_T = B_CHUNKS / THREADS;
     static constexpr int PIECES = A_PER_T + B_PER_T;
-    static constexpr int SCALE_CHUNKS = (BM + BN) / 2;    // two words of scales a row and slab
+    // 4-bit: a word of scales for 64 bytes of a row, A's and B's each in whole
+    // wavefront copies of 64 chunks.
+    static constexpr int KBLOCKS = CPR / 4;
+    static constexpr int SCALE_WAVES_A = (BM * KBLOCKS / 4 + 63) / 64, SCALE_WAVES_B = (BN * KBLOCKS / 4 + 63) / 64;
+    static constexpr int SCALE_CHUNKS = (SCALE_WAVES_A + SCALE_WAVES_B) * 64;
     static_assert(A_CHUNKS % THREADS == 0 && B_CHUNKS % THREADS == 0, "whole copies");
     static_assert(WM % 32 == 0 && WN % 32 == 0, "32 x 32 blocks");
+    static_assert(CPR == 4 || CPR == 8, "64 or 128 bytes of a row");
+    // Where chunk c of row r of a contiguous operand lies: the 16 rows that a
+    // fragment read touches at a time fall on 16 places of the 256 bytes of
+    // the banks.
+    static __device__ __forceinline__ int swizzle(int r) { return CPR == 4 ? (r >> 2) & 3 : (r >> 1) & 7; }
     static constexpr int stage_chunks(int kind) { return A_CHUNKS + B_CHUNKS + (kind == kFp4 ? SCALE_CHUNKS : 0); }
 };
 
@@ -73,24 +84,41 @@ struct LpOperand {
     int rows;             // rows that may be read (k contiguous), or columns (k strided)
 };
 
-__device__ __forceinline__ void lp_copy16(__amdgpu_buffer_rsrc_t r, uint32_t off, i32x4 *wave_chunk)
-{
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t)wave_chunk, 16, (int)off, 0, 0, 0);
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t lp_rsrc(const char *p, long long bytes)
+// A raw buffer descriptor of `bytes` from p on (word 3 as in make_rsrc).
+__device__ __forceinline__ i32x4 lp_rsrc(const char *p, long long bytes)
 {
     // Up to the end of the last 32-bit word: a word that holds one 16-bit
     // element of the operand is read whole.
     bytes = (bytes + 3) & ~3ll;
-    return make_rsrc(p, bytes < 0 ? 0u : bytes > 0x7ffffffcll ? 0x7ffffffcu : (uint32_t)bytes);
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    return i32x4{(int)(uint32_t)at, (int)((uint32_t)(at >> 32) & 0xffffu),
+                 (int)(bytes < 0 ? 0u : bytes > 0x7ffffffcll ? 0x7ffffffcu : (uint32_t)bytes), kRawBufferWord3};
 }
 
-// Row of a tile that LDS row r of B holds.
-__device__ __forceinline__ int lp_b_row(int r)
+// One 16-byte copy a lane from memory to LDS chunk wave_chunk + lane.  As
+// assembly, because the transposing LDS reads, which the compiler cannot
+// tell apart from the copies' destinations, would else each wait for every
+// copy in flight (counted in the built code: vmcnt(0) before each; the
+// product with row-major B ran at 560 TFLOPS).  It writes no register, and
+// lp_wait and lp_barrier count the copies, so nothing else has to know it.
+__device__ __forceinline__ void lp_copy16(i32x4 r, uint32_t off, i32x4 *wave_chunk)
 {
-    const int i = r & 31;
-    return (r & ~31) + 16 * ((i >> 2) & 1) + 4 * (i >> 3) + (i & 3);
+    const uint32_t at = (uint32_t)(uintptr_t)(lds_void_t)wave_chunk;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(at), "v"(off), "s"(r)
+                 : "memory", "m0");
+}
+
+// Column of C, in a block of 32, that row i of the first operand of a matrix
+// instruction feeds.  The instruction hands lane half h the results of rows
+// 8 q + 4 h + w, as its values 4 q + w; with this order its values are runs of
+// RUN neighbouring columns (16 bytes of C), the two halves' side by side.
+template <int RUN>
+__device__ __forceinline__ int lp_column(int i)
+{
+    const int v = 4 * (i >> 3) + (i & 3), h = (i >> 2) & 1;
+    return v / RUN * (2 * RUN) + h * RUN + v % RUN;
 }
 
 template <int WIDTH>
@@ -101,7 +129,7 @@ __device__ __forceinline__ int lp_strided_swizzle(int kr)
 
 // Byte offset, in its operand at slab 0, of the chunk that lane `tid` copies
 // as piece j.
-template <class T, bool IS_B, bool KS>
+template <class T, bool IS_B, bool KS, int RUN>
 __device__ __forceinline__ uint32_t lp_offset(const LpOperand &o, int j, int tid, int &kr)
 {
     constexpr int W = IS_B ? T::BN : T::BM;
@@ -111,9 +139,9 @@ __device__ __forceinline__ uint32_t lp_offset(const LpOperand &o, int j, int tid
         return (uint32_t)kr * (uint32_t)o.ld + (uint32_t)((c % (W / 8)) ^ lp_strided_swizzle<W>(kr)) * 16u;
     } else {
         kr = 0;
-        const int r = c / 8;
-        const int row = min(IS_B ? lp_b_row(r) : r, o.rows - 1);
-        return (uint32_t)row * (uint32_t)o.ld + (uint32_t)((c % 8) ^ ((r >> 1) & 7)) * 16u;
+        const int r = c / T::CPR;
+        const int row = min(IS_B ? (r & ~31) + lp_column<RUN>(r & 31) : r, o.rows - 1);
+        return (uint32_t)row * (uint32_t)o.ld + (uint32_t)((c % T::CPR) ^ T::swizzle(r)) * 16u;
     }
 }
 
@@ -125,12 +153,23 @@ __device__ __forceinline__ void lp_zero_tail(i32x4 *region, int tid, int left)
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         const int c = tid + j * T::THREADS;
-        const int k0 = ((c % 8) ^ ((c / 8 >> 1) & 7)) * 8;
+        const int k0 = ((c % T::CPR) ^ T::swizzle(c / T::CPR)) * 8;
         i32x4 v = region[c];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             v[i] &= (k0 + 2 * i < left ? 0xffff : 0) | (k0 + 2 * i + 1 < left ? (int)0xffff0000u : 0);
         region[c] = v;
+    }
+}
+
+// The same for A's 4-bit codes; `left` is a whole number of chunks.
+template <class T>
+__device__ __forceinline__ void lp_zero_tail4(i32x4 *region, int tid, int left)
+{
+#pragma unroll
+    for (int j = 0; j < T::A_PER_T; ++j) {
+        const int c = tid + j * T::THREADS;
+        if (((c % T::CPR) ^ T::swizzle(c / T::CPR)) * 32 >= left) region[c] = i32x4{};
     }
 }
 
@@ -143,20 +182,28 @@ __device__ __forceinline__ void lp_barrier()
     asm volatile("s_barrier" ::: "memory");
 }
 
+template <int N>
+__device__ __forceinline__ void lp_wait()
+{
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
 template <class T, int KIND>
 struct LpFrags {
     i32x4 a[2][T::MB], b[2][T::NB];
-    int sa[2][KIND == kFp4 ? T::MB : 1], sb[2][KIND == kFp4 ? T::NB : 1];
+    // 4-bit: scales of this pair of k-steps, and the words of the next one.
+    int sa[KIND == kFp4 ? T::MB : 1], sb[KIND == kFp4 ? T::NB : 1];
+    unsigned na[KIND == kFp4 ? T::MB : 1], nb[KIND == kFp4 ? T::NB : 1];
 };
 
-// Fragments of k-step p.
-template <class T, int KIND, bool A_KS, bool B_KS>
-__device__ __forceinline__ void lp_read(const i32x4 *As, const i32x4 *Bs, int p, int wr, int wc, int lane,
+// Fragment r, of MB + NB, of k-step p.
+template <class T, int KIND, bool A_KS, bool B_KS, int RUN>
+__device__ __forceinline__ void lp_read(const i32x4 *As, const i32x4 *Bs, int r, int p, int wr, int wc, int lane,
                                         LpFrags<T, KIND> &f)
 {
     const int l32 = lane & 31, half = lane >> 5;
     auto contiguous = [&](const i32x4 *region, int row) {
-        return region[row * 8 + ((2 * p + half) ^ ((l32 >> 1) & 7))];
+        return region[row * T::CPR + ((2 * p + half) ^ T::swizzle(l32))];
     };
     // Two transposing reads: k-rows 8 half + 0..3 and + 4..7 of the step.
     auto strided = [&](const i32x4 *region, int width, int col, int swz) {
@@ -169,36 +216,47 @@ __device__ __forceinline__ void lp_read(const i32x4 *As, const i32x4 *Bs, int p,
     };
     const int quad = ((lane >> 4) & 1) * 4 + (lane & 3);         // of the 8 column quads of a block
     const int krow = (lane & 15) >> 2;
-#pragma unroll
-    for (int mb = 0; mb < T::MB; ++mb) {
-        const int row = wr * T::WM + mb * 32;
+    // In the order in which the products of the next step want them.
+    if (r == 0 || (r >= 2 && r > T::NB)) {
+        const int mb = r == 0 ? 0 : r - T::NB, row = wr * T::WM + mb * 32;
         if constexpr (A_KS) f.a[p & 1][mb] = strided(As, T::BM, row + 4 * quad, lp_strided_swizzle<T::BM>(krow));
         else f.a[p & 1][mb] = contiguous(As, row + l32);
-    }
-#pragma unroll
-    for (int nb = 0; nb < T::NB; ++nb) {
-        const int row = wc * T::WN + nb * 32;
+    } else {
+        const int nb = r - 1, row = wc * T::WN + nb * 32;
         if constexpr (B_KS)
-            f.b[p & 1][nb] = strided(Bs, T::BN, row + 4 * (4 * (quad & 1) + (quad >> 1)),
+            f.b[p & 1][nb] = strided(Bs, T::BN, row + lp_column<RUN>(4 * quad),
                                      lp_strided_swizzle<T::BN>(krow));
         else f.b[p & 1][nb] = contiguous(Bs, row + l32);
     }
 }
 
-// Scale words of k-steps 2 q and 2 q + 1, shifted so that the lane's block of
-// step 2 q is byte 0 and of step 2 q + 1 byte 2.
-template <class T, int KIND>
+// Scale words of k-block q of a slab, k-steps 2 q and 2 q + 1.
+template <class T, int KIND, int RUN>
 __device__ __forceinline__ void lp_read_scales(const i32x4 *Ss, int q, int wr, int wc, int lane, LpFrags<T, KIND> &f)
 {
     if constexpr (KIND == kFp4) {
-        const int l32 = lane & 31, half = lane >> 5;
-        const unsigned *w = reinterpret_cast<const unsigned *>(Ss) + q * (T::BM + T::BN);
-        const int i = l32;
-        const int b_row = 16 * ((i >> 2) & 1) + 4 * (i >> 3) + (i & 3);
+        const int l32 = lane & 31;
+        const unsigned *wa = reinterpret_cast<const unsigned *>(Ss) + q * T::BM;
+        const unsigned *wb = reinterpret_cast<const unsigned *>(Ss) + T::SCALE_WAVES_A * 256 + q * T::BN;
+        const int b_row = lp_column<RUN>(l32);
 #pragma unroll
-        for (int mb = 0; mb < T::MB; ++mb) f.sa[q][mb] = (int)(w[wr * T::WM + mb * 32 + l32] >> (8 * half));
+        for (int mb = 0; mb < T::MB; ++mb) f.na[mb] = wa[wr * T::WM + mb * 32 + l32];
 #pragma unroll
-        for (int nb = 0; nb < T::NB; ++nb) f.sb[q][nb] = (int)(w[T::BM + wc * T::WN + nb * 32 + b_row] >> (8 * half));
+        for (int nb = 0; nb < T::NB; ++nb) f.nb[nb] = wb[wc * T::WN + nb * 32 + b_row];
+    }
+}
+
+// The words just read become those in use, shifted so that the lane's block
+// of the pair's first step is byte 0 and of its second byte 2.
+template <class T, int KIND>
+__device__ __forceinline__ void lp_take_scales(int lane, LpFrags<T, KIND> &f)
+{
+    if constexpr (KIND == kFp4) {
+        const int shift = 8 * (lane >> 5);
+#pragma unroll
+        for (int mb = 0; mb < T::MB; ++mb) f.sa[mb] = (int)(f.na[mb] >> shift);
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb) f.sb[nb] = (int)(f.nb[nb] >> shift);
     }
 }
 
@@ -216,10 +274,10 @@ __device__ __forceinline__ void lp_mfma(int i, int p, const LpFrags<T, KIND> &f,
         const i32x8 a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
         if (p & 1)
             acc[mb][nb] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, acc[mb][nb], 4, 4, 2,
-                                                                          f.sb[p >> 1][nb], 2, f.sa[p >> 1][mb]);
+                                                                          f.sb[nb], 2, f.sa[mb]);
         else
             acc[mb][nb] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, acc[mb][nb], 4, 4, 0,
-                                                                          f.sb[p >> 1][nb], 0, f.sa[p >> 1][mb]);
+                                                                          f.sb[nb], 0, f.sa[mb]);
     }
 }
 
@@ -235,12 +293,15 @@ struct LpProblem {
 // REG: operands whose rows are not 4-byte aligned (bfloat16 rows of odd
 // length) cannot be copied straight into LDS; their chunks pass through
 // registers, one slab ahead, with the tails made zero on the way.
-template <class T, int KIND, bool A_KS, bool B_KS, bool REG = false>
+template <class T, int KIND, bool A_KS, bool B_KS, int RUN, bool REG = false>
 struct LpLoop {
-    static_assert(!REG || (KIND == kBf16 && T::STAGES == 2), "register copies: bfloat16, two stages");
-    static constexpr int KSLAB = KIND == kFp4 ? 256 : 64;
-    static constexpr int SCALE_PER_T = (T::SCALE_CHUNKS + T::THREADS - 1) / T::THREADS;
-    static_assert(KIND != kFp4 || (T::BM % 64 == 0 && T::BN % 64 == 0), "scale words in whole copies");
+    static_assert(!REG || (KIND == kBf16 && T::STAGES >= 2), "register copies: bfloat16, two stages or more");
+    static constexpr int KSLAB = T::CPR * (KIND == kFp4 ? 32 : 8);
+    // Scale words of a slab: [A, B][k-block][row], four a chunk.  The first
+    // wavefronts copy A's, the next ones B's, and further ones the same again:
+    // a branch around the copy would split the slab's schedule.
+    static constexpr int SCALE_COPIES = T::SCALE_WAVES_A + T::SCALE_WAVES_B;
+    static_assert(KIND != kFp4 || T::THREADS / 64 >= SCALE_COPIES, "one copy of scales a wavefront");
     const LpProblem &q;
     i32x4 *lds;
     int tid, lane, wave, wr, wc;
@@ -248,62 +309,66 @@ struct LpLoop {
     uint32_t a_off[T::A_PER_T], b_off[T::B_PER_T];
     int a_kr[T::A_PER_T], b_kr[T::B_PER_T];
     i32x4 regs[REG ? T::PIECES : 1];
-    uint32_t s_off[KIND == kFp4 ? SCALE_PER_T : 1];
+    uint32_t s_off;                // 4-bit: the lane's scale chunk
+    int s_wave;
+    bool s_is_a;
 
     __device__ __forceinline__ i32x4 *stage(int s) const { return lds + s * T::stage_chunks(KIND); }
 
     __device__ __forceinline__ void setup()
     {
 #pragma unroll
-        for (int j = 0; j < T::A_PER_T; ++j) a_off[j] = lp_offset<T, false, A_KS>(q.a, j, tid, a_kr[j]);
+        for (int j = 0; j < T::A_PER_T; ++j) a_off[j] = lp_offset<T, false, A_KS, RUN>(q.a, j, tid, a_kr[j]);
 #pragma unroll
-        for (int j = 0; j < T::B_PER_T; ++j) b_off[j] = lp_offset<T, true, B_KS>(q.b, j, tid, b_kr[j]);
-        if constexpr (KIND == kFp4)
-#pragma unroll
-            for (int j = 0; j < SCALE_PER_T; ++j) {
-                const int c = j * T::THREADS + tid, at = c % (T::SCALE_CHUNKS / 2);
-                const bool is_a = at < T::BM / 4;
-                s_off[j] = (c < T::SCALE_CHUNKS / 2 ? 0u : (uint32_t)(is_a ? q.a_scale_step : q.b_scale_step)) +
-                           (uint32_t)(is_a ? at : at - T::BM / 4) * 16u;
-            }
+        for (int j = 0; j < T::B_PER_T; ++j) b_off[j] = lp_offset<T, true, B_KS, RUN>(q.b, j, tid, b_kr[j]);
+        if constexpr (KIND == kFp4) {
+            s_wave = wave % SCALE_COPIES;
+            s_is_a = s_wave < T::SCALE_WAVES_A;
+            const int per = s_is_a ? T::BM / 4 : T::BN / 4;        // chunks of a k-block (128 columns)
+            const int c = (s_wave - (s_is_a ? 0 : T::SCALE_WAVES_A)) * 64 + lane;
+            const uint32_t step = (uint32_t)(s_is_a ? q.a_scale_step : q.b_scale_step);
+            s_off = c >= T::KBLOCKS * per ? kOobOffset : (c < per ? 0u : step) + (uint32_t)(c < per ? c : c - per) * 16u;
+        }
         slabs = (q.k + KSLAB - 1) / KSLAB;
         tail = q.k % KSLAB;
     }
 
-    // Copy slab kt into its stage.
-    __device__ __forceinline__ void copy(int kt) const
+    // Copies of slab kt: descriptors of the operands from the slab's first k on.
+    struct Source {
+        i32x4 a, b, s;
+        i32x4 *st;
+        int left;                  // elements from the slab's first on
+    };
+    __device__ __forceinline__ Source source(int kt) const
     {
-        i32x4 *const st = stage(kt % T::STAGES);
-        const int left = q.k - kt * KSLAB;             // elements from the slab's first on
-        const long long sa = A_KS ? (long long)kt * KSLAB * q.a.ld : (long long)kt * 128;
-        const long long sb = B_KS ? (long long)kt * KSLAB * q.b.ld : (long long)kt * 128;
-        const __amdgpu_buffer_rsrc_t ra = lp_rsrc(q.a.p + sa, q.a.bytes - sa);
-        const __amdgpu_buffer_rsrc_t rb = lp_rsrc(q.b.p + sb, q.b.bytes - sb);
-#pragma unroll
-        for (int j = 0; j < T::A_PER_T; ++j)
-            lp_copy16(ra, A_KS && a_kr[j] >= left ? kOobOffset : a_off[j], st + j * T::THREADS + wave * 64);
-#pragma unroll
-        for (int j = 0; j < T::B_PER_T; ++j)
-            lp_copy16(rb, B_KS && b_kr[j] >= left ? kOobOffset : b_off[j],
-                      st + T::A_CHUNKS + j * T::THREADS + wave * 64);
+        Source c;
+        c.st = stage(kt % T::STAGES);
+        c.left = q.k - kt * KSLAB;
+        const long long sa = A_KS ? (long long)kt * KSLAB * q.a.ld : (long long)kt * (T::CPR * 16);
+        const long long sb = B_KS ? (long long)kt * KSLAB * q.b.ld : (long long)kt * (T::CPR * 16);
+        c.a = lp_rsrc(q.a.p + sa, q.a.bytes - sa);
+        c.b = lp_rsrc(q.b.p + sb, q.b.bytes - sb);
         if constexpr (KIND == kFp4) {
-            // Words of scales: [k-block][rows of A, rows of B], four rows a
-            // chunk; the wavefronts take 64 chunks each.  A block past the
-            // last one is past the extents and reads as zero.
-            const long long ka = (long long)(2 * kt) * q.a_scale_step, kb = (long long)(2 * kt) * q.b_scale_step;
-            const __amdgpu_buffer_rsrc_t rsa =
-                lp_rsrc(reinterpret_cast<const char *>(q.a_scales) + ka, q.a_scale_bytes - ka);
-            const __amdgpu_buffer_rsrc_t rsb =
-                lp_rsrc(reinterpret_cast<const char *>(q.b_scales) + kb, q.b_scale_bytes - kb);
-            i32x4 *const ss = st + T::A_CHUNKS + T::B_CHUNKS;
-#pragma unroll
-            for (int j = 0; j < SCALE_PER_T; ++j) {
-                const int w0 = j * T::THREADS + wave * 64;
-                if (w0 < T::SCALE_CHUNKS) {
-                    if ((w0 + lane) % (T::SCALE_CHUNKS / 2) < T::BM / 4) lp_copy16(rsa, s_off[j], ss + w0);
-                    else lp_copy16(rsb, s_off[j], ss + w0);
-                }
-            }
+            const long long k = (long long)(T::KBLOCKS * kt) * (s_is_a ? q.a_scale_step : q.b_scale_step);
+            c.s = lp_rsrc(reinterpret_cast<const char *>(s_is_a ? q.a_scales : q.b_scales) + k,
+                          (s_is_a ? q.a_scale_bytes : q.b_scale_bytes) - k);
+        }
+        return c;
+    }
+    static constexpr int COPIES = T::PIECES + (KIND == kFp4 ? 1 : 0);
+
+    // Copy i, of COPIES.
+    __device__ __forceinline__ void copy(const Source &c, int i) const
+    {
+        if (i < T::A_PER_T) {
+            lp_copy16(c.a, A_KS && a_kr[i] >= c.left ? kOobOffset : a_off[i], c.st + i * T::THREADS + wave * 64);
+        } else if (i < T::PIECES) {
+            const int j = i - T::A_PER_T;
+            lp_copy16(c.b, B_KS && b_kr[j] >= c.left ? kOobOffset : b_off[j],
+                      c.st + T::A_CHUNKS + j * T::THREADS + wave * 64);
+        } else if constexpr (KIND == kFp4) {
+            // A block past the last one is past the extents and reads as zero.
+            lp_copy16(c.s, s_off, c.st + T::A_CHUNKS + T::B_CHUNKS + s_wave * 64);
         }
     }
 
@@ -317,8 +382,8 @@ struct LpLoop {
                 return load_chunk(reinterpret_cast<const __bf16 *>(o.p + (long long)kt * KSLAB * o.ld + off),
                                   kr < left ? o.rows - col : 0);
             }
-            const int k0 = ((c % 8) ^ ((c / 8 >> 1) & 7)) * 8;
-            return load_chunk(reinterpret_cast<const __bf16 *>(o.p + (long long)kt * 128 + off), left - k0);
+            const int k0 = ((c % T::CPR) ^ T::swizzle(c / T::CPR)) * 8;
+            return load_chunk(reinterpret_cast<const __bf16 *>(o.p + (long long)kt * (T::CPR * 16) + off), left - k0);
         };
 #pragma unroll
         for (int j = 0; j < T::A_PER_T; ++j)
@@ -345,60 +410,77 @@ struct LpLoop {
         }
     }
 
-    __device__ __forceinline__ void read(int kt, int p, LpFrags<T, KIND> &f) const
+    static constexpr int READS = T::MB + T::NB;
+    __device__ __forceinline__ void read(int kt, int p, int r, LpFrags<T, KIND> &f) const
     {
         const i32x4 *const st = stage(kt % T::STAGES);
-        if (KIND == kFp4 && (p & 1) == 0) lp_read_scales<T, KIND>(st + T::A_CHUNKS + T::B_CHUNKS, p >> 1, wr, wc, lane, f);
-        lp_read<T, KIND, A_KS, B_KS>(st, st + T::A_CHUNKS, p, wr, wc, lane, f);
+        if (KIND == kFp4 && r == 0 && (p & 1) == 0)
+            lp_read_scales<T, KIND, RUN>(st + T::A_CHUNKS + T::B_CHUNKS, p >> 1, wr, wc, lane, f);
+        lp_read<T, KIND, A_KS, B_KS, RUN>(st, st + T::A_CHUNKS, r, p, wr, wc, lane, f);
     }
 
-    // One slab.  WAIT: copies that may stay in flight when the next slab is
-    // taken over; -1: there is no next slab.
-    template <int WAIT, bool COPY>
-    __device__ __forceinline__ void slab(int kt, LpFrags<T, KIND> &f, f32x16 (&acc)[T::MB][T::NB])
+    // The products of k-step p, one read of the next step (slab kt_next, step
+    // p_next) and, in COPY's step, one copy after each.
+    template <bool READ, bool COPY>
+    __device__ __forceinline__ void step(int p, int kt_next, int p_next, const Source &c, LpFrags<T, KIND> &f,
+                                         f32x16 (&acc)[T::MB][T::NB]) const
     {
         constexpr int NM = T::MB * T::NB;
-        // A 4-bit slab of one k-block (the last one of an odd number) holds
-        // two k-steps' values; the others' codes are another row's.
-        const bool half_slab = KIND == kFp4 && WAIT < 0 && tail != 0;
+        if ((p & 1) == 0) lp_take_scales<T, KIND>(lane, f);
+        constexpr int RPM = (READS + NM - 1) / NM, CPM = (COPIES + NM - 1) / NM;
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
-            if (KIND == kFp4 && WAIT < 0 && p >= 2 && half_slab) break;
-            __builtin_amdgcn_s_setprio(1);
-            lp_mfma<T, KIND>(0, p, f, acc);
-            __builtin_amdgcn_sched_barrier(0);
-            read(kt, p + 1, f);
+        for (int i = 0; i < NM; ++i) {
+            lp_mfma<T, KIND>(i, p, f, acc);
+            if constexpr (READ)
 #pragma unroll
-            for (int i = 1; i < NM; ++i) lp_mfma<T, KIND>(i, p, f, acc);
-            __builtin_amdgcn_s_setprio(0);
+                for (int r = i * RPM; r < (i + 1) * RPM && r < READS; ++r) read(kt_next, p_next, r, f);
+            if constexpr (COPY)
+#pragma unroll
+                for (int j = i * CPM; j < (i + 1) * CPM && j < COPIES; ++j) copy(c, j);
             __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (WAIT >= 0) {
+    }
+
+    // One slab.  COPY: the slab STAGES ahead is copied, as soon as this one's
+    // last fragments are read.  LAST: there is no next slab.
+    template <bool COPY, bool LAST>
+    __device__ __forceinline__ void slab(int kt, LpFrags<T, KIND> &f, f32x16 (&acc)[T::MB][T::NB])
+    {
+        // 4-bit slabs of two k-blocks: the last one of an odd number holds
+        // half the steps' values; the others' codes are another row's.
+        const bool half_slab = KIND == kFp4 && LAST && tail != 0;
+        Source c;
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int p = 0; p + 1 < T::STEPS; ++p)
+            if (p < T::STEPS / 2 || !half_slab) step<true, false>(p, kt, p + 1, c, f, acc);
+        __builtin_amdgcn_s_setprio(0);
+        if constexpr (!LAST) {
             if constexpr (REG) {
                 store(kt + 1);
-            } else if (kt + 2 == slabs && tail != 0 && KIND == kBf16 && !(A_KS && B_KS)) {
-                __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (15 << 8));
-                fix_tail(kt + 1);
+                lp_barrier<63>();
+            } else if constexpr (COPY) {
+                lp_barrier<(T::STAGES - 2) * COPIES>();
+            } else {
+                // The slabs after the next one may still be on their way.
+                if (T::STAGES > 3 && slabs - 2 - kt >= 2) lp_wait<2 * COPIES>();
+                else if (T::STAGES > 2 && slabs - 2 - kt >= 1) lp_wait<COPIES>();
+                else lp_wait<0>();
+                if (kt + 2 == slabs && tail != 0) fix_tail(kt + 1);
+                lp_barrier<63>();
             }
-            lp_barrier<WAIT>();
             if constexpr (COPY && REG) load(kt + 2);
-            else if constexpr (COPY) copy(kt + T::STAGES);
+            if constexpr (COPY && !REG) c = source(kt + T::STAGES);
             __builtin_amdgcn_sched_barrier(0);
-            lp_mfma<T, KIND>(0, 3, f, acc);
-            __builtin_amdgcn_sched_barrier(0);
-            read(kt + 1, 0, f);
-#pragma unroll
-            for (int i = 1; i < NM; ++i) lp_mfma<T, KIND>(i, 3, f, acc);
-            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(1);
+            step<true, COPY && !REG>(T::STEPS - 1, kt + 1, 0, c, f, acc);
         } else if (!half_slab) {
-#pragma unroll
-            for (int i = 0; i < NM; ++i) lp_mfma<T, KIND>(i, 3, f, acc);
+            step<false, false>(T::STEPS - 1, 0, 0, c, f, acc);
         }
     }
 
     __device__ __forceinline__ void run(f32x16 (&acc)[T::MB][T::NB])
     {
-        constexpr int P = T::PIECES;
         setup();
         if (slabs == 0) return;
         LpFrags<T, KIND> f;
@@ -406,83 +488,165 @@ struct LpLoop {
             load(0);
             store(0);
             if (slabs > 1) load(1);
+            lp_barrier<63>();
         } else {
 #pragma unroll
             for (int s = 0; s < T::STAGES; ++s)
-                if (s < slabs) copy(s);
+                if (s < slabs) {
+                    const Source c = source(s);
+#pragma unroll
+                    for (int i = 0; i < COPIES; ++i) copy(c, i);
+                }
+            if (slabs == 1) {
+                lp_wait<0>();
+                if (tail) fix_tail(0);
+                lp_barrier<63>();
+            } else if (slabs >= T::STAGES) {
+                lp_barrier<(T::STAGES - 1) * COPIES>();
+            } else {
+                lp_barrier<0>();
+            }
         }
-        if constexpr (REG) {
-            lp_barrier<63>();
-        } else if (slabs == 1) {
-            __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (15 << 8));
-            if (tail) fix_tail(0);
-            lp_barrier<0>();
-        } else if (KIND == kBf16 && slabs >= T::STAGES) {
-            lp_barrier<(T::STAGES - 1) * P>();
-        } else {
-            lp_barrier<0>();
-        }
-        read(0, 0, f);
+#pragma unroll
+        for (int r = 0; r < READS; ++r) read(0, 0, r, f);
         int kt = 0;
-        // (4-bit: the wavefronts' numbers of scale copies differ, so every
-        // copy in flight is counted as the values' alone: a wait for fewer.)
-        constexpr int WAIT = REG ? 63 : (T::STAGES - 2) * P;
-        for (; kt + T::STAGES < slabs; ++kt) slab<WAIT, true>(kt, f, acc);
-        for (; kt + 1 < slabs; ++kt) slab<REG ? 63 : 0, false>(kt, f, acc);
-        slab<-1, false>(kt, f, acc);
+        constexpr int AHEAD = REG ? 2 : T::STAGES;
+        for (; kt + AHEAD < slabs; ++kt) slab<true, false>(kt, f, acc);
+        for (; kt + 1 < slabs; ++kt) slab<false, false>(kt, f, acc);
+        slab<false, true>(kt, f, acc);
     }
 };
 
-// C's 32 x 32 blocks: lane l32 holds row l32 of the block, columns 16 half ..
-// + 15.  WIDE: rows and column runs of C are 16-byte aligned and n is a
-// multiple of the elements in 16 bytes.
+// C's 32 x 32 blocks: lane l32 holds row l32 of the block, in runs of RUN
+// columns.  WIDE: rows and column runs of C are 16-byte aligned and n is a
+// multiple of RUN.  Bias and activation are passes of their own over the
+// accumulators, so that a call without them jumps over two pieces of code
+// and not, element by element, through all of it: with the activation's
+// branch at each element the epilogue waited for instructions (34000 cycles a
+// tile of 256 x 256).
 template <class T, class E, bool WIDE>
-__device__ __forceinline__ void lp_store(char *c, long long ldc, int rows, int cols, const float *bias, int act,
-                                         bool zero, int wr, int wc, int lane, const f32x16 (&acc)[T::MB][T::NB])
+__device__ __forceinline__ void lp_store(char *c, long long ldc, int rows, int cols, const float *bias, int act, int wr,
+                                         int wc, int lane, f32x16 (&acc)[T::MB][T::NB])
 {
+    constexpr int RUN = 16 / sizeof(E);
     const int l32 = lane & 31, half = lane >> 5;
+    const int col0 = wc * T::WN + half * RUN;
+    if (bias) {
 #pragma unroll
-    for (int nb = 0; nb < T::NB; ++nb) {
-        const int col = wc * T::WN + nb * 32 + 16 * half;
-        float b[16];
-#pragma unroll
-        for (int v = 0; v < 16; ++v) b[v] = bias && col + v < cols ? bias[col + v] : 0.0f;
-#pragma unroll
-        for (int mb = 0; mb < T::MB; ++mb) {
-            const int row = wr * T::WM + mb * 32 + l32;
-            E y[16];
+        for (int nb = 0; nb < T::NB; ++nb)
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
-                float x = acc[mb][nb][v] + b[v];
-                if (act) x = activate(x, act);
-                // One rounding, to the type of C.
-                y[v] = (E)(zero ? 0.0f : x);
+                const int col = col0 + nb * 32 + v / RUN * (2 * RUN) + v % RUN;
+                const float b = col < cols ? bias[col] : 0.0f;
+#pragma unroll
+                for (int mb = 0; mb < T::MB; ++mb) acc[mb][nb][v] += b;
             }
-            E *const p = reinterpret_cast<E *>(c + row * ldc) + col;
-            if (row < rows) {
+    }
+    if (act == 1) {
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb)
+#pragma unroll
+            for (int mb = 0; mb < T::MB; ++mb)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[mb][nb][v] = activate(acc[mb][nb][v], 1);
+    } else if (act == 2) {
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb)
+#pragma unroll
+            for (int mb = 0; mb < T::MB; ++mb)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[mb][nb][v] = gelu_rcp(acc[mb][nb][v]);
+    }
+#pragma unroll
+    for (int mb = 0; mb < T::MB; ++mb) {
+        const int row = wr * T::WM + mb * 32 + l32;
+        if (row >= rows) continue;
+        E *const p = reinterpret_cast<E *>(c + row * ldc);
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb)
+#pragma unroll
+            for (int v0 = 0; v0 < 16; v0 += RUN) {
+                const int col = col0 + nb * 32 + v0 * 2;
+                // One rounding, to the type of C.
+                struct alignas(16) Run {
+                    E e[RUN];
+                } r;
+#pragma unroll
+                for (int i = 0; i < RUN; ++i) r.e[i] = (E)acc[mb][nb][v0 + i];
                 if constexpr (WIDE) {
-                    constexpr int N = 16 / sizeof(E);
-#pragma unroll
-                    for (int v = 0; v < 16; v += N)
-                        if (col + v < cols) {
-                            struct alignas(16) Run {
-                                E e[N];
-                            } r;
-#pragma unroll
-                            for (int i = 0; i < N; ++i) r.e[i] = y[v + i];
-                            *reinterpret_cast<Run *>(p + v) = r;
-                        }
+                    if (col < cols) *reinterpret_cast<Run *>(p + col) = r;
                 } else {
 #pragma unroll
-                    for (int v = 0; v < 16; ++v)
-                        if (col + v < cols) p[v] = y[v];
+                    for (int i = 0; i < RUN; ++i)
+                        if (col + i < cols) p[col + i] = r.e[i];
                 }
             }
-        }
     }
 }
 
-// C_e = act(A_e . B_e + bias_e).
+// One tile of C_e = act(A_e . B_e + bias_e): rows from `row` on, of which the
+// expert has `rows`, columns from col on.  Expert -1: zeros.
+template <class T, int KIND, bool B_KS, class E, bool WIDE, bool REG = false>
+__device__ __forceinline__ void lp_tile(const GroupedArgs &g, i32x4 *lds, int tid, int lane, int wave, int expert,
+                                        int row, int rows, int col)
+{
+    const int cols = g.n - col;
+    const int wr = wave % T::WAVES_M, wc = wave / T::WAVES_M;
+    f32x16 acc[T::MB][T::NB];
+#pragma unroll
+    for (int mb = 0; mb < T::MB; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] = f32x16{};
+    if (expert >= 0) {
+        LpProblem q;
+        const long long row_bytes = KIND == kFp4 ? (long long)g.a_kblocks * 64 : (long long)g.k * 2;
+        q.a = {g.A + row * g.lda, (g.m - 1 - row) * g.lda + row_bytes, (int)g.lda, g.m - row};
+        const char *const b = g.B + expert * g.expert_stride;
+        if constexpr (B_KS)
+            q.b = {b + (long long)col * 2, (long long)(g.k - 1) * g.ldb + (long long)cols * 2, (int)g.ldb, cols};
+        else
+            q.b = {b + col * g.ldb, (cols - 1) * g.ldb + row_bytes, (int)g.ldb, cols};
+        q.k = g.k;
+        if constexpr (KIND == kFp4) {
+            q.k = g.a_kblocks * 128;
+            q.a_scales = g.a_scales + (long long)row * 4;
+            q.a_scale_step = (long long)g.m * 4;
+            q.a_scale_bytes = g.a_kblocks * q.a_scale_step - (long long)row * 4;
+            q.b_scale_step = (long long)g.n * 4;
+            q.b_scales = g.b_scales + expert * (g.a_kblocks * q.b_scale_step) + (long long)col * 4;
+            q.b_scale_bytes = g.a_kblocks * q.b_scale_step - (long long)col * 4;
+        }
+        LpLoop<T, KIND, false, B_KS, 16 / sizeof(E), REG> loop{q, lds, tid, lane, wave, wr, wc};
+        loop.run(acc);
+    }
+    const float *bias = g.bias && expert >= 0 ? g.bias + expert * g.bias_stride + col : nullptr;
+    lp_store<T, E, WIDE>(g.C + row * g.ldc + (long long)col * sizeof(E), g.ldc, rows, cols, bias, expert < 0 ? 0 : g.act,
+                         wr, wc, lane, acc);
+}
+
+// One tile of dB_e = A_e^T . G_e: g.m rows of A (g.k columns) and G (g.n
+// columns), the expert's lo .. hi; zeros where it has none.
+template <class T, bool WIDE, bool REG = false>
+__device__ __forceinline__ void lp_grad_tile(const GroupedArgs &g, i32x4 *lds, int tid, int lane, int wave, int expert,
+                                             int lo, int hi, int row, int col)
+{
+    const int wr = wave % T::WAVES_M, wc = wave / T::WAVES_M;
+    f32x16 acc[T::MB][T::NB];
+#pragma unroll
+    for (int mb = 0; mb < T::MB; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] = f32x16{};
+    LpProblem q;
+    const long long last = hi - lo - 1;      // -1: no rows, no bytes are read
+    q.a = {g.A + lo * g.lda + (long long)row * 2, last * g.lda + (long long)(g.k - row) * 2, (int)g.lda, g.k - row};
+    q.b = {g.B + lo * g.ldb + (long long)col * 2, last * g.ldb + (long long)(g.n - col) * 2, (int)g.ldb, g.n - col};
+    q.k = hi - lo;
+    LpLoop<T, kBf16, true, true, 8, REG> loop{q, lds, tid, lane, wave, wr, wc};
+    loop.run(acc);
+    lp_store<T, __bf16, WIDE>(g.C + expert * g.expert_stride + row * g.ldc + (long long)col * 2, g.ldc, g.k - row,
+                              g.n - col, nullptr, 0, wr, wc, lane, acc);
+}
+
 template <class T, int KIND, bool B_KS, class E, bool WIDE, bool REG = false>
 __global__ __launch_bounds__(T::THREADS) void lp_grouped_kernel(GroupedArgs g)
 {
@@ -492,42 +656,9 @@ __global__ __launch_bounds__(T::THREADS) void lp_grouped_kernel(GroupedArgs g)
     RowTile rt;
     int tn;
     if (!find_tile<T::BM>(g, blockIdx.x, lane, rt, tn)) return;
-    const int col0 = tn * T::BN, cols = g.n - col0;
-    const int wr = wave % T::WAVES_M, wc = wave / T::WAVES_M;
-    f32x16 acc[T::MB][T::NB];
-#pragma unroll
-    for (int mb = 0; mb < T::MB; ++mb)
-#pragma unroll
-        for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] = f32x16{};
-    if (rt.expert >= 0) {
-        LpProblem q;
-        const long long row_bytes = KIND == kFp4 ? (long long)g.a_kblocks * 64 : (long long)g.k * 2;
-        q.a = {g.A + rt.row * g.lda, (g.m - 1 - rt.row) * g.lda + row_bytes, (int)g.lda, g.m - rt.row};
-        const char *const b = g.B + rt.expert * g.expert_stride;
-        if constexpr (B_KS)
-            q.b = {b + (long long)col0 * 2, (long long)(g.k - 1) * g.ldb + (long long)cols * 2, (int)g.ldb, cols};
-        else
-            q.b = {b + col0 * g.ldb, (cols - 1) * g.ldb + row_bytes, (int)g.ldb, cols};
-        q.k = g.k;
-        if constexpr (KIND == kFp4) {
-            q.k = g.a_kblocks * 128;
-            q.a_scales = g.a_scales + (long long)rt.row * 4;
-            q.a_scale_step = (long long)g.m * 4;
-            q.a_scale_bytes = g.a_kblocks * q.a_scale_step - (long long)rt.row * 4;
-            q.b_scale_step = (long long)g.n * 4;
-            q.b_scales = g.b_scales + rt.expert * (g.a_kblocks * q.b_scale_step) + (long long)col0 * 4;
-            q.b_scale_bytes = g.a_kblocks * q.b_scale_step - (long long)col0 * 4;
-        }
-        LpLoop<T, KIND, false, B_KS, REG> loop{q, lds, tid, lane, wave, wr, wc};
-        loop.run(acc);
-    }
-    const float *bias = g.bias && rt.expert >= 0 ? g.bias + rt.expert * g.bias_stride + col0 : nullptr;
-    lp_store<T, E, WIDE>(g.C + rt.row * g.ldc + (long long)col0 * sizeof(E), g.ldc, rt.rows, cols, bias, g.act,
-                         rt.expert < 0, wr, wc, lane, acc);
+    lp_tile<T, KIND, B_KS, E, WIDE, REG>(g, lds, tid, lane, wave, rt.expert, rt.row, rt.rows, tn * T::BN);
 }
 
-// dB_e = A_e^T . G_e: g.m rows of A (g.k columns) and G (g.n columns); tiles of
-// the experts' k x n matrices.  An expert without rows gets zeros.
 template <class T, bool WIDE, bool REG = false>
 __global__ __launch_bounds__(T::THREADS) void lp_weight_grad_kernel(GroupedArgs g)
 {
@@ -540,27 +671,10 @@ __global__ __launch_bounds__(T::THREADS) void lp_weight_grad_kernel(GroupedArgs 
     const int r = logical % per;
     const int width = g.group_m * g.tiles_n;
     const int first = r / width * g.group_m, size = min(g.tiles_m - first, g.group_m);
-    const int tm = first + r % width % size, tn = r % width / size;
-    int lo, hi;
-    entry_rows(g, expert, lo, hi);
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    hi = __builtin_amdgcn_readfirstlane(hi);
-    const int row0 = tm * T::BM, col0 = tn * T::BN;
-    const int wr = wave % T::WAVES_M, wc = wave / T::WAVES_M;
-    f32x16 acc[T::MB][T::NB];
-#pragma unroll
-    for (int mb = 0; mb < T::MB; ++mb)
-#pragma unroll
-        for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] = f32x16{};
-    LpProblem q;
-    const long long last = hi - lo - 1;      // -1: no rows, no bytes are read
-    q.a = {g.A + lo * g.lda + (long long)row0 * 2, last * g.lda + (long long)(g.k - row0) * 2, (int)g.lda, g.k - row0};
-    q.b = {g.B + lo * g.ldb + (long long)col0 * 2, last * g.ldb + (long long)(g.n - col0) * 2, (int)g.ldb, g.n - col0};
-    q.k = hi - lo;
-    LpLoop<T, kBf16, true, true, REG> loop{q, lds, tid, lane, wave, wr, wc};
-    loop.run(acc);
-    lp_store<T, __bf16, WIDE>(g.C + expert * g.expert_stride + row0 * g.ldc + (long long)col0 * 2, g.ldc,
-                              g.k - row0, g.n - col0, nullptr, 0, false, wr, wc, lane, acc);
+    const Rows rows = entry_rows(g, expert);
+    lp_grad_tile<T, WIDE, REG>(g, lds, tid, lane, wave, expert, __builtin_amdgcn_readfirstlane(rows.lo),
+                               __builtin_amdgcn_readfirstlane(rows.hi), (first + r % width % size) * T::BM,
+                               r % width / size * T::BN);
 }
 
 }  // namespace gemmf32
