@@ -1,4 +1,5 @@
-"""Build libgemm_f32.so in-tree with hipcc for gfx950.
+"""Build libgemm_f32.so, and the Python module _expert_binding.so in front of its
+expert-layer entry points, in-tree with hipcc for gfx950.
 
 Usage: ``python -m dense_gemm_optimisation_fp32_amd.build`` (or call
 ``build()``).  Always recompiles.
@@ -20,12 +21,15 @@ import os
 import re
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libgemm_f32.so")
+BINDING_SOURCE = os.path.join(CSRC, "expert_binding.c")
+BINDING_PATH = os.path.join(PKG_DIR, "_expert_binding.so")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 HOST_SOURCES = [os.path.join(CSRC, "gemm_f32.hip"), os.path.join(CSRC, "expert_ops.hip")]
 
@@ -140,6 +144,17 @@ def build(verbose: bool = False) -> str:
     if p.returncode != 0:
         _fail("link", p.stderr)
     os.replace(tmp, LIB_PATH)
+
+    # The Python module in front of the expert-layer entry points.
+    tmp = BINDING_PATH + ".tmp"
+    cmd = ["gcc", "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-o", tmp, BINDING_SOURCE]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        _fail("expert_binding.c", p.stderr)
+    os.replace(tmp, BINDING_PATH)
     return LIB_PATH
 
 

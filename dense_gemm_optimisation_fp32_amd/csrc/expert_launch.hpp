@@ -17,6 +17,13 @@ inline int grouped_row_tiles(const GroupedArgs &a, int bm)
     return (int)(tiles < a.m ? tiles : a.m);
 }
 
+// Workgroups of a weight gradient with a tile each: every XCD's share of every
+// expert's tiles.
+inline unsigned grad_workgroups(const GroupedArgs &a)
+{
+    return (unsigned)((a.tiles_m * a.tiles_n + a.num_xcd - 1) / a.num_xcd) * a.num_xcd * a.groups;
+}
+
 // Which of a tile shape's kernels a call takes.
 struct LpCall {
     bool fp4, bf16;         // 4-bit operands; 16-bit results
@@ -33,13 +40,13 @@ int record_hip_error(hipError_t e);
 
 void launch_mx4_quantize(const Mx4Args &a, bool bf16, bool columns, hipStream_t s);
 void launch_mx4_dequantize(const Mx4Args &a, bool bf16, hipStream_t s);
-void launch_f32_grouped(GroupedArgs a, bool b_contiguous, hipStream_t s);
-void launch_f32_weight_grad(GroupedArgs a, hipStream_t s);
+void launch_f32_grouped(const GroupedArgs &a, bool b_contiguous, hipStream_t s);
+void launch_f32_weight_grad(const GroupedArgs &a, hipStream_t s);
 void launch_lp256(GroupedArgs a, const LpCall &c, hipStream_t s);
 void launch_lp128(const GroupedArgs &a, const LpCall &c, hipStream_t s);
 void launch_lp128_unaligned(const GroupedArgs &a, const LpCall &c, hipStream_t s);
-// At most 16 or 32 rows a tile (row_tiles 1 or 2).
-void launch_few(const GroupedArgs &a, bool bf16, bool fp4, bool b_contiguous, int row_tiles, hipStream_t s);
+// Few rows an expert: tiles of 16 rows.
+void launch_few(const GroupedArgs &a, bool bf16, bool fp4, bool b_contiguous, int cu_count, hipStream_t s);
 void launch_route(const RouteArgs &a, bool bf16, bool grad, hipStream_t s);
 
 }  // namespace gemmf32

@@ -108,7 +108,7 @@ int expert_grouped_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t gr
     const bool copies = dtype == EXPERT_F32 || (aligned(A, 4) && aligned(B, 4) && a.lda % 4 == 0 && a.ldb % 4 == 0 &&
                                                 a.expert_stride % 4 == 0);
     if (rows <= kFewRows) {
-        launch_few(a, dtype == EXPERT_BF16, false, col, rows <= 16 ? 1 : 2, s);
+        launch_few(a, dtype == EXPERT_BF16, false, col, cus, s);
     } else if (dtype == EXPERT_F32) {
         launch_f32_grouped(a, col, s);
     } else {
@@ -252,7 +252,7 @@ int expert_mx4_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups
     const bool bf16 = dtype == EXPERT_BF16;
     const int64_t rows = mean_rows(m, groups);
     if (need == 0) {
-        launch_few(a, bf16, true, true, 1, s);
+        launch_few(a, bf16, true, true, cus, s);
         return launched();
     }
     u8 *const xc = static_cast<u8 *>(workspace), *const xs = xc + m * (kp / 2);

@@ -98,12 +98,9 @@ __global__ __launch_bounds__(T::THREADS) void f32_weight_grad_kernel(GroupedArgs
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave % T::WAVES_M, wc = wave / T::WAVES_M;
     const int l32 = lane & 31, half = lane >> 5;
-    const int per = a.tiles_m * a.tiles_n;
-    const int logical = xcd_contiguous(blockIdx.x, per * a.groups, a.num_xcd);
-    const int expert = logical / per, r = logical % per;
-    const int width = a.group_m * a.tiles_n;
-    const int first = r / width * a.group_m, size = min(a.tiles_m - first, a.group_m);
-    const int row0 = (first + r % width % size) * T::BM, col0 = r % width / size * T::BN;
+    GradTile t;
+    if (!grad_tile(a, blockIdx.x % a.num_xcd, blockIdx.x / a.num_xcd, t)) return;
+    const int expert = t.expert, row0 = t.tm * T::BM, col0 = t.tn * T::BN;
     const Rows rows = entry_rows(a, expert);
     int lo = __builtin_amdgcn_readfirstlane(rows.lo);
     const int hi = __builtin_amdgcn_readfirstlane(rows.hi);

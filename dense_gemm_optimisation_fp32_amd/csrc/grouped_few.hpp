@@ -2,11 +2,11 @@
 // by the bytes of the experts' matrices, each read once.
 //
 // A workgroup takes 16 MT rows of one expert and a strip of columns, and its
-// wavefronts split k.  B goes straight from memory into registers, 16 bytes
-// a lane, one iteration's loads ahead of the products; the products run on
-// 16-row matrix instructions whose rows past the expert's are wasted, which
-// costs nothing that the memory does not cover.  The order of k inside an
-// instruction is free as long as A and B agree, which the layouts use:
+// wavefronts split k.  A and B go straight from memory into registers, 16
+// bytes a lane, one iteration's loads ahead of the products; the products run
+// on 16-row matrix instructions whose rows past the expert's are wasted,
+// which costs nothing that the memory does not cover.  The order of k inside
+// an instruction is free as long as A and B agree, which the layouts use:
 //   k contiguous  a lane holds 16 bytes of one column: four neighbouring k
 //                 (32 bits), eight (bfloat16) or a block of 32 (4-bit).  Four
 //                 lanes share a column, so an iteration's four loads cover
@@ -16,9 +16,15 @@
 //                 columns of k-row 8 g + j, turned by one byte permute a
 //                 register into pairs along k.
 // The wavefronts' sums meet in LDS and are added in the order of k's parts:
-// the result is the same in every run.  4-bit products quantise the rows of
-// X on the way: a lane's operand is one block of 32, so the largest
-// magnitude, the scale and the codes need no other lane.
+// the result is the same in every run.
+//
+// 4-bit products quantise the rows of X on the way: the workgroup quantises
+// them, 4096 columns at a time, into LDS while its first weights are under
+// way (a thread a block of 32: the largest magnitude, the scale and the codes
+// need no other lane).
+//
+// Small calls are bound by latency: they take strips of 16 columns and eight
+// wavefronts, so that all of B is under way at once (see the launch).
 #pragma once
 
 #include "lp_gemm.hpp"
@@ -28,31 +34,38 @@ namespace gemmf32 {
 
 enum FewKind { kFewF32 = 0, kFewBf16 = 1, kFewFp4 = 2 };
 
-template <int KIND, bool B_KS, class X>
+template <int KIND, bool B_KS, class X, int MT_, int WAVES_, int NB_>
 struct FewTile {
     using E = X;                                     // elements of A and C
-    static constexpr int WAVES = 4, THREADS = WAVES * 64;
-    // Columns of a workgroup, and of the k that one wavefront's iteration covers.
-    static constexpr int NB = B_KS ? (KIND == kFewF32 ? 4 : 8) : 2;       // 16-column blocks
-    static constexpr int BN = 16 * NB;
+    static constexpr int MT = MT_, WAVES = WAVES_, THREADS = WAVES * 64;
+    // 16-column blocks of a workgroup, and the k that one wavefront's
+    // iteration covers.
+    static constexpr int NB = B_KS ? (KIND == kFewF32 ? 4 : 8) : NB_;
+    static constexpr int BM = 16 * MT, BN = 16 * NB;
     static constexpr int KI = KIND == kFewFp4 ? 512 : KIND == kFewF32 ? (B_KS ? 32 : 64) : (B_KS ? 32 : 128);
     static constexpr int LOADS = B_KS ? 8 : 4 * NB;  // 16-byte loads of B a lane and iteration
-    static constexpr int A_LOADS = KIND == kFewF32 ? KI / 16 : KI / 32;   // of A (not 4-bit)
+    static constexpr int A_LOADS = KIND == kFewFp4 ? 0 : KIND == kFewF32 ? KI / 16 : KI / 32;   // of A
+    // 4-bit: columns that LDS holds of X, bytes of a row's codes there (16
+    // more than the codes: rows on different banks).
+    static constexpr int CHUNK = 4096, CODE_ROW = CHUNK / 2 + 16;
+    static_assert(KIND != kFewFp4 || MT == 1, "4-bit: 16 rows");
 };
 
-template <class T, int KIND, bool B_KS>
+template <class T, int KIND>
 struct FewRegs {
+    i32x4 a[KIND == kFewFp4 ? 1 : T::MT * T::A_LOADS];
     i32x4 b[T::LOADS];
     int s[KIND == kFewFp4 ? T::LOADS : 1];
 };
 
-template <int KIND, bool B_KS, class X, int MT>
-__global__ __launch_bounds__(256) void few_grouped_kernel(GroupedArgs g)
+template <int KIND, bool B_KS, class T>
+__global__ __launch_bounds__(T::THREADS) void few_grouped_kernel(GroupedArgs g)
 {
-    using T = FewTile<KIND, B_KS, X>;
     using E = typename T::E;
-    constexpr int BM = 16 * MT, BN = T::BN, ROW = BN + 4;
+    constexpr int BM = T::BM, BN = T::BN, ROW = BN + 4, MT = T::MT;
     __shared__ float red[T::WAVES][BM * ROW];
+    __shared__ __align__(16) u8 codes[KIND == kFewFp4 ? 16 * T::CODE_ROW : 16];
+    __shared__ u8 scales[KIND == kFewFp4 ? 16 * (T::CHUNK / 32 + 4) : 4];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     RowTile rt;
@@ -69,6 +82,7 @@ __global__ __launch_bounds__(256) void few_grouped_kernel(GroupedArgs g)
         for (int nb = 0; nb < T::NB; ++nb) acc[mt][nb] = f32x4{};
 
     if (rt.expert >= 0) {
+        constexpr int N = 16 / sizeof(E);
         const char *const bx = g.B + rt.expert * g.expert_stride;
         const E *pa[MT];
 #pragma unroll
@@ -89,8 +103,17 @@ __global__ __launch_bounds__(256) void few_grouped_kernel(GroupedArgs g)
         }
         const int cols_left = g.n - (col0 + l16 * (KIND == kFewF32 ? 4 : 8));   // (k strided)
 
-        auto load_b = [&](int it, FewRegs<T, KIND, B_KS> &r) {
+        auto load = [&](int it, FewRegs<T, KIND> &r) {
             const int k0 = it * T::KI;
+            if constexpr (KIND != kFewFp4) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int s = 0; s < T::A_LOADS; ++s) {
+                        const int kk = k0 + (s * 4 + grp) * N;
+                        r.a[mt * T::A_LOADS + s] = load_chunk(pa[mt] + kk, g.k - kk);
+                    }
+            }
             if constexpr (B_KS) {
                 constexpr int PER = KIND == kFewF32 ? 4 : 8;
 #pragma unroll
@@ -99,7 +122,7 @@ __global__ __launch_bounds__(256) void few_grouped_kernel(GroupedArgs g)
                     const int kr = KIND == kFewF32 ? (j / 4) * 16 + j % 4 : j;
                     const int kk = k0 + kr + grp * PER;
                     r.b[j] = load_chunk(reinterpret_cast<const E *>(pb[0] + (long long)(k0 + kr) * g.ldb),
-                                      kk < g.k ? cols_left : 0);
+                                        kk < g.k ? cols_left : 0);
                 }
             } else if constexpr (KIND == kFewFp4) {
 #pragma unroll
@@ -107,15 +130,11 @@ __global__ __launch_bounds__(256) void few_grouped_kernel(GroupedArgs g)
                     const int kb = min(it * 4 + s, blocks - 1);
 #pragma unroll
                     for (int nb = 0; nb < T::NB; ++nb) {
-                        struct __attribute__((packed, aligned(1))) Chunk {
-                            i32x4 v;
-                        };
-                        r.b[s * T::NB + nb] = reinterpret_cast<const Chunk *>(pb[nb] + (long long)kb * 64)->v;
+                        r.b[s * T::NB + nb] = *reinterpret_cast<const i32x4 *>(pb[nb] + (long long)kb * 64);
                         r.s[s * T::NB + nb] = sb[((long long)kb * g.n + min(col0 + nb * 16 + l16, g.n - 1)) * 4];
                     }
                 }
             } else {
-                constexpr int N = 16 / sizeof(E);
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const int kk = k0 + (s * 4 + grp) * N;
@@ -126,36 +145,22 @@ __global__ __launch_bounds__(256) void few_grouped_kernel(GroupedArgs g)
                 }
             }
         };
-        auto multiply = [&](int it, const FewRegs<T, KIND, B_KS> &r) {
-            const int k0 = it * T::KI;
+        auto multiply = [&](int it, const FewRegs<T, KIND> &r) {
             if constexpr (KIND == kFewFp4) {
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const int kb = it * 4 + s;
                     if (kb >= blocks) break;
+                    const int in = kb % (T::CHUNK / 128), row = min(l16, rows - 1);
+                    const i32x4 c = *reinterpret_cast<const i32x4 *>(codes + row * T::CODE_ROW + in * 64 + grp * 16);
+                    const int byte = scales[row * (T::CHUNK / 32 + 4) + in * 4 + grp];
+                    const i32x8 a = {c[0], c[1], c[2], c[3], 0, 0, 0, 0};
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const int k = kb * 128 + grp * 32;
-                        float v[4][8];
-                        unsigned largest = 0;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            load8(pa[mt] + k + 8 * i, g.k - k - 8 * i, v[i]);
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) largest = max(largest, magnitude(v[i][c]));
-                        }
-                        const MxBlock m = mx_block(largest);
-                        i32x8 a = {};
-                        if (m.byte != 255)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) a[i] = (int)mx_codes(v[i], m.factor);
-#pragma unroll
-                        for (int nb = 0; nb < T::NB; ++nb) {
-                            const i32x4 w = r.b[s * T::NB + nb];
-                            const i32x8 b = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
-                            acc[mt][nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                b, a, acc[mt][nb], 4, 4, 0, r.s[s * T::NB + nb], 0, (int)m.byte);
-                        }
+                    for (int nb = 0; nb < T::NB; ++nb) {
+                        const i32x4 w = r.b[s * T::NB + nb];
+                        const i32x8 b = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+                        acc[0][nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc[0][nb], 4, 4, 0,
+                                                                                      r.s[s * T::NB + nb], 0, byte);
                     }
                 }
             } else {
@@ -163,9 +168,7 @@ __global__ __launch_bounds__(256) void few_grouped_kernel(GroupedArgs g)
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int s = 0; s < T::A_LOADS; ++s) {
-                        constexpr int N = 16 / sizeof(E);
-                        const int kk = k0 + (s * 4 + grp) * N;
-                        const i32x4 a = load_chunk(pa[mt] + kk, g.k - kk);
+                        const i32x4 a = r.a[mt * T::A_LOADS + s];
                         if constexpr (KIND == kFewF32) {
                             const f32x4 af = __builtin_bit_cast(f32x4, a);
                             if constexpr (B_KS) {
@@ -208,21 +211,56 @@ __global__ __launch_bounds__(256) void few_grouped_kernel(GroupedArgs g)
                     }
             }
         };
+        // 4-bit: X's columns [c0, c0 + CHUNK), a thread a block of 32.
+        auto quantise = [&](int c0) {
+            const int per_row = min(T::CHUNK, blocks * 128 - c0) / 32;
+            for (int u = tid; u < rows * per_row; u += T::THREADS) {
+                const int row = u / per_row, blk = u % per_row, k = c0 + blk * 32;
+                const E *const p = reinterpret_cast<const E *>(g.A + (rt.row + row) * g.lda) + k;
+                float v[4][8];
+                unsigned largest = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    load8(p + 8 * i, g.k - k - 8 * i, v[i]);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) largest = max(largest, magnitude(v[i][c]));
+                }
+                const MxBlock m = mx_block(largest);
+                i32x4 a = {};
+                if (m.byte != 255)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a[i] = (int)mx_codes(v[i], m.factor);
+                *reinterpret_cast<i32x4 *>(codes + row * T::CODE_ROW + blk * 16) = a;
+                scales[row * (T::CHUNK / 32 + 4) + blk] = (u8)m.byte;
+            }
+        };
 
         const int its = KIND == kFewFp4 ? (blocks + 3) / 4 : (g.k + T::KI - 1) / T::KI;
-        if (wave < its) {
-            FewRegs<T, KIND, B_KS> r[2];
-            load_b(wave, r[0]);
-            int it = wave;
-            while (true) {
-                if (it + T::WAVES < its) load_b(it + T::WAVES, r[1]);
+        constexpr int CHUNK_ITS = T::CHUNK / T::KI;
+        static_assert(KIND != kFewFp4 || CHUNK_ITS % T::WAVES == 0, "a chunk is whole rounds of the wavefronts");
+        FewRegs<T, KIND> r[2];
+        if (wave < its) load(wave, r[0]);
+        // Every wavefront comes to each chunk's barriers, with work or without.
+        for (int first = 0; first < its; first += KIND == kFewFp4 ? CHUNK_ITS : its) {
+            const int last = KIND == kFewFp4 ? min(first + CHUNK_ITS, its) : its;
+            if constexpr (KIND == kFewFp4) {
+                if (first) __syncthreads();
+                quantise(first * T::KI);
+                __syncthreads();
+            }
+            int it = first + wave;
+            while (it < last) {
+                if (it + T::WAVES < its) load(it + T::WAVES, r[1]);
                 multiply(it, r[0]);
                 it += T::WAVES;
-                if (it >= its) break;
-                if (it + T::WAVES < its) load_b(it + T::WAVES, r[0]);
+                if (KIND == kFewFp4 || it >= last) {
+                    // (4-bit: a chunk may end after an odd number of rounds.)
+                    if constexpr (KIND == kFewFp4) r[0] = r[1];
+                    continue;
+                }
+                if (it + T::WAVES < its) load(it + T::WAVES, r[0]);
                 multiply(it, r[1]);
                 it += T::WAVES;
-                if (it >= its) break;
             }
         }
     }

@@ -6,35 +6,38 @@ namespace gemmf32 {
 
 namespace {
 
-template <int KIND, bool B_KS, class X, int MT>
-void launch_mt(GroupedArgs a, hipStream_t s)
+template <int KIND, bool B_KS, class T>
+void launch_tile(GroupedArgs a, hipStream_t s)
 {
-    using T = FewTile<KIND, B_KS, X>;
-    a.tiles_m = grouped_row_tiles(a, 16 * MT);
+    a.tiles_m = grouped_row_tiles(a, T::BM);
     a.tiles_n = (a.n + T::BN - 1) / T::BN;
-    few_grouped_kernel<KIND, B_KS, X, MT><<<(unsigned)a.tiles_m * a.tiles_n, T::THREADS, 0, s>>>(a);
+    few_grouped_kernel<KIND, B_KS, T><<<(unsigned)a.tiles_m * a.tiles_n, T::THREADS, 0, s>>>(a);
 }
 
 template <int KIND, bool B_KS, class X>
-void launch_kind(const GroupedArgs &a, int row_tiles, hipStream_t s)
+void launch_kind(const GroupedArgs &a, int cu_count, hipStream_t s)
 {
-    if (row_tiles <= 1) launch_mt<KIND, B_KS, X, 1>(a, s);
-    else launch_mt<KIND, B_KS, X, 2>(a, s);
+    using Large = FewTile<KIND, B_KS, X, 1, 4, 2>;
+    using Small = FewTile<KIND, B_KS, X, 1, 8, 1>;
+    // Row tiles that there are at least, for one a used expert.
+    const long long rows = (a.m + 15) / 16, used = rows > a.groups ? rows : a.m < a.groups ? a.m : a.groups;
+    if (used * ((a.n + Large::BN - 1) / Large::BN) < 4ll * cu_count) launch_tile<KIND, B_KS, Small>(a, s);
+    else launch_tile<KIND, B_KS, Large>(a, s);
 }
 
 }  // namespace
 
-void launch_few(const GroupedArgs &a, bool bf16, bool fp4, bool b_contiguous, int row_tiles, hipStream_t s)
+void launch_few(const GroupedArgs &a, bool bf16, bool fp4, bool b_contiguous, int cu_count, hipStream_t s)
 {
     if (fp4) {
-        if (bf16) launch_kind<kFewFp4, false, __bf16>(a, row_tiles, s);
-        else launch_kind<kFewFp4, false, float>(a, row_tiles, s);
+        if (bf16) launch_kind<kFewFp4, false, __bf16>(a, cu_count, s);
+        else launch_kind<kFewFp4, false, float>(a, cu_count, s);
     } else if (b_contiguous) {
-        if (bf16) launch_kind<kFewBf16, false, __bf16>(a, row_tiles, s);
-        else launch_kind<kFewF32, false, float>(a, row_tiles, s);
+        if (bf16) launch_kind<kFewBf16, false, __bf16>(a, cu_count, s);
+        else launch_kind<kFewF32, false, float>(a, cu_count, s);
     } else {
-        if (bf16) launch_kind<kFewBf16, true, __bf16>(a, row_tiles, s);
-        else launch_kind<kFewF32, true, float>(a, row_tiles, s);
+        if (bf16) launch_kind<kFewBf16, true, __bf16>(a, cu_count, s);
+        else launch_kind<kFewF32, true, float>(a, cu_count, s);
     }
 }
 

@@ -22,7 +22,7 @@ void launch_lp256(GroupedArgs a, const LpCall &c, hipStream_t s)
     a.tiles_m = c.weight_grad ? (a.k + Tile::BM - 1) / Tile::BM : grouped_row_tiles(a, Tile::BM);
     a.tiles_n = (a.n + Tile::BN - 1) / Tile::BN;
     // A workgroup a CU, as many on each XCD.
-    const long long tiles = (long long)a.tiles_m * a.tiles_n * (c.weight_grad ? a.groups : 1);
+    const long long tiles = c.weight_grad ? grad_workgroups(a) : (long long)a.tiles_m * a.tiles_n;
     const long long most = c.cu_count / a.num_xcd * a.num_xcd;
     const unsigned grid = (unsigned)(tiles < most ? (tiles + a.num_xcd - 1) / a.num_xcd * a.num_xcd : most);
     if (c.weight_grad) launch_pipe<kBf16, true, true, __bf16>(a, c.wide, grid, s);

@@ -7,21 +7,29 @@ namespace gemmf32 {
 __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a)
 {
     extern __shared__ int lds[];
-    int *const base = lds, *const held = lds + a.groups, *const carry = lds + 5 * a.groups;
+    int *const base = lds, *const carry = lds + a.groups, *const held = lds + (a.groups + 2) / 2 * 2;
     int *const totals = held;   // until the places are counted
     const int parts = gridDim.x;
-    // Threads share an expert where there are more threads than experts:
-    // part p adds up every (threads / experts)-th workgroup's counts.
+    // Threads share an expert where there are more threads than experts, each
+    // every share-th workgroup's counts, eight loads at a time.
     const int share = max(1, kRouteThreads / a.groups);
     for (int e = threadIdx.x; e < a.groups; e += kRouteThreads) base[e] = totals[e] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < a.groups * share; i += kRouteThreads) {
         const int e = i % a.groups;
         int before = 0, all = 0;
-        for (int b = i / a.groups; b < parts; b += share) {
-            const int n = a.counts[(long long)b * a.groups + e];
-            all += n;
-            before += b < (int)blockIdx.x ? n : 0;
+        for (int b0 = i / a.groups; b0 < parts; b0 += 8 * share) {
+            int n[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int b = b0 + u * share;
+                n[u] = b < parts ? a.counts[(long long)b * a.groups + e] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                all += n[u];
+                before += b0 + u * share < (int)blockIdx.x ? n[u] : 0;
+            }
         }
         atomicAdd(base + e, before);
         atomicAdd(totals + e, all);
@@ -30,7 +38,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a)
     route_offsets(a, totals, carry, blockIdx.x == gridDim.x - 1);
     for (int e = threadIdx.x; e < a.groups; e += kRouteThreads) base[e] += totals[e];
     __syncthreads();
-    route_place(a, blockIdx.x * kRouteTokens, base, held);
+    if (a.groups <= 512) route_place<kRouteWaves>(a, blockIdx.x * kRouteTokens, base, held);
+    else route_place<kRouteFewWaves>(a, blockIdx.x * kRouteTokens, base, held);
 }
 
 namespace {
@@ -38,15 +47,15 @@ namespace {
 template <class E, int V>
 void launch_v(const RouteArgs &a, bool grad, hipStream_t s)
 {
-    const int lds = route_lds_words(a.groups) * 4;
+    const int found = route_found_words(a.choices), place = route_place_words(a.groups);
     if (grad) {
-        route_grad_kernel<E, V><<<(a.tokens + 15) / 16, kRouteThreads, 0, s>>>(a);
+        route_grad_kernel<E, V><<<(a.tokens + 15) / 16, kGradThreads, 0, s>>>(a);
     } else if (a.tokens <= kRouteTokens) {
-        route_one_kernel<E, V><<<1, kRouteThreads, lds, s>>>(a);
+        route_one_kernel<E, V><<<1, kRouteThreads, (a.groups + 2 + (found > place ? found : place)) * 4, s>>>(a);
     } else {
         const int parts = (a.tokens + kRouteTokens - 1) / kRouteTokens;
-        route_choose_kernel<E, V><<<parts, kRouteThreads, a.groups * 4, s>>>(a);
-        route_place_kernel<<<parts, kRouteThreads, lds, s>>>(a);
+        route_choose_kernel<E, V><<<parts, kRouteThreads, (a.groups + 1 + found) * 4, s>>>(a);
+        route_place_kernel<<<parts, kRouteThreads, (a.groups + 2 + place) * 4, s>>>(a);
     }
 }
 

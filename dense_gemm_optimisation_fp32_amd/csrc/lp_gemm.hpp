@@ -665,16 +665,11 @@ __global__ __launch_bounds__(T::THREADS) void lp_weight_grad_kernel(GroupedArgs 
     __shared__ i32x4 lds[T::STAGES * T::stage_chunks(kBf16)];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int per = g.tiles_m * g.tiles_n;
-    const int logical = xcd_contiguous(blockIdx.x, per * g.groups, g.num_xcd);
-    const int expert = logical / per;
-    const int r = logical % per;
-    const int width = g.group_m * g.tiles_n;
-    const int first = r / width * g.group_m, size = min(g.tiles_m - first, g.group_m);
-    const Rows rows = entry_rows(g, expert);
-    lp_grad_tile<T, WIDE, REG>(g, lds, tid, lane, wave, expert, __builtin_amdgcn_readfirstlane(rows.lo),
-                               __builtin_amdgcn_readfirstlane(rows.hi), (first + r % width % size) * T::BM,
-                               r % width / size * T::BN);
+    GradTile t;
+    if (!grad_tile(g, blockIdx.x % g.num_xcd, blockIdx.x / g.num_xcd, t)) return;
+    const Rows rows = entry_rows(g, t.expert);
+    lp_grad_tile<T, WIDE, REG>(g, lds, tid, lane, wave, t.expert, __builtin_amdgcn_readfirstlane(rows.lo),
+                               __builtin_amdgcn_readfirstlane(rows.hi), t.tm * T::BM, t.tn * T::BN);
 }
 
 }  // namespace gemmf32

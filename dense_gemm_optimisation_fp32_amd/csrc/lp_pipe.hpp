@@ -97,18 +97,17 @@ struct LpPipe {
 
     // --- the sequence of tiles -------------------------------------------------
 
-    // Tile number `logical` of all.
+    // Tile number `logical` of all (weight gradient: of this XCD's; expert -1: none).
     __device__ __forceinline__ LpJob job(int logical) const
     {
         LpJob j;
         int tm;
         if constexpr (GRAD) {
-            const int per = g.tiles_m * g.tiles_n, r = logical % per;
-            j.expert = logical / per;
-            const int width = g.group_m * g.tiles_n, first = r / width * g.group_m;
-            const int size = min(g.tiles_m - first, g.group_m);
-            tm = first + r % width % size;
-            j.col = r % width / size * T::BN;
+            GradTile t;
+            if (!grad_tile(g, blockIdx.x % g.num_xcd, logical, t)) return LpJob{-1, 0, 0, 0, 0};
+            j.expert = t.expert;
+            tm = t.tm;
+            j.col = t.tn * T::BN;
             const Rows rows = entry_rows(g, j.expert);
             j.row = __builtin_amdgcn_readfirstlane(rows.lo);
             j.k = __builtin_amdgcn_readfirstlane(rows.hi) - j.row;
@@ -325,13 +324,14 @@ struct LpPipe {
         // (workgroups go to the XCDs in turn), an XCD's workgroups take its
         // tiles in turn.
         const int x = blockIdx.x % g.num_xcd, per = total / g.num_xcd, rem = total % g.num_xcd;
-        const int first = x * per + min(x, rem) + (int)(blockIdx.x / g.num_xcd);
-        tile_end = (x + 1) * per + min(x + 1, rem);
+        const int begin = GRAD ? 0 : x * per + min(x, rem);
+        const int first = begin + (int)(blockIdx.x / g.num_xcd);
+        tile_end = GRAD ? total : (x + 1) * per + min(x + 1, rem);
         tile_step = gridDim.x / g.num_xcd;
         next_tile = first;
         // A last round that would leave half the XCD's workgroups without a
         // tile is split: halves of 128 x 256 or quarters of 128 x 128.
-        const int tiles = tile_end - (x * per + min(x, rem)), last = tiles % tile_step;
+        const int last = (tile_end - begin) % tile_step;
         const int parts = 4 * last <= tile_step ? 4 : 2 * last <= tile_step ? 2 : 0;
         if (parts) tile_end -= last;
         if (first < tile_end) whole_tiles(first);
@@ -358,7 +358,7 @@ struct LpPipe {
         static_assert(T2::THREADS == T::THREADS && T2::STAGES * T2::stage_chunks(KIND) <= S * STAGE, "the same workgroup");
         if (j.col >= g.n) return;
         if constexpr (GRAD) {
-            if (j.rows + down >= g.k) return;
+            if (j.expert < 0 || j.rows + down >= g.k) return;
             lp_grad_tile<T2, WIDE>(g, lds, tid, lane, wave, j.expert, j.row, j.row + j.k, j.rows + down, j.col);
         } else {
             if (down >= j.rows) return;
@@ -424,6 +424,7 @@ struct LpPipe {
             int lane_e = lane;
             asm volatile("" : "+v"(lane_e));
             if constexpr (GRAD) {
+                if (j.expert < 0) continue;
                 char *const out = g.C + j.expert * g.expert_stride + j.rows * g.ldc + (long long)j.col * 2;
                 lp_store<T, E, WIDE>(out, g.ldc, g.k - j.rows, g.n - j.col, nullptr, 0, wr, wc, lane_e, acc);
             } else {
@@ -449,13 +450,13 @@ __global__ __launch_bounds__(T::THREADS) void lp_pipe_kernel(GroupedArgs g)
     int total;
     int *const table = reinterpret_cast<int *>(lds + T::STAGES * T::stage_chunks(KIND));
     if constexpr (GRAD) {
-        total = g.tiles_m * g.tiles_n * g.groups;
+        total = grad_share(g) * g.groups;        // of an XCD
     } else {
         // Every wavefront sums the row tiles for itself and writes the same table.
         int sum = 0;
         for (int b = 0; b < entries; b += 64) {
             const Rows rows = entry_rows(g, b + lane);
-            const int s = sum + wave_inclusive_sum((rows.hi - rows.lo + T::BM - 1) / T::BM, lane);
+            const int s = sum + wave_inclusive_sum((rows.hi - rows.lo + T::BM - 1) / T::BM);
             if (b + lane < entries) {
                 table[b + lane] = s;
                 table[entries + b + lane] = rows.lo;

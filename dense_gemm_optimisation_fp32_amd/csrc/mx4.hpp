@@ -77,6 +77,14 @@ __device__ __forceinline__ void load8(const E *p, int left, float (&v)[8])
     }
 }
 
+// x of another lane: CTRL 0xb1 and 0x4e the neighbour and the other pair of
+// four, 0x124 and 0x128 four and eight places on in the row of 16.
+template <int CTRL>
+__device__ __forceinline__ unsigned mx_lane(unsigned x)
+{
+    return (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true);
+}
+
 // Rows contiguous along k: four lanes hold a block, eight values each, and
 // sixteen lanes the four blocks of a scale word.
 template <class E>
@@ -84,22 +92,22 @@ __global__ __launch_bounds__(256) void mx4_quantize_rows_kernel(Mx4Args a)
 {
     const int lane = threadIdx.x & 63;
     const int segments = (a.kp + 511) / 512;              // 512 columns a wavefront
-    const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const long long row = unit / segments;
+    const unsigned unit = blockIdx.x * 4 + (threadIdx.x >> 6);      // (fits: the host checks)
+    const long long row = unit / (unsigned)segments;
     if (row >= a.rows) return;
-    const int col = (int)(unit % segments) * 512 + lane * 8;
+    const int col = (int)(unit % (unsigned)segments) * 512 + lane * 8;
     float v[8] = {};
     if (col < a.k) load8(reinterpret_cast<const E *>(a.x) + row * a.ld + col, a.k - col, v);
     unsigned largest = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) largest = max(largest, magnitude(v[i]));
-    largest = max(largest, (unsigned)__shfl_xor((int)largest, 1));
-    largest = max(largest, (unsigned)__shfl_xor((int)largest, 2));
+    largest = max(largest, mx_lane<0xb1>(largest));
+    largest = max(largest, mx_lane<0x4e>(largest));
     const MxBlock b = mx_block(largest);
     const unsigned codes = b.byte == 255 ? 0u : mx_codes(v, b.factor);
     unsigned word = b.byte << (8 * ((lane >> 2) & 3));
-    word |= (unsigned)__shfl_xor((int)word, 4);
-    word |= (unsigned)__shfl_xor((int)word, 8);
+    word |= mx_lane<0x128>(word);
+    word |= mx_lane<0x124>(word);
     if (col < a.kp) {
         *reinterpret_cast<unsigned *>(a.codes + row * (a.kp / 2) + col / 2) = codes;
         if ((lane & 15) == 0)
@@ -135,38 +143,53 @@ __global__ __launch_bounds__(256) void mx4_quantize_columns_kernel(Mx4Args a)
     a.scales[((long long)kb * a.rows + row) * 4 + wave] = (u8)b.byte;
 }
 
-// Codes and scales back to values: eight columns a lane.  The scale byte 0
-// is 2^-127, below the normal numbers: set by its mantissa bit.
+// Codes and scales back to values: 16 bytes of them a lane and store, so that
+// a wavefront's store is one run (32 bits: two runs of 256 columns; with eight
+// neighbouring columns a lane the stores had gaps, 79 us at 8192 x 7168).  The
+// scale byte 0 is 2^-127, below the normal numbers: set by its mantissa bit.
 template <class E>
 __global__ __launch_bounds__(256) void mx4_dequantize_kernel(Mx4Args a)
 {
+    constexpr int N = 16 / sizeof(E), RUNS = 8 / N;
     const int lane = threadIdx.x & 63;
     const int segments = (a.k + 511) / 512;
-    const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const long long row = unit / segments;
+    const unsigned unit = blockIdx.x * 4 + (threadIdx.x >> 6);
+    const long long row = unit / (unsigned)segments;
     if (row >= a.rows) return;
-    const int col = (int)(unit % segments) * 512 + lane * 8;
-    if (col >= a.k) return;
-    const unsigned codes = *reinterpret_cast<const unsigned *>(a.codes + row * (a.kp / 2) + col / 2);
-    const unsigned byte = a.scales[((long long)(col / 128) * a.rows + row) * 4 + ((col >> 5) & 3)];
-    const float scale = byte == 255 ? __builtin_nanf("") : __uint_as_float(byte ? byte << 23 : 0x00400000u);
-    struct __attribute__((packed, aligned(sizeof(E)))) Eight {
-        E e[8];
-    } t;
-    const f32x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0);
-    const f32x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1);
-    const f32x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2);
-    const f32x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
-    // A code times a power of two is exact in 32 and in 16 bits.
-    t.e[0] = (E)(v0.x * scale), t.e[1] = (E)(v0.y * scale), t.e[2] = (E)(v1.x * scale), t.e[3] = (E)(v1.y * scale);
-    t.e[4] = (E)(v2.x * scale), t.e[5] = (E)(v2.y * scale), t.e[6] = (E)(v3.x * scale), t.e[7] = (E)(v3.y * scale);
-    E *p = reinterpret_cast<E *>(const_cast<char *>(a.x)) + row * a.ld + col;
-    if (col + 8 <= a.k) {
-        *reinterpret_cast<Eight *>(p) = t;
-    } else {
+    struct __attribute__((packed, aligned(sizeof(E)))) Run {
+        E e[N];
+    } t[RUNS];
+    int col[RUNS];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i < a.k) p[i] = t.e[i];
+    for (int q = 0; q < RUNS; ++q) {
+        col[q] = (int)(unit % (unsigned)segments) * 512 + q * 64 * N + lane * N;
+        if (col[q] >= a.k) continue;
+        const u8 *const p = a.codes + row * (a.kp / 2) + col[q] / 2;
+        const unsigned codes = N == 8 ? *reinterpret_cast<const unsigned *>(p) : *reinterpret_cast<const unsigned short *>(p);
+        const unsigned byte = a.scales[((long long)(col[q] / 128) * a.rows + row) * 4 + ((col[q] >> 5) & 3)];
+        const float scale = byte == 255 ? __builtin_nanf("") : __uint_as_float(byte ? byte << 23 : 0x00400000u);
+        // A code times a power of two is exact in 32 and in 16 bits.
+        const f32x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0);
+        const f32x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1);
+        t[q].e[0] = (E)(v0.x * scale), t[q].e[1] = (E)(v0.y * scale);
+        t[q].e[2] = (E)(v1.x * scale), t[q].e[3] = (E)(v1.y * scale);
+        if constexpr (N == 8) {
+            const f32x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2);
+            const f32x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
+            t[q].e[4] = (E)(v2.x * scale), t[q].e[5] = (E)(v2.y * scale);
+            t[q].e[6] = (E)(v3.x * scale), t[q].e[7] = (E)(v3.y * scale);
+        }
+    }
+    E *const out = reinterpret_cast<E *>(const_cast<char *>(a.x)) + row * a.ld;
+#pragma unroll
+    for (int q = 0; q < RUNS; ++q) {
+        if (col[q] + N <= a.k) {
+            *reinterpret_cast<Run *>(out + col[q]) = t[q];
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (col[q] + i < a.k) out[col[q] + i] = t[q].e[i];
+        }
     }
 }
 

@@ -13,14 +13,23 @@
 //            softmax sums over, g the slots' gradients at the chosen ones.
 //
 // A token is held by 16 lanes, each V neighbouring experts: four tokens a
-// wavefront, and a choice costs V + 4 maxima, a ballot and V compares.  The
-// lanes hold the experts in order, so the lowest lane with the largest value
-// holds the lowest expert.  The sort is a counting sort in two launches (one
-// where a single workgroup holds every token): workgroups of kRouteTokens
-// tokens count their experts; then each workgroup adds up the counts of
-// the workgroups before it (a few KiB from the L2 cache each) and places its
-// own slots, 64 at a time, by the lanes that hold the same expert.  No
-// atomics on memory: the order is the same in every run.
+// wavefront.  A choice is V compares, four maxima over the lanes (row
+// rotations, no LDS), a ballot and V compares to strike the chosen one out.
+// The lanes hold the experts in order, so the lowest lane with the largest
+// value holds the lowest expert.  The chosen ones go to LDS, and the softmax is
+// taken once, a lane a slot.
+//
+// The sort is a counting sort in two launches (one where a single workgroup
+// holds every token): workgroups of kRouteTokens tokens count their experts;
+// then each workgroup adds up the counts of the workgroups before it (from
+// the L2 cache) and places its own slots, 64 at a time, by the lanes that hold
+// the same expert.  No atomics on memory: the order is the same in every run.
+//
+// Bound by latency: 16 wavefronts a workgroup, so that the loads and the
+// chains of dependent operations of many tokens overlap.  32768 tokens, 128
+// experts, 8 choices, bfloat16 (us, choose + place): 4 wavefronts a workgroup
+// and the lanes' values exchanged through LDS 33 + 37, as it stands see the
+// launch.
 #pragma once
 
 #include "mx4.hpp"
@@ -28,7 +37,9 @@
 namespace gemmf32 {
 
 constexpr int kRouteTokens = 128;      // tokens of a workgroup
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 1024;
+constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr int kRouteFewWaves = 4;      // of them place, where the counts of all would not fit LDS
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxChoices = 32;
 
@@ -47,20 +58,35 @@ struct RouteArgs {
     long long ldd;
 };
 
+// x from the lane N places on in the row of 16.
 template <int N>
-__device__ __forceinline__ float row_max(float x)
+__device__ __forceinline__ float row_rotate(float x)
 {
-#pragma unroll
-    for (int d = 1; d < N; d <<= 1) x = fmaxf(x, __shfl_xor(x, d));
-    return x;
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + N, 0xf, 0xf, true));
 }
 
-template <int N>
+__device__ __forceinline__ float row_max(float x)
+{
+    x = fmaxf(x, row_rotate<8>(x));
+    x = fmaxf(x, row_rotate<4>(x));
+    x = fmaxf(x, row_rotate<2>(x));
+    return fmaxf(x, row_rotate<1>(x));
+}
+
 __device__ __forceinline__ float row_sum(float x)
 {
-#pragma unroll
-    for (int d = 1; d < N; d <<= 1) x += __shfl_xor(x, d);
-    return x;
+    x += row_rotate<8>(x);
+    x += row_rotate<4>(x);
+    x += row_rotate<2>(x);
+    return x + row_rotate<1>(x);
+}
+
+// LDS written by a lane is read by another one of the same wavefront.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // The V logits of a lane; absent experts, and NaN, are -inf.
@@ -86,20 +112,26 @@ __device__ __forceinline__ void route_load(const RouteArgs &a, int token, int su
     }
 }
 
-// Chooses for the workgroup's tokens and counts the experts in LDS.
+// What a choice found: the logit, and its expert or -1.
+struct Choice {
+    float logit;
+    int expert;
+};
+
+// Chooses for the workgroup's tokens and counts the experts in LDS.  `found`
+// (LDS): `choices` entries for every 16 lanes.
 template <class E, int V>
-__device__ __forceinline__ void route_choose(const RouteArgs &a, int first, int *counts)
+__device__ __forceinline__ void route_choose(const RouteArgs &a, int first, int *counts, Choice *found)
 {
     const int lane = threadIdx.x & 63, sub = lane & 15, group = lane >> 4;
     const int last = min(first + kRouteTokens, a.tokens);
+    Choice *const mine = found + (threadIdx.x >> 4) * a.choices;
     for (int t0 = first + (threadIdx.x >> 6) * 4; t0 < last; t0 += kRouteThreads / 16) {
         const int token = t0 + group;
         const bool live = token < last;
         float x[V];
         route_load<E, V>(a, live ? token : last - 1, sub, x);
-        float all = 0.0f, top = 0.0f, mine = 0.0f;
-        float sum = 0.0f, w_mine[2] = {};
-        int e_mine[2] = {-1, -1};
+        float all = 0.0f, top = 0.0f;
         for (int j = 0; j < a.choices; ++j) {
             float best = x[0];
             int at = 0;
@@ -109,57 +141,63 @@ __device__ __forceinline__ void route_choose(const RouteArgs &a, int first, int 
                 best = more ? x[i] : best;
                 at = more ? i : at;
             }
-            const float m = row_max<16>(best);
+            const float m = row_max(best);
             const bool used = m > -__builtin_inff();
             if (j == 0) {
                 top = used ? m : 0.0f;
                 if (!a.normalize) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) all += expf(x[i] - top);
-                    all = row_sum<16>(all);
+                    all = row_sum(all);
                 }
             }
             const unsigned long long hit = __ballot(best == m);
             const int who = __builtin_ctz((unsigned)(hit >> (16 * group)) & 0xffffu);
-            const int expert = __shfl(sub * V + at, group * 16 + who);
-            mine = used ? expf(m - top) : 0.0f;
-            sum += mine;
-            if (sub == (j & 15)) {
-                w_mine[j >> 4] = mine;
-                e_mine[j >> 4] = used ? expert : -1;
-            }
             if (sub == who) {
+                mine[j] = Choice{m, used ? sub * V + at : -1};
 #pragma unroll
                 for (int i = 0; i < V; ++i)
                     if (i == at) x[i] = -__builtin_inff();
             }
         }
-        const float total = a.normalize ? sum : all;
-        if (live)
+        wave_sync();
+        // A lane a slot (two past sixteen choices).
+        float w[2] = {};
+        int e[2] = {-1, -1};
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int j = sub + 16 * q;
-                if (j < a.choices) {
-                    const long long s = (long long)token * a.choices + j;
-                    a.weights[s] = e_mine[q] < 0 ? 0.0f : w_mine[q] / total;
-                    a.experts[s] = e_mine[q];
-                    if (e_mine[q] >= 0) atomicAdd(counts + e_mine[q], 1);
-                }
+        for (int q = 0; q < 2; ++q)
+            if (sub + 16 * q < a.choices) {
+                const Choice c = mine[sub + 16 * q];
+                e[q] = c.expert;
+                w[q] = c.expert < 0 ? 0.0f : expf(c.logit - top);
             }
+        const float total = a.normalize ? row_sum(w[0] + w[1]) : all;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int j = sub + 16 * q;
+            if (live && j < a.choices) {
+                const long long s = (long long)token * a.choices + j;
+                a.weights[s] = e[q] < 0 ? 0.0f : w[q] / total;
+                a.experts[s] = e[q];
+                if (e[q] >= 0) atomicAdd(counts + e[q], 1);
+            }
+        }
+        wave_sync();
     }
 }
 
 // Places the workgroup's slots.  `base` (LDS): where its slots of each
-// expert begin; `held` (LDS): the wavefronts' own counts.
+// expert begin; `held` (LDS): the wavefronts' own counts.  W wavefronts place.
+template <int W>
 __device__ __forceinline__ void route_place(const RouteArgs &a, int first, int *base, int *held)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = a.choices, last = min(first + kRouteTokens, a.tokens);
-    constexpr int kPart = kRouteTokens / 4;
-    // A wavefront's slots, in order: those of a quarter of the tokens.
-    const int s0 = min(first + wave * kPart, last) * c, s1 = min(first + (wave + 1) * kPart, last) * c;
-    int *mine = held + wave * a.groups;
-    for (int e = threadIdx.x; e < 4 * a.groups; e += kRouteThreads) held[e] = 0;
+    constexpr int kPart = kRouteTokens / W;
+    // A wavefront's slots, in order: those of its part of the tokens.
+    const int s0 = min(first + wave * kPart, last) * c, s1 = wave < W ? min(first + (wave + 1) * kPart, last) * c : s0;
+    int *const mine = held + (wave < W ? wave : 0) * a.groups;
+    for (int e = threadIdx.x; e < W * a.groups; e += kRouteThreads) held[e] = 0;
     __syncthreads();
     for (int s = s0 + lane; s < s1; s += 64) {
         const int e = a.experts[s];
@@ -168,7 +206,8 @@ __device__ __forceinline__ void route_place(const RouteArgs &a, int first, int *
     __syncthreads();
     for (int e = threadIdx.x; e < a.groups; e += kRouteThreads) {
         int at = base[e];
-        for (int w = 0; w < 4; ++w) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
             const int n = held[w * a.groups + e];
             held[w * a.groups + e] = at;
             at += n;
@@ -187,17 +226,20 @@ __device__ __forceinline__ void route_place(const RouteArgs &a, int first, int *
         const int before = __popcll(same & ((1ull << lane) - 1));
         int at = 0;
         if (e >= 0) at = mine[e] + before;
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         if (e >= 0) {
             a.order[at] = slot;
             if (before == 0) mine[e] = at + __popcll(same);
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
     }
 }
 
-// LDS words of the kernels below, for `groups` experts.
-constexpr int route_lds_words(int groups) { return 5 * groups + 64; }
+// LDS words of the kernels below: a count an expert, the placing wavefronts'
+// counts, or the choices found, and one more word.
+constexpr int route_waves(int groups) { return groups <= 512 ? kRouteWaves : kRouteFewWaves; }
+constexpr int route_found_words(int choices) { return kRouteThreads / 16 * choices * 2; }
+constexpr int route_place_words(int groups) { return route_waves(groups) * groups; }
 
 // Exclusive sum over the experts of `totals` (LDS), into offsets, and -1 in
 // the places that no slot takes (in the last workgroup).
@@ -209,7 +251,7 @@ __device__ __forceinline__ void route_offsets(const RouteArgs &a, int *totals, i
         int run = 0;
         for (int b = 0; b < a.groups; b += 64) {
             const int n = b + lane < a.groups ? totals[b + lane] : 0;
-            const int s = wave_inclusive_sum(n, lane);
+            const int s = wave_inclusive_sum(n);
             if (b + lane < a.groups) {
                 totals[b + lane] = run + s - n;
                 if (write) a.offsets[b + lane] = run + s - n;
@@ -231,15 +273,16 @@ template <class E, int V>
 __global__ __launch_bounds__(kRouteThreads) void route_one_kernel(RouteArgs a)
 {
     extern __shared__ int lds[];
-    int *const base = lds, *const held = lds + a.groups, *const carry = lds + 5 * a.groups;
+    int *const base = lds, *const carry = lds + a.groups, *const held = lds + (a.groups + 2) / 2 * 2;
     for (int e = threadIdx.x; e < a.groups; e += kRouteThreads) base[e] = 0;
     __syncthreads();
-    route_choose<E, V>(a, 0, base);
+    route_choose<E, V>(a, 0, base, reinterpret_cast<Choice *>(held));
     // The chosen experts are read back by other lanes of this workgroup.
     __threadfence_block();
     __syncthreads();
     route_offsets(a, base, carry, true);
-    route_place(a, 0, base, held);
+    if (a.groups <= 512) route_place<kRouteWaves>(a, 0, base, held);
+    else route_place<kRouteFewWaves>(a, 0, base, held);
 }
 
 // First of two launches: choose and count.
@@ -249,21 +292,26 @@ __global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RouteArgs a
     extern __shared__ int lds[];
     for (int e = threadIdx.x; e < a.groups; e += kRouteThreads) lds[e] = 0;
     __syncthreads();
-    route_choose<E, V>(a, blockIdx.x * kRouteTokens, lds);
+    route_choose<E, V>(a, blockIdx.x * kRouteTokens, lds, reinterpret_cast<Choice *>(lds + (a.groups + 1) / 2 * 2));
     __syncthreads();
     for (int e = threadIdx.x; e < a.groups; e += kRouteThreads) a.counts[(long long)blockIdx.x * a.groups + e] = lds[e];
 }
 
 // Second: where each workgroup's slots of an expert begin, and their places.
-// V is not used: one kernel.
 __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a);
 
+constexpr int kGradThreads = 256;
+
 template <class E, int V>
-__global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteArgs a)
+__global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteArgs a)
 {
-    const int lane = threadIdx.x & 63, sub = lane & 15;
-    const int token = blockIdx.x * (kRouteThreads / 16) + (threadIdx.x >> 4);
+    // What each slot adds to its expert's gradient, for the 16 lanes that
+    // hold the token.
+    __shared__ Choice adds[kGradThreads / 16][kRouteMaxChoices];
+    const int sub = threadIdx.x & 15;
+    const int token = blockIdx.x * (kGradThreads / 16) + (threadIdx.x >> 4);
     if (token >= a.tokens) return;
+    Choice *const mine = adds[threadIdx.x >> 4];
     const long long s0 = (long long)token * a.choices;
     // The slots' weights and gradients, a lane one slot (two past sixteen
     // choices); unused slots count nothing.
@@ -274,13 +322,15 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteArgs a)
         const int j = sub + 16 * q;
         if (j < a.choices) {
             e[q] = a.experts[s0 + j];
-            if (e[q] >= 0) {
-                w[q] = a.weights[s0 + j];
-                g[q] = a.grad[s0 + j];
-            }
+            w[q] = a.weights[s0 + j];
+            g[q] = e[q] >= 0 ? a.grad[s0 + j] : 0.0f;
         }
     }
-    const float dot = row_sum<16>(w[0] * g[0] + w[1] * g[1]);
+    const float dot = row_sum(w[0] * g[0] + w[1] * g[1]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        if (sub + 16 * q < a.choices)
+            mine[sub + 16 * q] = Choice{a.normalize ? w[q] * (g[q] - dot) : w[q] * g[q], e[q]};
     float d[V];
     if (a.normalize) {
 #pragma unroll
@@ -290,27 +340,25 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteArgs a)
         route_load<E, V>(a, token, sub, x);
 #pragma unroll
         for (int i = 0; i < V; ++i) top = fmaxf(top, x[i]);
-        top = row_max<16>(top);
+        top = row_max(top);
         top = top > -__builtin_inff() ? top : 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             x[i] = expf(x[i] - top);
             sum += x[i];
         }
-        sum = row_sum<16>(sum);
+        sum = row_sum(sum);
         const float each = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) d[i] = -x[i] * each * dot;
     }
+    wave_sync();
     for (int j = 0; j < a.choices; ++j) {
-        const int from = (lane & 48) + (j & 15);
-        const int ej = __shfl(j < 16 ? e[0] : e[1], from);
-        const float wj = __shfl(j < 16 ? w[0] : w[1], from), gj = __shfl(j < 16 ? g[0] : g[1], from);
-        const int i0 = ej - sub * V;
-        const float add = a.normalize ? wj * (gj - dot) : wj * gj;
+        const Choice c = mine[j];
+        const int i0 = c.expert - sub * V;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (ej >= 0 && i == i0) d[i] += add;
+            if (c.expert >= 0 && i == i0) d[i] += c.logit;
     }
     E *p = reinterpret_cast<E *>(a.dlogits) + (long long)token * a.ldd + sub * V;
     const int left = a.groups - sub * V;

@@ -33,37 +33,34 @@ EXPERT_FUNCTIONS = (
 )
 
 _fns = None
+_raw_stream = torch._C._cuda_getCurrentRawStream     # current_stream(device).cuda_stream in a tenth of its time
+_current_device = torch._C._cuda_getDevice
 
 
 def _functions():
-    """The library's entry points with their signatures, set once."""
+    """The entry points on integers, {name: function}, bound once."""
     global _fns
     if _fns is None:
         lib = load_library()
-        i64, i32, vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
-        signatures = {
-            "expert_grouped_linear": ([i32, i64, i64, i64, i64, vp, i64, vp, i32, i64, i64, vp, vp, i32, vp, i64, vp], i32),
-            "expert_grouped_weight_grad": ([i32, i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, i64, i64, vp], i32),
-            "expert_mx4_quantize": ([i32, i64, i64, vp, i32, i64, vp, vp, vp], i32),
-            "expert_mx4_dequantize": ([i32, i64, i64, vp, vp, vp, i64, vp], i32),
-            "expert_mx4_workspace": ([i64, i64, i64, i64], i64),
-            "expert_mx4_linear": ([i32, i64, i64, i64, i64, vp, i64, vp, vp, vp, vp, i32, vp, i64, vp, i64, vp], i32),
-            "expert_route_workspace": ([i64, i64], i64),
-            "expert_route": ([i32, i64, i64, i64, i32, vp, i64, vp, vp, vp, vp, vp, i64, vp], i32),
-            "expert_route_grad": ([i32, i64, i64, i64, i32, vp, i64, vp, vp, vp, vp, i64, vp], i32),
-        }
-        fns = {}
-        for name, (args, res) in signatures.items():
-            fn = getattr(lib, name)
-            fn.argtypes = args
-            fn.restype = res
-            fns[name] = fn
-        _fns = fns
+        try:
+            from . import _expert_binding
+        except ImportError as e:
+            raise RuntimeError("_expert_binding.so is not built; run __graft_entry__.build() or "
+                               "python -m dense_gemm_optimisation_fp32_amd.build") from e
+        _expert_binding.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                              for name in EXPERT_FUNCTIONS})
+        _fns = {name: getattr(_expert_binding, name) for name in EXPERT_FUNCTIONS}
     return _fns
 
 
-def _call(name, *args):
-    st = _functions()[name](*args)
+def _call(name, index, *args):
+    """Entry point `name` on device `index` and its current stream, the last argument."""
+    fn = (_fns or _functions())[name]
+    if index == _current_device():
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
     if st != GEMM_F32_SUCCESS:
         raise GemmF32Error(st, name)
 
@@ -98,25 +95,6 @@ def _rows(x, what):
             raise ValueError(f"{what} has overlapping rows")
         return ld
     return x.shape[1]
-
-
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-class _On:
-    """The tensors' device as the current one, where it is not already."""
-
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
 
 
 def _offsets(offsets, groups, device):
@@ -179,9 +157,8 @@ def grouped_linear(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, bias
     bias_ptr = _bias(bias, groups, n, device)
     out = _out(out, (m, n), a.dtype, device)
     ldc = _rows(out, "out")
-    with _On(device):
-        _call("expert_grouped_linear", dt, m, n, k, groups, a.data_ptr(), lda, b.data_ptr(), layout, ldb, se,
-              offsets.data_ptr(), bias_ptr, _ACTIVATIONS[activation], out.data_ptr(), ldc, _stream(device))
+    _call("expert_grouped_linear", device.index, dt, m, n, k, groups, a.data_ptr(), lda, b.data_ptr(), layout, ldb,
+          se, offsets.data_ptr(), bias_ptr, _ACTIVATIONS[activation], out.data_ptr(), ldc)
     return out
 
 
@@ -208,9 +185,8 @@ def grouped_weight_grad(a: torch.Tensor, grad: torch.Tensor, offsets: torch.Tens
         raise ValueError("out needs unit stride along its rows")
     if k == 1:
         ldd = n
-    with _On(device):
-        _call("expert_grouped_weight_grad", dt, m, n, k, groups, a.data_ptr(), lda, grad.data_ptr(), ldg,
-              offsets.data_ptr(), out.data_ptr(), ldd, se, _stream(device))
+    _call("expert_grouped_weight_grad", device.index, dt, m, n, k, groups, a.data_ptr(), lda, grad.data_ptr(), ldg,
+          offsets.data_ptr(), out.data_ptr(), ldd, se)
     return out
 
 
@@ -270,10 +246,11 @@ def mx4_quantize(x: torch.Tensor) -> Mx4Tensor:
     kb = _blocks(k)
     codes = torch.empty((r, kb * 64), dtype=torch.uint8, device=x.device)
     scales = torch.empty((kb, r, 4), dtype=torch.uint8, device=x.device)
-    with _On(x.device):
-        _call("expert_mx4_quantize", dt, r, k, x.data_ptr(), layout, ld, codes.data_ptr(), scales.data_ptr(),
-              _stream(x.device))
-    return Mx4Tensor(codes, scales, k)
+    _call("expert_mx4_quantize", x.device.index, dt, r, k, x.data_ptr(), layout, ld, codes.data_ptr(),
+          scales.data_ptr())
+    q = Mx4Tensor.__new__(Mx4Tensor)          # (checked by construction)
+    q.codes, q.scales, q.k = codes, scales, k
+    return q
 
 
 def mx4_dequantize(q: Mx4Tensor, dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -287,9 +264,8 @@ def mx4_dequantize(q: Mx4Tensor, dtype: torch.dtype = torch.float32, out: torch.
     r = q.codes.shape[0]
     out = _out(out, (r, q.k), dtype, q.device)
     ld = _rows(out, "out")
-    with _On(q.device):
-        _call("expert_mx4_dequantize", dt, r, q.k, q.codes.data_ptr(), q.scales.data_ptr(), out.data_ptr(), ld,
-              _stream(q.device))
+    _call("expert_mx4_dequantize", q.device.index, dt, r, q.k, q.codes.data_ptr(), q.scales.data_ptr(),
+          out.data_ptr(), ld)
     return out
 
 
@@ -324,10 +300,9 @@ def mx4_linear(x: torch.Tensor, w: Mx4Tensor, offsets: torch.Tensor | None = Non
     ldy = _rows(out, "out")
     need = _functions()["expert_mx4_workspace"](m, n, k, groups)
     space = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    with _On(device):
-        _call("expert_mx4_linear", dt, m, n, k, groups, x.data_ptr(), ldx, w.codes.data_ptr(), w.scales.data_ptr(),
-              offsets_ptr, bias_ptr, _ACTIVATIONS[activation], out.data_ptr(), ldy,
-              space.data_ptr() if need else None, need, _stream(device))
+    _call("expert_mx4_linear", device.index, dt, m, n, k, groups, x.data_ptr(), ldx, w.codes.data_ptr(),
+          w.scales.data_ptr(), offsets_ptr, bias_ptr, _ACTIVATIONS[activation], out.data_ptr(), ldy,
+          space.data_ptr() if need else None, need)
     return out
 
 
@@ -355,18 +330,14 @@ def route(logits: torch.Tensor, choices: int, normalize: bool = True) -> Routing
         raise ValueError(f"choices must be from 1 to the {groups} experts")
     device = logits.device
     weights = torch.empty((tokens, choices), dtype=torch.float32, device=device)
-    # experts, offsets, order and the workspace: one allocation.
-    slots = tokens * choices
-    need = _functions()["expert_route_workspace"](tokens, groups) // 4
-    ints = torch.empty(2 * slots + groups + 1 + need, dtype=torch.int32, device=device)
-    experts = ints[:slots].view(tokens, choices)
-    order = ints[slots:2 * slots]
-    offsets = ints[2 * slots:2 * slots + groups + 1]
-    base = ints.data_ptr()
-    with _On(device):
-        _call("expert_route", dt, tokens, groups, choices, 1 if normalize else 0, logits.data_ptr(), ld,
-              weights.data_ptr(), base, base + 4 * (2 * slots), base + 4 * slots,
-              base + 4 * (2 * slots + groups + 1) if need else None, 4 * need, _stream(device))
+    experts = torch.empty((tokens, choices), dtype=torch.int32, device=device)
+    offsets = torch.empty(groups + 1, dtype=torch.int32, device=device)
+    order = torch.empty(tokens * choices, dtype=torch.int32, device=device)
+    need = _functions()["expert_route_workspace"](tokens, groups)
+    space = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _call("expert_route", device.index, dt, tokens, groups, choices, 1 if normalize else 0, logits.data_ptr(), ld,
+          weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(), order.data_ptr(),
+          space.data_ptr() if need else None, need)
     return Routing(weights, experts, offsets, order, bool(normalize))
 
 
@@ -386,8 +357,6 @@ def route_grad(logits: torch.Tensor, r: Routing, grad: torch.Tensor) -> torch.Te
     device = logits.device
     _on(device, weights=r.weights, experts=r.experts, grad=grad)
     out = torch.empty((tokens, groups), dtype=logits.dtype, device=device)
-    with _On(device):
-        _call("expert_route_grad", dt, tokens, groups, r.weights.shape[1], 1 if r.normalize else 0,
-              logits.data_ptr(), ld, r.weights.data_ptr(), r.experts.data_ptr(), grad.data_ptr(), out.data_ptr(),
-              groups, _stream(device))
+    _call("expert_route_grad", device.index, dt, tokens, groups, r.weights.shape[1], 1 if r.normalize else 0,
+          logits.data_ptr(), ld, r.weights.data_ptr(), r.experts.data_ptr(), grad.data_ptr(), out.data_ptr(), groups)
     return out
