@@ -28,7 +28,7 @@ REPO_DIR = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libgemm_f32.so")
-BINDING_SOURCE = os.path.join(CSRC, "expert_binding.c")
+BINDING_SOURCE = os.path.join(CSRC, "expert_binding.cpp")
 BINDING_PATH = os.path.join(PKG_DIR, "_expert_binding.so")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 HOST_SOURCES = [os.path.join(CSRC, "gemm_f32.hip"), os.path.join(CSRC, "expert_ops.hip")]
@@ -146,14 +146,21 @@ def build(verbose: bool = False) -> str:
     os.replace(tmp, LIB_PATH)
 
     # The Python module in front of the expert-layer entry points.
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    include = os.path.join(os.path.dirname(torch.__file__), "include")
     tmp = BINDING_PATH + ".tmp"
-    cmd = ["gcc", "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
-           "-o", tmp, BINDING_SOURCE]
+    cmd = ["g++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-o", tmp, BINDING_SOURCE,
+           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
     p = subprocess.run(cmd, capture_output=True, text=True)
     if p.returncode != 0:
-        _fail("expert_binding.c", p.stderr)
+        _fail("expert_binding.cpp", p.stderr)
     os.replace(tmp, BINDING_PATH)
     return LIB_PATH
 
