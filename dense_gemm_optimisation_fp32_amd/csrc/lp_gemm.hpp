@@ -100,11 +100,14 @@ __device__ __forceinline__ i32x4 lp_rsrc(const char *p, long long bytes)
 // tell apart from the copies' destinations, would else each wait for every
 // copy in flight (counted in the built code: vmcnt(0) before each; the
 // product with row-major B ran at 560 TFLOPS).  It writes no register, and
-// lp_wait and lp_barrier count the copies, so nothing else has to know it.
+// lp_wait and lp_barrier count the copies, so nothing else has to know it.  The
+// no-ops are the wait that a memory instruction needs after a vector
+// instruction has written its scalar operands (five issue slots), which the
+// compiler does not see to inside assembly.
 __device__ __forceinline__ void lp_copy16(i32x4 r, uint32_t off, i32x4 *wave_chunk)
 {
     const uint32_t at = (uint32_t)(uintptr_t)(lds_void_t)wave_chunk;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(at), "v"(off), "s"(r)
                  : "memory", "m0");

@@ -335,10 +335,11 @@ struct LpPipe {
         const int parts = 4 * last <= tile_step ? 4 : 2 * last <= tile_step ? 2 : 0;
         if (parts) tile_end -= last;
         if (first < tile_end) whole_tiles(first);
+        // The copies past the last tile still write LDS: they are waited for
+        // before it is used again, or given back.
+        lp_wait<0>();
         const int q = (int)(blockIdx.x / g.num_xcd);
         if (parts && q < parts * last) {
-            // (The copies past the last tile still write LDS.)
-            lp_wait<0>();
             __syncthreads();
             LpJob j = job(tile_end + q / parts);
             const int part = q % parts;
