@@ -57,8 +57,18 @@ bool large_tiles(int64_t rows, int64_t m, int64_t n, int64_t groups, int cus)
     return rows >= 192 && groups <= kPipeGroups && (m / 256 + groups / 2 + 1) * ((n + 255) / 256) >= cus;
 }
 
-// Up to this many rows an expert on average, the few-row kernels.
+// Up to this many rows an expert on average, the few-row kernels: one tile of
+// theirs holds all rows of such an expert, so its matrix is read once; of more
+// rows, every 16 read it again.
 constexpr int64_t kFewRows = 16;
+
+// The row tiles are counted on the device in 32 bits, also those of offsets
+// that are not sorted, where every expert may seem to own nearly all rows.
+bool counts_ok(int64_t m, int64_t groups)
+{
+    const int64_t least = mean_rows(m, groups) <= kFewRows ? 16 : 64;      // rows of a tile
+    return m / least + 1 <= kMaxInt / (groups + 2);
+}
 
 }  // namespace
 
@@ -80,7 +90,7 @@ int expert_grouped_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t gr
         return GEMM_F32_ERR_INVALID_VALUE;
     if (dtype == EXPERT_F32 && (col ? (n - 1) * ldb + k : (k - 1) * ldb + n) * size > kMaxInt - 3)
         return GEMM_F32_ERR_INVALID_VALUE;
-    if (!grid_ok(m, n, 16, 32, groups + 2)) return GEMM_F32_ERR_INVALID_VALUE;
+    if (!grid_ok(m, n, 16, 32, groups + 2) || !counts_ok(m, groups)) return GEMM_F32_ERR_INVALID_VALUE;
     GroupedArgs a{};
     int cus = 0;
     const int st = current_device(&cus, &a.num_xcd);
@@ -221,7 +231,8 @@ int expert_mx4_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups
     if ((offsets && !aligned(offsets, 4)) || !here(codes, 16) || !here(scales, 4) || (bias && !aligned(bias, 4)) ||
         (m > 0 && (!here(X, size) || !here(Y, size))))
         return GEMM_F32_ERR_INVALID_VALUE;
-    if (!grid_ok(m, n, 16, 32, groups + 2) || m > (kMaxInt - 3) / ((k + 31) / 32)) return GEMM_F32_ERR_INVALID_VALUE;
+    if (!grid_ok(m, n, 16, 32, groups + 2) || !counts_ok(m, groups) || m > (kMaxInt - 3) / ((k + 31) / 32))
+        return GEMM_F32_ERR_INVALID_VALUE;
     const int64_t need = expert_mx4_workspace(m, n, k, groups);
     if (need > 0 && !here(workspace, 16)) return GEMM_F32_ERR_INVALID_VALUE;
     if (workspace_bytes < need) return GEMM_F32_ERR_SCRATCH_TOO_SMALL;

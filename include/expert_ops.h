@@ -23,8 +23,10 @@
  *    to no expert: their rows of C are zero.
  *  - m may be 0 (no rows); groups, n and k are at least 1.  One row of an
  *    operand is below 8 MiB, an expert's matrix and C's tile rows in 32-bit
- *    precision below 2 GiB (GEMM_F32_ERR_INVALID_VALUE otherwise); the whole
- *    of A, B or C may be larger.
+ *    precision below 2 GiB, and (m / 64 + 1) (groups + 2) of a product below
+ *    2^31, with m / 16 where an expert has 16 rows or fewer on average
+ *    (GEMM_F32_ERR_INVALID_VALUE otherwise); the whole of A, B or C may be
+ *    larger.
  *  - Errors: GEMM_F32_ERR_INVALID_VALUE (an argument outside the above),
  *    GEMM_F32_ERR_NO_DEVICE, GEMM_F32_ERR_UNSUPPORTED_DEVICE,
  *    GEMM_F32_ERR_HIP (a launch failed; gemm_f32_last_hip_error),

@@ -139,3 +139,17 @@ def test_mx4_tensor():
     assert tuple(q.shape) == (3, 5, 200)
     with pytest.raises(TypeError):
         g.Mx4Tensor(torch.zeros((5, 64)), torch.zeros((1, 5, 4)), 100)
+
+
+@pytest.mark.parametrize("name,base,m,groups,ok", [
+    (n, b, m, e, ok) for n, b in (("expert_grouped_linear", LINEAR), ("expert_mx4_linear", MX4))
+    for m, e, ok in ((1 << 29, 1000, False), (1 << 25, 1000, True), (700000, 60000, False), (700000, 44000, True))])
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not real")
+def test_row_tiles_are_counted_in_32_bits(name, base, m, groups, ok):
+    """Unsorted offsets can make every expert seem to own all rows: the sum of
+    such row tiles has to fit as well."""
+    args = dict(base, m=m, groups=groups)
+    if "work" in args:
+        args["work_bytes"] = 1 << 40
+    status = x._functions()[name](*args.values())
+    assert (status == BAD) != ok
