@@ -1,7 +1,7 @@
 // Products grouped by expert where an expert has few rows (decoding): bound
 // by the bytes of the experts' matrices, each read once.
 //
-// A workgroup takes 16 MT rows of one expert and a strip of columns, and its
+// A workgroup takes 16 rows of one expert and a strip of columns, and its
 // wavefronts split k.  A and B go straight from memory into registers, 16
 // bytes a lane, one iteration's loads ahead of the products; the products run
 // on 16-row matrix instructions whose rows past the expert's are wasted,
@@ -34,26 +34,25 @@ namespace gemmf32 {
 
 enum FewKind { kFewF32 = 0, kFewBf16 = 1, kFewFp4 = 2 };
 
-template <int KIND, bool B_KS, class X, int MT_, int WAVES_, int NB_>
+template <int KIND, bool B_KS, class X, int WAVES_, int NB_>
 struct FewTile {
     using E = X;                                     // elements of A and C
-    static constexpr int MT = MT_, WAVES = WAVES_, THREADS = WAVES * 64;
+    static constexpr int WAVES = WAVES_, THREADS = WAVES * 64;
     // 16-column blocks of a workgroup, and the k that one wavefront's
     // iteration covers.
     static constexpr int NB = B_KS ? (KIND == kFewF32 ? 4 : 8) : NB_;
-    static constexpr int BM = 16 * MT, BN = 16 * NB;
+    static constexpr int BM = 16, BN = 16 * NB;
     static constexpr int KI = KIND == kFewFp4 ? 512 : KIND == kFewF32 ? (B_KS ? 32 : 64) : (B_KS ? 32 : 128);
     static constexpr int LOADS = B_KS ? 8 : 4 * NB;  // 16-byte loads of B a lane and iteration
     static constexpr int A_LOADS = KIND == kFewFp4 ? 0 : KIND == kFewF32 ? KI / 16 : KI / 32;   // of A
     // 4-bit: columns that LDS holds of X, bytes of a row's codes there (16
     // more than the codes: rows on different banks).
     static constexpr int CHUNK = 4096, CODE_ROW = CHUNK / 2 + 16;
-    static_assert(KIND != kFewFp4 || MT == 1, "4-bit: 16 rows");
 };
 
 template <class T, int KIND>
 struct FewRegs {
-    i32x4 a[KIND == kFewFp4 ? 1 : T::MT * T::A_LOADS];
+    i32x4 a[KIND == kFewFp4 ? 1 : T::A_LOADS];
     i32x4 b[T::LOADS];
     int s[KIND == kFewFp4 ? T::LOADS : 1];
 };
@@ -62,7 +61,7 @@ template <int KIND, bool B_KS, class T>
 __global__ __launch_bounds__(T::THREADS) void few_grouped_kernel(GroupedArgs g)
 {
     using E = typename T::E;
-    constexpr int BM = T::BM, BN = T::BN, ROW = BN + 4, MT = T::MT;
+    constexpr int BM = T::BM, BN = T::BN, ROW = BN + 4;
     __shared__ float red[T::WAVES][BM * ROW];
     __shared__ __align__(16) u8 codes[KIND == kFewFp4 ? 16 * T::CODE_ROW : 16];
     __shared__ u8 scales[KIND == kFewFp4 ? 16 * (T::CHUNK / 32 + 4) : 4];
@@ -75,19 +74,14 @@ __global__ __launch_bounds__(T::THREADS) void few_grouped_kernel(GroupedArgs g)
     const int l16 = lane & 15, grp = lane >> 4;
     const int rows = min(rt.rows, BM);
 
-    f32x4 acc[MT][T::NB];
+    f32x4 acc[T::NB];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nb = 0; nb < T::NB; ++nb) acc[mt][nb] = f32x4{};
+    for (int nb = 0; nb < T::NB; ++nb) acc[nb] = f32x4{};
 
     if (rt.expert >= 0) {
         constexpr int N = 16 / sizeof(E);
         const char *const bx = g.B + rt.expert * g.expert_stride;
-        const E *pa[MT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-            pa[mt] = reinterpret_cast<const E *>(g.A + (rt.row + min(mt * 16 + l16, rows - 1)) * g.lda);
+        const E *const pa = reinterpret_cast<const E *>(g.A + (rt.row + min(l16, rows - 1)) * g.lda);
         // 4-bit: codes of 128 columns are 64 bytes; counted in k-blocks.
         const int blocks = g.a_kblocks;
         const u8 *sb = nullptr;
@@ -107,12 +101,10 @@ __global__ __launch_bounds__(T::THREADS) void few_grouped_kernel(GroupedArgs g)
             const int k0 = it * T::KI;
             if constexpr (KIND != kFewFp4) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int s = 0; s < T::A_LOADS; ++s) {
-                        const int kk = k0 + (s * 4 + grp) * N;
-                        r.a[mt * T::A_LOADS + s] = load_chunk(pa[mt] + kk, g.k - kk);
-                    }
+                for (int s = 0; s < T::A_LOADS; ++s) {
+                    const int kk = k0 + (s * 4 + grp) * N;
+                    r.a[s] = load_chunk(pa + kk, g.k - kk);
+                }
             }
             if constexpr (B_KS) {
                 constexpr int PER = KIND == kFewF32 ? 4 : 8;
@@ -159,56 +151,54 @@ __global__ __launch_bounds__(T::THREADS) void few_grouped_kernel(GroupedArgs g)
                     for (int nb = 0; nb < T::NB; ++nb) {
                         const i32x4 w = r.b[s * T::NB + nb];
                         const i32x8 b = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
-                        acc[0][nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc[0][nb], 4, 4, 0,
-                                                                                      r.s[s * T::NB + nb], 0, byte);
+                        acc[nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc[nb], 4, 4, 0,
+                                                                                  r.s[s * T::NB + nb], 0, byte);
                     }
                 }
             } else {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int s = 0; s < T::A_LOADS; ++s) {
+                    const i32x4 a = r.a[s];
+                    if constexpr (KIND == kFewF32) {
+                        const f32x4 af = __builtin_bit_cast(f32x4, a);
+                        if constexpr (B_KS) {
+                            // k-rows 4 grp + j of the run; set c: columns 4 i + c.
 #pragma unroll
-                    for (int s = 0; s < T::A_LOADS; ++s) {
-                        const i32x4 a = r.a[mt * T::A_LOADS + s];
-                        if constexpr (KIND == kFewF32) {
-                            const f32x4 af = __builtin_bit_cast(f32x4, a);
-                            if constexpr (B_KS) {
-                                // k-rows 4 grp + j of the run; set c: columns 4 i + c.
+                            for (int j = 0; j < 4; ++j) {
+                                const f32x4 bf = __builtin_bit_cast(f32x4, r.b[s * 4 + j]);
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const f32x4 bf = __builtin_bit_cast(f32x4, r.b[s * 4 + j]);
-#pragma unroll
-                                    for (int c = 0; c < 4; ++c)
-                                        acc[mt][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(bf[c], af[j], acc[mt][c], 0, 0, 0);
-                                }
-                            } else {
-#pragma unroll
-                                for (int nb = 0; nb < T::NB; ++nb) {
-                                    const f32x4 bf = __builtin_bit_cast(f32x4, r.b[s * T::NB + nb]);
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j)
-                                        acc[mt][nb] = __builtin_amdgcn_mfma_f32_16x16x4f32(bf[j], af[j], acc[mt][nb], 0, 0, 0);
-                                }
+                                for (int c = 0; c < 4; ++c)
+                                    acc[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(bf[c], af[j], acc[c], 0, 0, 0);
                             }
                         } else {
-                            const bf16x8 af = __builtin_bit_cast(bf16x8, a);
 #pragma unroll
                             for (int nb = 0; nb < T::NB; ++nb) {
-                                i32x4 b;
-                                if constexpr (B_KS) {
-                                    // Column nb of the lane's eight, its k-rows in pairs.
+                                const f32x4 bf = __builtin_bit_cast(f32x4, r.b[s * T::NB + nb]);
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        b[i] = (int)__builtin_amdgcn_perm((unsigned)r.b[2 * i + 1][nb / 2],
-                                                                          (unsigned)r.b[2 * i][nb / 2],
-                                                                          nb & 1 ? 0x07060302u : 0x05040100u);
-                                } else {
-                                    b = r.b[s * T::NB + nb];
-                                }
-                                acc[mt][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), af,
-                                                                                      acc[mt][nb], 0, 0, 0);
+                                for (int j = 0; j < 4; ++j)
+                                    acc[nb] = __builtin_amdgcn_mfma_f32_16x16x4f32(bf[j], af[j], acc[nb], 0, 0, 0);
                             }
                         }
+                    } else {
+                        const bf16x8 af = __builtin_bit_cast(bf16x8, a);
+#pragma unroll
+                        for (int nb = 0; nb < T::NB; ++nb) {
+                            i32x4 b;
+                            if constexpr (B_KS) {
+                                // Column nb of the lane's eight, its k-rows in pairs.
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    b[i] = (int)__builtin_amdgcn_perm((unsigned)r.b[2 * i + 1][nb / 2],
+                                                                      (unsigned)r.b[2 * i][nb / 2],
+                                                                      nb & 1 ? 0x07060302u : 0x05040100u);
+                            } else {
+                                b = r.b[s * T::NB + nb];
+                            }
+                            acc[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), af,
+                                                                              acc[nb], 0, 0, 0);
+                        }
                     }
+                }
             }
         };
         // 4-bit: X's columns [c0, c0 + CHUNK), a thread a block of 32.
@@ -268,14 +258,12 @@ __global__ __launch_bounds__(T::THREADS) void few_grouped_kernel(GroupedArgs g)
     // Lane (l16, grp) holds row l16 and columns 4 grp + v of each block:
     // column 16 nb + i (k contiguous) or NB i + nb (k strided) of the strip.
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nb = 0; nb < T::NB; ++nb)
 #pragma unroll
-        for (int nb = 0; nb < T::NB; ++nb)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int i = 4 * grp + v;
-                red[wave][(mt * 16 + l16) * ROW + (B_KS ? T::NB * i + nb : nb * 16 + i)] = acc[mt][nb][v];
-            }
+        for (int v = 0; v < 4; ++v) {
+            const int i = 4 * grp + v;
+            red[wave][l16 * ROW + (B_KS ? T::NB * i + nb : nb * 16 + i)] = acc[nb][v];
+        }
     __syncthreads();
     const float *const bias = g.bias && rt.expert >= 0 ? g.bias + rt.expert * g.bias_stride + col0 : nullptr;
     for (int e = tid; e < rows * BN; e += T::THREADS) {

@@ -17,9 +17,13 @@ void launch_tile(GroupedArgs a, hipStream_t s)
 template <int KIND, bool B_KS, class X>
 void launch_kind(const GroupedArgs &a, int cu_count, hipStream_t s)
 {
-    using Large = FewTile<KIND, B_KS, X, 1, 4, 2>;
-    using Small = FewTile<KIND, B_KS, X, 1, 8, 1>;
-    // Row tiles that there are at least, for one a used expert.
+    using Large = FewTile<KIND, B_KS, X, 4, 2>;
+    using Small = FewTile<KIND, B_KS, X, 8, 1>;
+    // Row tiles that there are about: below four workgroups a CU the call is
+    // bound by latency (4096 columns, k = 1024, 2 of 8 experts in 32 bits: 12.0
+    // us with the larger strips, 8.9 with the smaller; 14336 columns, k = 4096
+    // in 4 bits 15.1 / 12.5), above by bandwidth (16 rows over 8 experts, 14336
+    // columns, k = 4096, bfloat16: 137 us, 6.1 TB/s).
     const long long rows = (a.m + 15) / 16, used = rows > a.groups ? rows : a.m < a.groups ? a.m : a.groups;
     if (used * ((a.n + Large::BN - 1) / Large::BN) < 4ll * cu_count) launch_tile<KIND, B_KS, Small>(a, s);
     else launch_tile<KIND, B_KS, Large>(a, s);

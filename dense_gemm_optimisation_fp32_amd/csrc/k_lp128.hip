@@ -3,7 +3,7 @@
 
 namespace gemmf32 {
 
-using Tile = LpTile<128, 128, 2, 2, 8, 2>;
+using Tile = LpTile<128, 128, 2, 2>;
 
 void launch_lp128(const GroupedArgs &a, const LpCall &c, hipStream_t s) { launch_lp<Tile>(a, c, s); }
 void launch_lp128_unaligned(const GroupedArgs &a, const LpCall &c, hipStream_t s) { launch_lp_unaligned<Tile>(a, c, s); }

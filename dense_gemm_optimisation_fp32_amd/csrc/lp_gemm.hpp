@@ -12,11 +12,10 @@
 // 4-bit values; four k-steps.
 //
 // Operands travel from memory straight into LDS (buffer_load ... lds, 16
-// bytes a lane) into a ring of STAGES slabs; the kernel is bound by the
-// matrix cores and by the LDS reads that feed them (a 128 x 64 wavefront
-// tile reads 96 bytes a cycle and CU of the 128 there are).  The last k-step
-// of a slab comes after the barrier that hands the next slab over, so its
-// products cover the first reads of that slab.
+// bytes a lane) into two stages of a slab each.  The last k-step of a slab
+// comes after the barrier that hands the next slab over, so its products
+// cover the first reads of that slab.  What bounds the products: see
+// lp_pipe.hpp.
 //
 // LDS layouts (a copy places lane i's 16 bytes at the wavefront's base + 16 i,
 // so a layout is chosen by which global chunk each lane fetches):
@@ -50,11 +49,12 @@ typedef __attribute__((address_space(3))) void *lds_void_t;
 
 enum LpKind { kBf16 = 0, kFp4 = 1 };
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int CPR_, int STAGES_>
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_>
 struct LpTile {
-    static constexpr int CPR = CPR_;                      // 16-byte chunks of a row and slab: 4 or 8
+    static constexpr int CPR = 8;                         // 16-byte chunks of a row and slab
     static constexpr int STEPS = CPR / 2;                 // k-steps of a slab
-    static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, STAGES = STAGES_;
+    static constexpr int STAGES = 2;
+    static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
     static constexpr int THREADS = WAVES_M * WAVES_N * 64;
     static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
     static constexpr int MB = WM / 32, NB = WN / 32;      // 32 x 32 blocks of a wavefront
@@ -68,11 +68,10 @@ struct LpTile {
     static constexpr int SCALE_CHUNKS = (SCALE_WAVES_A + SCALE_WAVES_B) * 64;
     static_assert(A_CHUNKS % THREADS == 0 && B_CHUNKS % THREADS == 0, "whole copies");
     static_assert(WM % 32 == 0 && WN % 32 == 0, "32 x 32 blocks");
-    static_assert(CPR == 4 || CPR == 8, "64 or 128 bytes of a row");
     // Where chunk c of row r of a contiguous operand lies: the 16 rows that a
     // fragment read touches at a time fall on 16 places of the 256 bytes of
     // the banks.
-    static __device__ __forceinline__ int swizzle(int r) { return CPR == 4 ? (r >> 2) & 3 : (r >> 1) & 7; }
+    static __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 7; }
     static constexpr int stage_chunks(int kind) { return A_CHUNKS + B_CHUNKS + (kind == kFp4 ? SCALE_CHUNKS : 0); }
 };
 
@@ -298,7 +297,7 @@ struct LpProblem {
 // registers, one slab ahead, with the tails made zero on the way.
 template <class T, int KIND, bool A_KS, bool B_KS, int RUN, bool REG = false>
 struct LpLoop {
-    static_assert(!REG || (KIND == kBf16 && T::STAGES >= 2), "register copies: bfloat16, two stages or more");
+    static_assert(!REG || KIND == kBf16, "register copies: bfloat16");
     static constexpr int KSLAB = T::CPR * (KIND == kFp4 ? 32 : 8);
     // Scale words of a slab: [A, B][k-block][row], four a chunk.  The first
     // wavefronts copy A's, the next ones B's, and further ones the same again:
@@ -444,9 +443,9 @@ struct LpLoop {
         }
     }
 
-    // One slab.  COPY: the slab STAGES ahead is copied, as soon as this one's
-    // last fragments are read.  LAST: there is no next slab.
-    template <bool COPY, bool LAST>
+    // One slab.  COPY: the slab two ahead is copied, as soon as this one's
+    // last fragments are read.  FIX: the next slab is the last, LAST: this one.
+    template <bool COPY, bool FIX, bool LAST>
     __device__ __forceinline__ void slab(int kt, LpFrags<T, KIND> &f, f32x16 (&acc)[T::MB][T::NB])
     {
         // 4-bit slabs of two k-blocks: the last one of an odd number holds
@@ -462,14 +461,9 @@ struct LpLoop {
             if constexpr (REG) {
                 store(kt + 1);
                 lp_barrier<63>();
-            } else if constexpr (COPY) {
-                lp_barrier<(T::STAGES - 2) * COPIES>();
             } else {
-                // The slabs after the next one may still be on their way.
-                if (T::STAGES > 3 && slabs - 2 - kt >= 2) lp_wait<2 * COPIES>();
-                else if (T::STAGES > 2 && slabs - 2 - kt >= 1) lp_wait<COPIES>();
-                else lp_wait<0>();
-                if (kt + 2 == slabs && tail != 0) fix_tail(kt + 1);
+                lp_wait<0>();
+                if (FIX && tail != 0) fix_tail(kt + 1);
                 lp_barrier<63>();
             }
             if constexpr (COPY && REG) load(kt + 2);
@@ -504,19 +498,16 @@ struct LpLoop {
                 lp_wait<0>();
                 if (tail) fix_tail(0);
                 lp_barrier<63>();
-            } else if (slabs >= T::STAGES) {
-                lp_barrier<(T::STAGES - 1) * COPIES>();
             } else {
-                lp_barrier<0>();
+                lp_barrier<COPIES>();
             }
         }
 #pragma unroll
         for (int r = 0; r < READS; ++r) read(0, 0, r, f);
         int kt = 0;
-        constexpr int AHEAD = REG ? 2 : T::STAGES;
-        for (; kt + AHEAD < slabs; ++kt) slab<true, false>(kt, f, acc);
-        for (; kt + 1 < slabs; ++kt) slab<false, false>(kt, f, acc);
-        slab<false, true>(kt, f, acc);
+        for (; kt + 2 < slabs; ++kt) slab<true, false, false>(kt, f, acc);
+        if (kt + 1 < slabs) slab<false, true, false>(kt++, f, acc);
+        slab<false, false, true>(kt, f, acc);
     }
 };
 

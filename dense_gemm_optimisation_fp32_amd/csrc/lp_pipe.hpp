@@ -8,10 +8,20 @@
 // Layouts, fragments and products are those of lp_gemm.hpp.  A stage is
 // refilled as soon as the barrier has freed it: three quarters of its copies
 // among the products behind the barrier, the rest among the next slab's
-// first (all in one burst fill the address queue, and the products behind
-// them wait: 1143 against 1154 TFLOPS at 16384 x 14336 x 4096).  Measured
-// there too: slabs of 64 instead of 128 bytes a row, four stages deep, 1054;
-// touching lines two slabs ahead of their copies, 1139.
+// first.  Measured in TFLOPS on 16384 x 14336 x 4096 in bfloat16, normal
+// values, 8 experts: so 1154; all copies behind the barrier 1143; slabs of 64
+// instead of 128 bytes a row, four stages deep, 1054; 4 instead of 8
+// wavefronts 1046; touching lines two slabs ahead of their copies 1139.
+//
+// What bounds it: the matrix cores are busy two thirds of the time, and the
+// clock falls with the operands' bits (a library product of the same sizes
+// 1339 with normal values, 2062 with zeros; this kernel with one expert 1266
+// and 1406).  The rest is the copies: the same products without them ran at
+// 1331 and 1944 (n = 8192).  It is not LDS reads (a CU gave 215 bytes a cycle
+// of the 96 that a tile asks for), nor conflicts of banks (none counted), nor
+// the rate of the copies alone (64 bytes a cycle and CU, of which a tile
+// needs 32).  Rows that are not a power of two of bytes apart run 6 % faster
+// (k = 4160 for 4096).
 //
 // Every slab issues the same number of copies, so one count of copies in
 // flight serves every wait: past the last tile they read nothing (a
@@ -283,8 +293,8 @@ struct LpPipe {
         }
     }
 
-    // One slab: the products of stage `get`, the second half of the copies
-    // under way, and behind the barrier the first half of the next ones.
+    // One slab: the products of stage `get`, the last quarter of the copies
+    // under way, and behind the barrier the first three of the next ones.
     // fix: elements of the next slab, if fewer than it has room for (else 0).
     // LAST: of its tile; the next tile reads its own first fragments, so that
     // the epilogue has their registers.
@@ -310,7 +320,7 @@ struct LpPipe {
             fix_tail(then, fix);
             lp_barrier<63>();
         } else {
-            lp_barrier<(S - 2) * COPIES>();
+            lp_barrier<0>();
         }
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
@@ -345,9 +355,9 @@ struct LpPipe {
             const int part = q % parts;
             if (parts == 4) {
                 j.col += part / 2 * 128;
-                part_tile<LpTile<128, 128, 2, 4, 8, 2>>(j, part % 2 * 128);
+                part_tile<LpTile<128, 128, 2, 4>>(j, part % 2 * 128);
             } else {
-                part_tile<LpTile<128, 256, 2, 4, 8, 2>>(j, part * 128);
+                part_tile<LpTile<128, 256, 2, 4>>(j, part * 128);
             }
         }
     }
@@ -388,7 +398,7 @@ struct LpPipe {
             for (int i = 0; i < COPIES; ++i) copy(c, i);
             if (s + 1 < S) advance();
         }
-        // The last of these slabs' second half is issued again by the first
+        // The last of these slabs' last quarter is issued again by the first
         // slab's work below: the same bytes to the same place.
         bool started = false;
         for (int tile = first; tile < tile_end; tile += tile_step) {

@@ -349,6 +349,105 @@ def test_mx4_linear_shows_infinities_and_nan(m):
     assert not y[keep].isnan().any()
 
 
+# --- sizes that take 256 x 256 tiles -------------------------------------------
+#
+# Rows and columns with a tile for every CU (256): fewer tiles than CUs; a
+# second round that is split in quarters and one that is split in halves; two
+# whole rounds; more experts than lanes, some without rows.  Few k, so that a
+# tile is one slab, two, or a few with a last one that is not full.
+
+PIPE = {
+    "uneven": ([300, 511, 0, 257], 9472),
+    "odd_columns": ([300, 511, 0, 257], 9475),
+    "quarters": ([5000], 3400),
+    "halves": ([0, 4990], 4600),
+    "rounds": ([7990, 2], 4600),
+    "many": ([(97 * i) % 400 for i in range(70)], 600),
+}
+
+
+def against_experts(y, a, b, sizes, bias, act, tail):
+    """The rows of each expert, and zeros past the last."""
+    at = 0
+    for e, r in enumerate(sizes):
+        x, w = a[at:at + r].double(), b[e].double().contiguous()
+        ref, s = x @ w, x.abs() @ w.abs()
+        if bias is not None:
+            ref, s = ref + bias[e].double(), s + bias[e].double().abs()
+        if act == "relu":
+            ref = ref.clamp(min=0)
+        elif act == "gelu":
+            ref = ref * torch.special.ndtr(ref)
+        close(y[at:at + r], ref, s, act=True)
+        at += r
+    assert (y[at:at + tail] == 0).all()
+
+
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("k,act", [(40, None), (64, "relu"), (70, "gelu"), (192, None), (330, "gelu")])
+@pytest.mark.parametrize("case", list(PIPE))
+def test_grouped_linear_large_tiles(layout, k, act, case):
+    sizes, n = PIPE[case]
+    tail = 37
+    # (Strides of 4-byte multiples: two more elements where the count is odd.)
+    a, b, off = grouped_case(BF16, layout, sizes, n, k, 50, tail=tail, pad_a=10, pad_b=2 + n % 2 if layout == "row" else 6)
+    a[sum(sizes):] = float("nan")
+    bias = normal((len(sizes), n), F32, 51) if act else None
+    full = torch.full((a.shape[0], n + 5), 7.0, dtype=BF16, device=DEV)
+    out = full[:, :n] if n % 2 else None
+    y = g.grouped_linear(a, b, off, bias=bias, activation=act, out=out)
+    against_experts(y, a, b, sizes, bias, act, tail)
+    assert (full[:, n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("rows,n,k", [([300, 511, 0, 857], 2100, 2000), ([300, 511, 0, 857], 2104, 2001),
+                                      ([1, 2000, 64, 63], 2104, 2000), ([700], 4100, 4000), ([0, 1153], 4352, 2056)])
+def test_grouped_weight_grad_large_tiles(rows, n, k):
+    tail = 5
+    m = sum(rows) + tail
+    a, grad = padded_rows(normal((m, k), BF16, 52), 2 + k % 2), padded_rows(normal((m, n), BF16, 53), 2)
+    a[m - tail:], grad[m - tail:] = float("nan"), float("nan")
+    out = g.grouped_weight_grad(a, grad, offsets_of(rows))
+    at = 0
+    for e, r in enumerate(rows):
+        x, y = a[at:at + r].double().t().contiguous(), grad[at:at + r].double()
+        close(out[e], x @ y, x.abs() @ y.abs())
+        at += r
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("k", [100, 256, 384, 900])
+@pytest.mark.parametrize("case", list(PIPE))
+def test_mx4_linear_large_tiles(dtype, k, case):
+    sizes, n = PIPE[case]
+    w, values = packed(len(sizes), n, k, 54)
+    m = sum(sizes) + 3
+    x, bias = normal((m, k), dtype, 55), normal((len(sizes), n), F32, 56)
+    x[m - 3:] = float("nan")
+    y = g.mx4_linear(x, w, offsets=offsets_of(sizes), bias=bias, activation="relu")
+    against_experts(y, quantised(x[: m - 3]), torch.stack(values).transpose(1, 2), sizes, bias, "relu", 3)
+
+
+def test_large_tiles_bound_nan_and_infinity_to_their_row():
+    sizes, n = PIPE["uneven"]
+    a, b, off = grouped_case(BF16, "col", sizes, n, 100, 57)
+    a[1, 3], a[300, 99] = float("nan"), float("inf")
+    y = g.grouped_linear(a, b, off, activation="gelu")
+    assert y[1].isnan().all() and not y[300].isfinite().all()
+    keep = torch.ones(a.shape[0], dtype=torch.bool, device=DEV)
+    keep[[1, 300]] = False
+    assert y[keep].isfinite().all()
+
+
+def test_large_tiles_nonsense_offsets_stay_inside():
+    a, b = normal((1000, 64), BF16, 58), normal((3, 64, 13300), BF16, 59)
+    grad = normal((1500, 2560), BF16, 60)
+    for bad in ([0, 5000, -3, 1000], [900, 10, 800, 20], [-5, -5, -5, -5]):
+        off = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        assert g.grouped_linear(a, b, off).shape == (1000, 13300)
+        assert g.grouped_weight_grad(grad, grad, off).shape == (3, 2560, 2560)
+
+
 # --- routing ---------------------------------------------------------------------
 
 def route_reference(logits, choices, normalize):
