@@ -328,6 +328,28 @@ struct LpPipe {
         __builtin_amdgcn_s_setprio(0);
     }
 
+    // A slab of a wavefront whose rows are past the tile's last: its copies
+    // and the barrier.
+    template <bool FIX>
+    __device__ __forceinline__ void idle_slab(int fix, Source &c)
+    {
+        const int then = get + STAGE == S * STAGE ? 0 : get + STAGE;
+        get = then;
+#pragma unroll
+        for (int j = FIRST; j < COPIES; ++j) copy(c, j);
+        advance();
+        c = source();
+        if (FIX && fix) {
+            lp_wait<0>();
+            fix_tail(then, fix);
+            lp_barrier<63>();
+        } else {
+            lp_barrier<0>();
+        }
+#pragma unroll
+        for (int j = 0; j < FIRST; ++j) copy(c, j);
+    }
+
     __device__ __forceinline__ void run()
     {
         // Tiles of this workgroup: the XCDs share the tiles in contiguous runs
@@ -405,21 +427,32 @@ struct LpPipe {
             const LpJob j = job(tile);
             const int slabs = (j.k + KSLAB - 1) / KSLAB;
             const int tail = A_KS && B_KS ? 0 : j.k % KSLAB;
+            if (slabs > 0 && !started) {
+                started = true;
+                lp_wait<(S - 1) * COPIES>();
+                if (slabs == 1 && tail) {
+                    lp_wait<0>();
+                    fix_tail(0, tail);
+                }
+                lp_barrier<63>();
+            }
+            if (!GRAD && wr * T::WM >= j.rows) {
+                // Nothing to multiply or store: LDS and the power are the other
+                // wavefronts' (the three products of 8192 rows over 16 uneven
+                // experts, k = 2048, n = 4096: 520 us multiplied all the same,
+                // 510 so; with wavefronts of different rows on a SIMD 509, but
+                // full tiles then take 1.7 % longer).
+                int kt = 0;
+                for (; kt + 2 < slabs; ++kt) idle_slab<false>(0, c);
+                for (; kt < slabs; ++kt) idle_slab<true>(slabs == 1 || kt + 2 == slabs ? tail : 0, c);
+                continue;
+            }
             f32x16 acc[T::MB][T::NB];
 #pragma unroll
             for (int mb = 0; mb < T::MB; ++mb)
 #pragma unroll
                 for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] = f32x16{};
             if (slabs > 0) {
-                if (!started) {
-                    started = true;
-                    lp_wait<(S - 1) * COPIES>();
-                    if (slabs == 1 && tail) {
-                        lp_wait<0>();
-                        fix_tail(0, tail);
-                    }
-                    lp_barrier<63>();
-                }
                 LpFrags<T, KIND> f;
 #pragma unroll
                 for (int r = 0; r < READS; ++r) read(get, 0, r, f);
