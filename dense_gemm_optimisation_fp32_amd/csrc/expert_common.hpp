@@ -145,6 +145,13 @@ __device__ __forceinline__ bool grad_tile(const GroupedArgs &g, int x, int q, Gr
     return true;
 }
 
+// LDS written by a lane is read by another one of the same wavefront.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // 16 bytes of a row at p, elements at or past `left` zero.  Any alignment that
 // the elements have: unaligned wide loads are in order on this target.
 template <class E>

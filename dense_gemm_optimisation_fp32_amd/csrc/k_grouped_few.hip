@@ -19,13 +19,16 @@ void launch_kind(const GroupedArgs &a, int cu_count, hipStream_t s)
 {
     using Large = FewTile<KIND, B_KS, X, 4, 2>;
     using Small = FewTile<KIND, B_KS, X, 8, 1>;
-    // Row tiles that there are about: below four workgroups a CU the call is
-    // bound by latency (4096 columns, k = 1024, 2 of 8 experts in 32 bits: 12.0
-    // us with the larger strips, 8.9 with the smaller; 14336 columns, k = 4096
-    // in 4 bits 15.1 / 12.5), above by bandwidth (16 rows over 8 experts, 14336
-    // columns, k = 4096, bfloat16: 137 us, 6.1 TB/s).
+    // Strips of the larger kind that there are about.  Few of them are bound by
+    // latency, many by bandwidth (16 rows over 8 experts, 14336 columns, k =
+    // 4096, bfloat16: 137 us, 6.1 TB/s): fewer than four a CU take the smaller
+    // strips (2 of 8 experts, 4096 columns, k = 1024, 32 bits: 12.0 us with the
+    // larger, 8.9 so).  In 4 bits, where a strip also quantises its rows, fewer
+    // than one a CU (4 rows, 4096 columns, k = 14336: 16.5 / 10.2 us; 14336
+    // columns, k = 4096: 10.4 / 12.0).
+    constexpr long long least = KIND == kFewFp4 ? 1 : 4;
     const long long rows = (a.m + 15) / 16, used = rows > a.groups ? rows : a.m < a.groups ? a.m : a.groups;
-    if (used * ((a.n + Large::BN - 1) / Large::BN) < 4ll * cu_count) launch_tile<KIND, B_KS, Small>(a, s);
+    if (used * ((a.n + Large::BN - 1) / Large::BN) < least * cu_count) launch_tile<KIND, B_KS, Small>(a, s);
     else launch_tile<KIND, B_KS, Large>(a, s);
 }
 

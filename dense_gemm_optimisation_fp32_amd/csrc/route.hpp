@@ -83,13 +83,6 @@ __device__ __forceinline__ float row_sum(float x)
     return x + row_rotate<1>(x);
 }
 
-// LDS written by a lane is read by another one of the same wavefront.
-__device__ __forceinline__ void wave_sync()
-{
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // The V logits of a lane; absent experts, and NaN, are -inf.
 template <class E, int V>
 __device__ __forceinline__ void route_load(const RouteArgs &a, int token, int sub, float (&x)[V])
