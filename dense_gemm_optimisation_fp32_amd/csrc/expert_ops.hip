@@ -57,6 +57,22 @@ bool large_tiles(int64_t rows, int64_t m, int64_t n, int64_t groups, int cus)
     return rows >= 192 && groups <= kPipeGroups && (m / 256 + groups / 2 + 1) * ((n + 255) / 256) >= cus;
 }
 
+// Up to this many rows an expert on average, 64 x 128 tiles (three workgroups a
+// CU): such a product is bound by the experts' matrices, and by how many of
+// their bytes are under way.  Measured, us, 128 / 64 rows a tile: bfloat16, 16
+// experts, k = 2048, n = 4096, 64 rows each 47 / 44, 64 on average of uneven
+// ones 79 / 58, 96 rows each 51 / 81 (their matrices are read twice); 4 bits, 32
+// experts, 32 rows each 43 / 39, 64 45 / 44, 96 47 / 55.
+constexpr int64_t kSmallTileRows = 64;
+
+// The bfloat16 and 4-bit tiles of `rows` rows an expert.
+void launch_tiles(const GroupedArgs &a, const LpCall &c, int64_t rows, hipStream_t s)
+{
+    if (rows <= kSmallTileRows) launch_lp64(a, c, s);
+    else if (large_tiles(rows, a.m, a.n, a.groups, c.cu_count)) launch_lp256(a, c, s);
+    else launch_lp128(a, c, s);
+}
+
 // Up to this many rows an expert on average, the few-row kernels: one tile of
 // theirs holds all rows of such an expert, so its matrix is read once; of more
 // rows, every 16 read it again.
@@ -123,9 +139,8 @@ int expert_grouped_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t gr
         launch_f32_grouped(a, col, s);
     } else {
         const LpCall c{false, true, col, false, wide_rows(C, a.ldc, n, size), cus};
-        if (!copies) launch_lp128_unaligned(a, c, s);
-        else if (large_tiles(rows, m, n, groups, cus)) launch_lp256(a, c, s);
-        else launch_lp128(a, c, s);
+        if (copies) launch_tiles(a, c, rows, s);
+        else launch_lp128_unaligned(a, c, s);
     }
     return launched();
 }
@@ -272,8 +287,7 @@ int expert_mx4_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups
     a.a_scales = xs;
     a.lda = kp / 2;
     const LpCall c{true, bf16, true, false, wide_rows(Y, a.ldc, n, size), cus};
-    if (large_tiles(rows, m, n, groups, cus)) launch_lp256(a, c, s);
-    else launch_lp128(a, c, s);
+    launch_tiles(a, c, rows, s);
     return launched();
 }
 

@@ -19,13 +19,9 @@ void launch_lp_grouped(const GroupedArgs &a, bool wide, hipStream_t s)
 template <class T>
 void launch_lp(GroupedArgs a, const LpCall &c, hipStream_t s)
 {
-    a.tiles_m = c.weight_grad ? (a.k + T::BM - 1) / T::BM : grouped_row_tiles(a, T::BM);
+    a.tiles_m = grouped_row_tiles(a, T::BM);
     a.tiles_n = (a.n + T::BN - 1) / T::BN;
-    if (c.weight_grad) {
-        const unsigned grid = grad_workgroups(a);
-        if (c.wide) lp_weight_grad_kernel<T, true><<<grid, T::THREADS, 0, s>>>(a);
-        else lp_weight_grad_kernel<T, false><<<grid, T::THREADS, 0, s>>>(a);
-    } else if (c.fp4) {
+    if (c.fp4) {
         if (c.bf16) launch_lp_grouped<T, kFp4, false, __bf16>(a, c.wide, s);
         else launch_lp_grouped<T, kFp4, false, float>(a, c.wide, s);
     } else if (c.b_contiguous) {
@@ -33,6 +29,16 @@ void launch_lp(GroupedArgs a, const LpCall &c, hipStream_t s)
     } else {
         launch_lp_grouped<T, kBf16, true, __bf16>(a, c.wide, s);
     }
+}
+
+template <class T>
+void launch_lp_grad(GroupedArgs a, const LpCall &c, hipStream_t s)
+{
+    a.tiles_m = (a.k + T::BM - 1) / T::BM;
+    a.tiles_n = (a.n + T::BN - 1) / T::BN;
+    const unsigned grid = grad_workgroups(a);
+    if (c.wide) lp_weight_grad_kernel<T, true><<<grid, T::THREADS, 0, s>>>(a);
+    else lp_weight_grad_kernel<T, false><<<grid, T::THREADS, 0, s>>>(a);
 }
 
 template <class T>
