@@ -43,8 +43,11 @@ void launch_mx4_dequantize(const Mx4Args &a, bool bf16, hipStream_t s);
 void launch_f32_grouped(const GroupedArgs &a, bool b_contiguous, hipStream_t s);
 void launch_f32_weight_grad(const GroupedArgs &a, hipStream_t s);
 void launch_lp256(GroupedArgs a, const LpCall &c, hipStream_t s);
-// 64 x 128 tiles: no weight gradient.
+// 64 x 128 tiles in two stages or three, 64 x 64 in four.
 void launch_lp64(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+void launch_lp64_ring(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+void launch_lp64_square(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+void launch_lp64_square_grad(const GroupedArgs &a, const LpCall &c, hipStream_t s);
 void launch_lp128(const GroupedArgs &a, const LpCall &c, hipStream_t s);
 void launch_lp128_unaligned(const GroupedArgs &a, const LpCall &c, hipStream_t s);
 // Few rows an expert: tiles of 16 rows.

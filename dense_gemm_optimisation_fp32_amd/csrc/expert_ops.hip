@@ -65,10 +65,25 @@ bool large_tiles(int64_t rows, int64_t m, int64_t n, int64_t groups, int cus)
 // experts, 32 rows each 43 / 39, 64 45 / 44, 96 47 / 55.
 constexpr int64_t kSmallTileRows = 64;
 
-// The bfloat16 and 4-bit tiles of `rows` rows an expert.
+// Tiles of bm x bn that there are about: every expert's last is not full.
+int64_t tiles_of(const GroupedArgs &a, int64_t rows, int bm, int bn)
+{
+    return a.groups * ((rows + bm - 1) / bm) * ((a.n + bn - 1) / bn);
+}
+
+// The bfloat16 and 4-bit tiles of `rows` rows an expert.  Few tiles are bound by
+// the latency of one slab after the other: tiles small enough to give every CU
+// one, and rings of as many slabs as LDS holds.  Measured, us, 128 x 128 tiles
+// (64 x 128 up to 64 rows) in two stages / 64 x 128 in three, two workgroups a
+// CU / 64 x 64 in four: bfloat16, one expert, k = n = 4096, 64 rows 54 / 33 /
+// 24, 256 rows 58 / 33 / 25, 512 rows 57 / 34 / 37; k = 2048, n = 1024, 16
+// experts, 64 rows each 31 / 21 / 18, 256 rows 34 / 32 / 40, 512 rows 42 / 57 /
+// 72; 4 bits, k = n = 4096, 192 rows 17 / 15 / 13.
 void launch_tiles(const GroupedArgs &a, const LpCall &c, int64_t rows, hipStream_t s)
 {
-    if (rows <= kSmallTileRows) launch_lp64(a, c, s);
+    if (tiles_of(a, rows, 64, 64) <= c.cu_count) launch_lp64_square(a, c, s);
+    else if (tiles_of(a, rows, 64, 128) <= 2 * c.cu_count) launch_lp64_ring(a, c, s);
+    else if (rows <= kSmallTileRows) launch_lp64(a, c, s);
     else if (large_tiles(rows, a.m, a.n, a.groups, c.cu_count)) launch_lp256(a, c, s);
     else launch_lp128(a, c, s);
 }
@@ -183,6 +198,11 @@ int expert_grouped_weight_grad(int dtype, int64_t m, int64_t n, int64_t k, int64
         const LpCall c{false, true, false, true, wide_rows(dB, a.ldc, n, size) && a.expert_stride % 16 == 0, cus};
         const bool copies = aligned(A, 4) && aligned(G, 4) && a.lda % 4 == 0 && a.ldb % 4 == 0;
         if (!copies) launch_lp128_unaligned(a, c, s);
+        // Few tiles: 64 x 64 in four stages (one expert, k = n = 1024, 128 x 128 / 64 x
+        // 64: 64 rows 4.5 / 3.9 us, 1024 rows 12.4 / 9.0, 4096 rows 43 / 26; at 2 to 4
+        // such tiles a CU, 64 x 128 in three stages gave nothing: k = n = 2048, 1024 rows
+        // 14.8 / 17.3).
+        else if (groups * ((k + 63) / 64) * ((n + 63) / 64) <= cus) launch_lp64_square_grad(a, c, s);
         // The larger tiles from 384 rows on, the length of the contraction, where there
         // is one for every CU (k = 2048, n = 4096, 256 / 128: 256 rows 139 / 128 us, 512
         // rows 194 / 208, 1024 rows 287 / 346).

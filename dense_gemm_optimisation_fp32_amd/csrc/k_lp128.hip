@@ -3,7 +3,7 @@
 
 namespace gemmf32 {
 
-using Tile = LpTile<128, 128, 2, 2>;
+using Tile = LpTile<128, 128, 2, 2, 2>;
 
 void launch_lp128(const GroupedArgs &a, const LpCall &c, hipStream_t s)
 {

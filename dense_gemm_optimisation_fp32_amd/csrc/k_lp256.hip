@@ -6,7 +6,7 @@ namespace gemmf32 {
 
 namespace {
 
-using Tile = LpTile<256, 256, 2, 4>;
+using Tile = LpTile<256, 256, 2, 4, 2>;
 
 template <int KIND, bool GRAD, bool B_KS, class E>
 void launch_pipe(const GroupedArgs &a, bool wide, unsigned grid, hipStream_t s)

@@ -12,10 +12,11 @@
 // 4-bit values; four k-steps.
 //
 // Operands travel from memory straight into LDS (buffer_load ... lds, 16
-// bytes a lane) into two stages of a slab each.  The last k-step of a slab
-// comes after the barrier that hands the next slab over, so its products
-// cover the first reads of that slab.  What bounds the products: see
-// lp_pipe.hpp.
+// bytes a lane) into a ring of STAGES slabs.  The last k-step of a slab comes
+// after the barrier that hands the next slab over, so its products cover the
+// first reads of that slab.  What bounds the products: see lp_pipe.hpp; few of
+// them are bound by how many slabs are under way, hence the longer rings of
+// the smaller tiles.
 //
 // LDS layouts (a copy places lane i's 16 bytes at the wavefront's base + 16 i,
 // so a layout is chosen by which global chunk each lane fetches):
@@ -49,12 +50,11 @@ typedef __attribute__((address_space(3))) void *lds_void_t;
 
 enum LpKind { kBf16 = 0, kFp4 = 1 };
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_>
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_>
 struct LpTile {
     static constexpr int CPR = 8;                         // 16-byte chunks of a row and slab
     static constexpr int STEPS = CPR / 2;                 // k-steps of a slab
-    static constexpr int STAGES = 2;
-    static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
+    static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, STAGES = STAGES_;
     static constexpr int THREADS = WAVES_M * WAVES_N * 64;
     static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
     static constexpr int MB = WM / 32, NB = WN / 32;      // 32 x 32 blocks of a wavefront
@@ -297,7 +297,7 @@ struct LpProblem {
 // registers, one slab ahead, with the tails made zero on the way.
 template <class T, int KIND, bool A_KS, bool B_KS, int RUN, bool REG = false>
 struct LpLoop {
-    static_assert(!REG || KIND == kBf16, "register copies: bfloat16");
+    static_assert(!REG || (KIND == kBf16 && T::STAGES == 2), "register copies: bfloat16, two stages");
     static constexpr int KSLAB = T::CPR * (KIND == kFp4 ? 32 : 8);
     // Scale words of a slab: [A, B][k-block][row], four a chunk.  The first
     // wavefronts copy A's, the next ones B's, and further ones the same again:
@@ -443,9 +443,9 @@ struct LpLoop {
         }
     }
 
-    // One slab.  COPY: the slab two ahead is copied, as soon as this one's
-    // last fragments are read.  FIX: the next slab is the last, LAST: this one.
-    template <bool COPY, bool FIX, bool LAST>
+    // One slab.  COPY: the slab STAGES ahead is copied, as soon as this one's
+    // last fragments are read.  LAST: there is no next slab.
+    template <bool COPY, bool LAST>
     __device__ __forceinline__ void slab(int kt, LpFrags<T, KIND> &f, f32x16 (&acc)[T::MB][T::NB])
     {
         // 4-bit slabs of two k-blocks: the last one of an odd number holds
@@ -461,9 +461,14 @@ struct LpLoop {
             if constexpr (REG) {
                 store(kt + 1);
                 lp_barrier<63>();
+            } else if constexpr (COPY) {
+                lp_barrier<(T::STAGES - 2) * COPIES>();
             } else {
-                lp_wait<0>();
-                if (FIX && tail != 0) fix_tail(kt + 1);
+                // The slabs after the next one may still be on their way.
+                if (T::STAGES > 3 && slabs - 2 - kt >= 2) lp_wait<2 * COPIES>();
+                else if (T::STAGES > 2 && slabs - 2 - kt >= 1) lp_wait<COPIES>();
+                else lp_wait<0>();
+                if (kt + 2 == slabs && tail != 0) fix_tail(kt + 1);
                 lp_barrier<63>();
             }
             if constexpr (COPY && REG) load(kt + 2);
@@ -498,16 +503,18 @@ struct LpLoop {
                 lp_wait<0>();
                 if (tail) fix_tail(0);
                 lp_barrier<63>();
+            } else if (slabs >= T::STAGES) {
+                lp_barrier<(T::STAGES - 1) * COPIES>();
             } else {
-                lp_barrier<COPIES>();
+                lp_barrier<0>();
             }
         }
 #pragma unroll
         for (int r = 0; r < READS; ++r) read(0, 0, r, f);
         int kt = 0;
-        for (; kt + 2 < slabs; ++kt) slab<true, false, false>(kt, f, acc);
-        if (kt + 1 < slabs) slab<false, true, false>(kt++, f, acc);
-        slab<false, false, true>(kt, f, acc);
+        for (; kt + T::STAGES < slabs; ++kt) slab<true, false>(kt, f, acc);
+        for (; kt + 1 < slabs; ++kt) slab<false, false>(kt, f, acc);
+        slab<false, true>(kt, f, acc);
     }
 };
 

@@ -377,9 +377,9 @@ struct LpPipe {
             const int part = q % parts;
             if (parts == 4) {
                 j.col += part / 2 * 128;
-                part_tile<LpTile<128, 128, 2, 4>>(j, part % 2 * 128);
+                part_tile<LpTile<128, 128, 2, 4, 2>>(j, part % 2 * 128);
             } else {
-                part_tile<LpTile<128, 256, 2, 4>>(j, part * 128);
+                part_tile<LpTile<128, 256, 2, 4, 2>>(j, part * 128);
             }
         }
     }

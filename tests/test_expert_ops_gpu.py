@@ -448,6 +448,61 @@ def test_large_tiles_nonsense_offsets_stay_inside():
         assert g.grouped_weight_grad(grad, grad, off).shape == (3, 2560, 2560)
 
 
+# --- sizes in between -------------------------------------------------------------
+#
+# More than two 64 x 128 tiles a CU, but no 256 x 256 tile for each; and one of
+# every ring for few tiles, at contractions shorter than the ring and longer.
+
+MIDDLE = {
+    "tiles_of_128": ([100, 181, 0, 140], 8200),
+    "tiles_of_128_odd": ([100, 181, 0, 140], 8203),
+    "tiles_of_64": ([(7 * i) % 50 for i in range(130)], 600),
+    "three_slabs": ([250, 0, 190], 2300),
+    "four_slabs": ([130], 1030),
+}
+
+
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("k,act", [(40, "relu"), (128, None), (190, "gelu"), (256, None), (330, None), (1000, "gelu")])
+@pytest.mark.parametrize("case", list(MIDDLE))
+def test_grouped_linear_middle_sizes(layout, k, act, case):
+    sizes, n = MIDDLE[case]
+    tail = 21
+    a, b, off = grouped_case(BF16, layout, sizes, n, k, 70, tail=tail, pad_a=10, pad_b=2 + n % 2 if layout == "row" else 6)
+    a[sum(sizes):] = float("nan")
+    bias = normal((len(sizes), n), F32, 71) if act else None
+    y = g.grouped_linear(a, b, off, bias=bias, activation=act)
+    against_experts(y, a, b, sizes, bias, act, tail)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("k", [100, 512, 900, 1300])
+@pytest.mark.parametrize("case", list(MIDDLE))
+def test_mx4_linear_middle_sizes(dtype, k, case):
+    sizes, n = MIDDLE[case]
+    w, values = packed(len(sizes), n, k, 72)
+    m = sum(sizes) + 3
+    x, bias = normal((m, k), dtype, 73), normal((len(sizes), n), F32, 74)
+    x[m - 3:] = float("nan")
+    y = g.mx4_linear(x, w, offsets=offsets_of(sizes), bias=bias, activation="relu")
+    against_experts(y, quantised(x[: m - 3]), torch.stack(values).transpose(1, 2), sizes, bias, "relu", 3)
+
+
+@pytest.mark.parametrize("rows", [[40, 0, 190, 61], [64, 128, 1, 257]])
+@pytest.mark.parametrize("n,k", [(1100, 1104), (530, 1001), (256, 260), (1104, 64)])
+def test_grouped_weight_grad_middle_sizes(rows, n, k):
+    tail = 5
+    m = sum(rows) + tail
+    a, grad = padded_rows(normal((m, k), BF16, 75), 2 + k % 2), padded_rows(normal((m, n), BF16, 76), 2)
+    a[m - tail:], grad[m - tail:] = float("nan"), float("nan")
+    out = g.grouped_weight_grad(a, grad, offsets_of(rows))
+    at = 0
+    for e, r in enumerate(rows):
+        x, y = a[at:at + r].double().t().contiguous(), grad[at:at + r].double()
+        close(out[e], x @ y, x.abs() @ y.abs())
+        at += r
+
+
 # --- routing ---------------------------------------------------------------------
 
 def route_reference(logits, choices, normalize):
