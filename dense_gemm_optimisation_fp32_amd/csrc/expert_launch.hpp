@@ -40,8 +40,8 @@ int record_hip_error(hipError_t e);
 
 void launch_mx4_quantize(const Mx4Args &a, bool bf16, bool columns, hipStream_t s);
 void launch_mx4_dequantize(const Mx4Args &a, bool bf16, hipStream_t s);
-void launch_f32_grouped(const GroupedArgs &a, bool b_contiguous, hipStream_t s);
-void launch_f32_weight_grad(const GroupedArgs &a, hipStream_t s);
+void launch_f32_grouped(const GroupedArgs &a, bool b_contiguous, int cu_count, hipStream_t s);
+void launch_f32_weight_grad(const GroupedArgs &a, int cu_count, hipStream_t s);
 void launch_lp256(GroupedArgs a, const LpCall &c, hipStream_t s);
 // 64 x 128 tiles in two stages or three, 64 x 64 in four.
 void launch_lp64(const GroupedArgs &a, const LpCall &c, hipStream_t s);

@@ -93,6 +93,22 @@ void launch_tiles(const GroupedArgs &a, const LpCall &c, int64_t rows, hipStream
 // rows, every 16 read it again.
 constexpr int64_t kFewRows = 16;
 
+// Whether a product takes the few-row kernels: also with more rows where C has
+// few 16 x 16 blocks, whose k those split over wavefronts while a tile takes
+// slab after slab.  Measured, us, tiles / few rows: 32 bits, up to four blocks a
+// CU: 3 experts, k = 6544, n = 1216, 18 rows 128 / 61 (B contiguous 115 / 44),
+// 128 rows, seven a CU, 128 / 131 (118 / 164); one expert, k = n = 4096, 64 rows
+// 81 / 40 (74 / 61), 128 rows 81 / 81 (76 / 98).  bfloat16 and 4 bits with B
+// contiguous, up to two: one expert, k = n = 4096, 32 rows 24 / 17 (4 bits 12.0 /
+// 9.6), 48 rows, three a CU, 24 / 24 (12.0 / 12.9); k = n = 1024, 128 rows 8.7 /
+// 6.1 (8.0 / 5.6).
+bool few_rows(bool f32, bool b_contiguous, int64_t rows, int64_t n, int64_t groups, int cus)
+{
+    if (rows <= kFewRows) return true;
+    const int64_t blocks = groups * ((rows + 15) / 16) * ((n + 15) / 16);
+    return blocks <= (f32 ? 4 : b_contiguous ? 2 : 0) * cus;
+}
+
 // The row tiles are counted on the device in 32 bits, also those of offsets
 // that are not sorted, where every expert may seem to own nearly all rows.
 bool counts_ok(int64_t m, int64_t groups)
@@ -148,10 +164,10 @@ int expert_grouped_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t gr
     // The copies of the bfloat16 tiles need 4-byte aligned rows.
     const bool copies = dtype == EXPERT_F32 || (aligned(A, 4) && aligned(B, 4) && a.lda % 4 == 0 && a.ldb % 4 == 0 &&
                                                 a.expert_stride % 4 == 0);
-    if (rows <= kFewRows) {
+    if (few_rows(dtype == EXPERT_F32, col, rows, n, groups, cus)) {
         launch_few(a, dtype == EXPERT_BF16, false, col, cus, s);
     } else if (dtype == EXPERT_F32) {
-        launch_f32_grouped(a, col, s);
+        launch_f32_grouped(a, col, cus, s);
     } else {
         const LpCall c{false, true, col, false, wide_rows(C, a.ldc, n, size), cus};
         if (copies) launch_tiles(a, c, rows, s);
@@ -193,7 +209,7 @@ int expert_grouped_weight_grad(int dtype, int64_t m, int64_t n, int64_t k, int64
     a.group_m = 8;
     const hipStream_t s = stream_of(stream);
     if (dtype == EXPERT_F32) {
-        launch_f32_weight_grad(a, s);
+        launch_f32_weight_grad(a, cus, s);
     } else {
         const LpCall c{false, true, false, true, wide_rows(dB, a.ldc, n, size) && a.expert_stride % 16 == 0, cus};
         const bool copies = aligned(A, 4) && aligned(G, 4) && a.lda % 4 == 0 && a.ldb % 4 == 0;
@@ -297,7 +313,7 @@ int expert_mx4_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups
     const hipStream_t s = stream_of(stream);
     const bool bf16 = dtype == EXPERT_BF16;
     const int64_t rows = mean_rows(m, groups);
-    if (need == 0) {
+    if (few_rows(false, true, rows, n, groups, cus)) {
         launch_few(a, bf16, true, true, cus, s);
         return launched();
     }

@@ -9,6 +9,7 @@ namespace {
 using Tile128 = DmaTile<128, 128, 16, 2, 2, 3, false>;
 using Tile64x128 = DmaTile<64, 128, 16, 2, 2, 2>;
 using Tile64 = DmaTile<64, 64, 16, 2, 2, 2>;
+using Tile64Ring = DmaTile<64, 64, 16, 2, 2, 4>;
 
 // Tiles of 64 rows below 608 rows an expert: an expert's last tile is half
 // empty on average, and 128 x 128 tiles run at 147 TFLOPS, 64 x 128 at about
@@ -18,6 +19,16 @@ using Tile64 = DmaTile<64, 64, 16, 2, 2, 2>;
 // 8192 rows, k = n = 1024: 139 / 134 / 146; 8 experts of 1024 rows, k = n =
 // 4096: 1982 / 2098 / 2207.
 int tile_of(int rows, int n) { return rows >= 608 ? 0 : n % 128 > 64 || n % 128 == 0 ? 1 : 2; }
+
+// Few tiles are bound by the latency of one slab after the other: 64 x 64 in four
+// slabs up to two a CU.  Measured, us, above / so: 3 experts, k = 6544, n = 1216,
+// 256 rows 282 / 130; one expert, k = n = 4096, 256 rows 188 / 87, k = 4096, n =
+// 14336, 128 rows 152 / 137; weight gradient of k = n = 1024, 64 rows 6.7 / 5.0,
+// 4096 rows 252 / 77.
+bool few_tiles(int groups, int rows, int n, int cu_count)
+{
+    return (long long)groups * ((rows + 63) / 64) * ((n + 63) / 64) <= 2ll * cu_count;
+}
 
 template <class T>
 void launch_tile(GroupedArgs a, bool b_contiguous, hipStream_t s)
@@ -39,9 +50,11 @@ void launch_grad(GroupedArgs a, hipStream_t s)
 
 }  // namespace
 
-void launch_f32_grouped(const GroupedArgs &a, bool b_contiguous, hipStream_t s)
+void launch_f32_grouped(const GroupedArgs &a, bool b_contiguous, int cu_count, hipStream_t s)
 {
-    switch (tile_of((a.m + a.groups - 1) / a.groups, a.n)) {
+    const int rows = (a.m + a.groups - 1) / a.groups;
+    if (few_tiles(a.groups, rows, a.n, cu_count)) return launch_tile<Tile64Ring>(a, b_contiguous, s);
+    switch (tile_of(rows, a.n)) {
     case 0: return launch_tile<Tile128>(a, b_contiguous, s);
     case 1: return launch_tile<Tile64x128>(a, b_contiguous, s);
     default: return launch_tile<Tile64>(a, b_contiguous, s);
@@ -50,8 +63,9 @@ void launch_f32_grouped(const GroupedArgs &a, bool b_contiguous, hipStream_t s)
 
 // Here the expert's rows are the contraction: smaller tiles where it is short
 // (the same sizes, us: 250 / 241 / 239; 161 / 133 / 138; 1904 / 1946 / 1993).
-void launch_f32_weight_grad(const GroupedArgs &a, hipStream_t s)
+void launch_f32_weight_grad(const GroupedArgs &a, int cu_count, hipStream_t s)
 {
+    if (few_tiles(a.groups, a.k, a.n, cu_count)) return launch_grad<Tile64Ring>(a, s);
     switch (tile_of((a.m + a.groups - 1) / a.groups, a.n)) {
     case 0: return launch_grad<Tile128>(a, s);
     case 1: return launch_grad<Tile64x128>(a, s);

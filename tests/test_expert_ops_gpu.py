@@ -503,6 +503,34 @@ def test_grouped_weight_grad_middle_sizes(rows, n, k):
         at += r
 
 
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("k,act", [(7, "relu"), (64, None), (333, "gelu")])
+@pytest.mark.parametrize("sizes,n", [([900, 400], 2200), ([100, 181, 0, 140], 8292), ([100, 181, 0, 140], 8200),
+                                     ([100, 181, 0, 140], 8203), ([250, 0, 190], 2300), ([130, 33], 530)])
+def test_grouped_linear_f32_middle_sizes(layout, k, act, sizes, n):
+    tail = 21
+    a, b, off = grouped_case(F32, layout, sizes, n, k, 77, tail=tail, pad_a=3, pad_b=5)
+    a[sum(sizes):] = float("nan")
+    bias = normal((len(sizes), n), F32, 78) if act else None
+    y = g.grouped_linear(a, b, off, bias=bias, activation=act)
+    against_experts(y, a, b, sizes, bias, act, tail)
+
+
+@pytest.mark.parametrize("rows", [[40, 0, 190, 61], [900, 400]])
+@pytest.mark.parametrize("n,k", [(1100, 1104), (1050, 1001), (256, 260), (530, 700)])
+def test_grouped_weight_grad_f32_middle_sizes(rows, n, k):
+    tail = 5
+    m = sum(rows) + tail
+    a, grad = padded_rows(normal((m, k), F32, 79), 3), padded_rows(normal((m, n), F32, 80), 1)
+    a[m - tail:], grad[m - tail:] = float("nan"), float("nan")
+    out = g.grouped_weight_grad(a, grad, offsets_of(rows))
+    at = 0
+    for e, r in enumerate(rows):
+        x, y = a[at:at + r].double().t().contiguous(), grad[at:at + r].double()
+        close(out[e], x @ y, x.abs() @ y.abs())
+        at += r
+
+
 # --- routing ---------------------------------------------------------------------
 
 def route_reference(logits, choices, normalize):
