@@ -41,6 +41,10 @@ bool grid_ok(int64_t rows, int64_t cols, int64_t row_tile, int64_t col_tile, int
     return (rows / row_tile + more) <= kMaxInt / ((cols + col_tile - 1) / col_tile);
 }
 
+// A workgroup of the routing kernels steps its slot counters by up to 1024 past
+// the last slot: more slots than this could wrap them.
+constexpr int64_t kMaxSlots = kMaxInt - 2047;
+
 // Rows an expert has on average.
 int64_t mean_rows(int64_t m, int64_t groups) { return (m + groups - 1) / groups; }
 
@@ -338,7 +342,7 @@ int expert_route(int dtype, int64_t tokens, int64_t groups, int64_t choices, int
                  int64_t workspace_bytes, void *stream)
 {
     if (!dtype_ok(dtype) || !size_ok(tokens, 0) || groups < 1 || groups > kRouteMaxExperts || choices < 1 ||
-        choices > groups || choices > kRouteMaxChoices || tokens * choices > kMaxInt || ld < groups ||
+        choices > groups || choices > kRouteMaxChoices || tokens * choices > kMaxSlots || ld < groups ||
         (normalize != 0 && normalize != 1) || !here(offsets, 4))
         return GEMM_F32_ERR_INVALID_VALUE;
     if (tokens > 0 && (!here(logits, elem(dtype)) || !here(weights, 4) || !here(experts, 4) || !here(order, 4)))

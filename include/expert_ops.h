@@ -112,7 +112,7 @@ int expert_mx4_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups
  * A slot for which no expert is left has expert -1 and weight 0 and is not in
  * order, whose places from offsets[groups] on hold -1.
  *   1 <= choices <= min(groups, 32), groups <= 1024, tokens >= 0,
- *   tokens * choices below 2^31.
+ *   tokens * choices at most 2^31 - 2048.
  * workspace: expert_route_workspace bytes, as above.
  */
 int64_t expert_route_workspace(int64_t tokens, int64_t groups);
