@@ -116,8 +116,9 @@ __global__ __launch_bounds__(T::THREADS) void f32_weight_grad_kernel(GroupedArgs
     for (int mb = 0; mb < T::MB; ++mb)
 #pragma unroll
         for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] = f32x16{};
-    for (; lo < hi; lo += run) {
-        g.k = min(run, hi - lo);
+    // (Counted by the rows left: lo + run could pass 32 bits.)
+    for (int left = hi - lo; left > 0; left -= g.k, lo += g.k) {
+        g.k = min(run, left);
         g.k_tiles = (g.k + T::BK - 1) / T::BK;
         const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A + lo * a.lda, extent_bytes((g.k - 1) * a.lda + a.k * 4ll));
         const __amdgpu_buffer_rsrc_t rb = make_rsrc(a.B + lo * a.ldb, extent_bytes((g.k - 1) * a.ldb + a.n * 4ll));
