@@ -19,9 +19,9 @@ inline int grouped_row_tiles(const GroupedArgs &a, int bm)
 
 // Workgroups of a weight gradient with a tile each: every XCD's share of every
 // expert's tiles.
-inline unsigned grad_workgroups(const GroupedArgs &a)
+inline long long grad_workgroups(const GroupedArgs &a)
 {
-    return (unsigned)((a.tiles_m * a.tiles_n + a.num_xcd - 1) / a.num_xcd) * a.num_xcd * a.groups;
+    return ((long long)a.tiles_m * a.tiles_n + a.num_xcd - 1) / a.num_xcd * a.num_xcd * a.groups;
 }
 
 // Which of a tile shape's kernels a call takes.

@@ -41,6 +41,14 @@ bool grid_ok(int64_t rows, int64_t cols, int64_t row_tile, int64_t col_tile, int
     return (rows / row_tile + more) <= kMaxInt / ((cols + col_tile - 1) / col_tile);
 }
 
+// So are those of a weight gradient: every XCD (eight at most) takes an equal
+// share of every expert's tiles, rounded up.
+bool grad_ok(int64_t n, int64_t k, int64_t groups)
+{
+    const int64_t tiles = (k + 63) / 64 * ((n + 63) / 64);
+    return (tiles + 7) / 8 * 8 <= kMaxInt / groups;
+}
+
 // A workgroup of the routing kernels steps its slot counters by up to 1024 past
 // the last slot: more slots than this could wrap them.
 constexpr int64_t kMaxSlots = kMaxInt - 2047;
@@ -193,7 +201,7 @@ int expert_grouped_weight_grad(int dtype, int64_t m, int64_t n, int64_t k, int64
     if (!here(offsets, 4) || !here(dB, size) || (m > 0 && (!here(A, size) || !here(G, size))))
         return GEMM_F32_ERR_INVALID_VALUE;
     if (dtype == EXPERT_F32 && ((k - 1) * ldd + n) * size > kMaxInt - 3) return GEMM_F32_ERR_INVALID_VALUE;
-    if ((k + 63) / 64 * ((n + 63) / 64) > kMaxInt / groups) return GEMM_F32_ERR_INVALID_VALUE;
+    if (!grad_ok(n, k, groups)) return GEMM_F32_ERR_INVALID_VALUE;
     GroupedArgs a{};
     int cus = 0;
     const int st = current_device(&cus, &a.num_xcd);

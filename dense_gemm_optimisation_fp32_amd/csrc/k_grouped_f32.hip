@@ -45,7 +45,7 @@ void launch_grad(GroupedArgs a, hipStream_t s)
 {
     a.tiles_m = (a.k + T::BM - 1) / T::BM;
     a.tiles_n = (a.n + T::BN - 1) / T::BN;
-    f32_weight_grad_kernel<T><<<grad_workgroups(a), T::THREADS, 0, s>>>(a);
+    f32_weight_grad_kernel<T><<<(unsigned)grad_workgroups(a), T::THREADS, 0, s>>>(a);
 }
 
 }  // namespace

@@ -36,7 +36,7 @@ void launch_lp_grad(GroupedArgs a, const LpCall &c, hipStream_t s)
 {
     a.tiles_m = (a.k + T::BM - 1) / T::BM;
     a.tiles_n = (a.n + T::BN - 1) / T::BN;
-    const unsigned grid = grad_workgroups(a);
+    const unsigned grid = (unsigned)grad_workgroups(a);
     if (c.wide) lp_weight_grad_kernel<T, true><<<grid, T::THREADS, 0, s>>>(a);
     else lp_weight_grad_kernel<T, false><<<grid, T::THREADS, 0, s>>>(a);
 }
@@ -47,7 +47,7 @@ void launch_lp_unaligned(GroupedArgs a, const LpCall &c, hipStream_t s)
     a.tiles_m = c.weight_grad ? (a.k + T::BM - 1) / T::BM : grouped_row_tiles(a, T::BM);
     a.tiles_n = (a.n + T::BN - 1) / T::BN;
     const unsigned grid = (unsigned)a.tiles_m * a.tiles_n;
-    if (c.weight_grad) lp_weight_grad_kernel<T, false, true><<<grad_workgroups(a), T::THREADS, 0, s>>>(a);
+    if (c.weight_grad) lp_weight_grad_kernel<T, false, true><<<(unsigned)grad_workgroups(a), T::THREADS, 0, s>>>(a);
     else if (c.b_contiguous) lp_grouped_kernel<T, kBf16, false, __bf16, false, true><<<grid, T::THREADS, 0, s>>>(a);
     else lp_grouped_kernel<T, kBf16, true, __bf16, false, true><<<grid, T::THREADS, 0, s>>>(a);
 }

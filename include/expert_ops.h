@@ -63,6 +63,8 @@ int expert_grouped_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t gr
 /*
  * dB_e = A_e^T . G_e: A m x k, G m x n; dB: groups matrices k x n,
  * expert_stride apart, rows ldd apart, of dtype; zero for an empty expert.
+ * ceil(k / 64) ceil(n / 64), rounded up to a multiple of 8, times groups is
+ * below 2^31.
  */
 int expert_grouped_weight_grad(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups, const void *A, int64_t lda,
                                const void *G, int64_t ldg, const int *offsets, void *dB, int64_t ldd,

@@ -30,3 +30,15 @@ def test_slot_counters_of_a_workgroup_stay_in_32_bits(tokens, choices):
     assert tokens * choices > 2 ** 31 - 2048
     assert route(tokens, 32, choices) == BAD
     assert route((2 ** 31 - 2048) // choices, 32, choices) == ACCEPTED
+
+
+def weight_grad(groups, k=32, n=16):
+    return x._functions()["expert_grouped_weight_grad"](0, 8, n, k, groups, OK, k, OK, n, OK, OK, n, k * n, None)
+
+
+@pytest.mark.parametrize("groups", [1 << 30, 1 << 29, 600_000_000, (1 << 28) + 1])
+def test_weight_gradient_workgroups_are_counted_in_32_bits(groups):
+    """Every XCD takes a share of every expert's tiles: at least eight
+    workgroups an expert, also where it has one tile."""
+    assert weight_grad(groups) == BAD
+    assert weight_grad(1 << 16) == ACCEPTED
