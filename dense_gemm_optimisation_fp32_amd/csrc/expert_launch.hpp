@@ -1,8 +1,10 @@
 // Launches of the expert-layer kernels, defined in their translation units
-// and called by the C entry points in expert_ops.hip.
+// and called by the C entry points in expert_ops.hip.  They return a
+// gemm_f32_status.
 #pragma once
 
 #include "expert_common.hpp"
+#include "launch.hpp"
 
 namespace gemmf32 {
 
@@ -33,25 +35,24 @@ struct LpCall {
     int cu_count;
 };
 
-// Status of the current device (a gemm_f32_status) and its facts; a failed
-// HIP call's status, recorded for gemm_f32_last_hip_error.  In gemm_f32.hip.
+// Status of the current device (a gemm_f32_status) and its facts.  In
+// gemm_f32.hip.
 int current_device(int *cu_count, int *num_xcd);
-int record_hip_error(hipError_t e);
 
-void launch_mx4_quantize(const Mx4Args &a, bool bf16, bool columns, hipStream_t s);
-void launch_mx4_dequantize(const Mx4Args &a, bool bf16, hipStream_t s);
-void launch_f32_grouped(const GroupedArgs &a, bool b_contiguous, int cu_count, hipStream_t s);
-void launch_f32_weight_grad(const GroupedArgs &a, int cu_count, hipStream_t s);
-void launch_lp256(GroupedArgs a, const LpCall &c, hipStream_t s);
+int launch_mx4_quantize(const Mx4Args &a, bool bf16, bool columns, hipStream_t s);
+int launch_mx4_dequantize(const Mx4Args &a, bool bf16, hipStream_t s);
+int launch_f32_grouped(const GroupedArgs &a, bool b_contiguous, int cu_count, hipStream_t s);
+int launch_f32_weight_grad(const GroupedArgs &a, int cu_count, hipStream_t s);
+int launch_lp256(GroupedArgs a, const LpCall &c, hipStream_t s);
 // 64 x 128 tiles in two stages or three, 64 x 64 in four.
-void launch_lp64(const GroupedArgs &a, const LpCall &c, hipStream_t s);
-void launch_lp64_ring(const GroupedArgs &a, const LpCall &c, hipStream_t s);
-void launch_lp64_square(const GroupedArgs &a, const LpCall &c, hipStream_t s);
-void launch_lp64_square_grad(const GroupedArgs &a, const LpCall &c, hipStream_t s);
-void launch_lp128(const GroupedArgs &a, const LpCall &c, hipStream_t s);
-void launch_lp128_unaligned(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+int launch_lp64(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+int launch_lp64_ring(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+int launch_lp64_square(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+int launch_lp64_square_grad(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+int launch_lp128(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+int launch_lp128_unaligned(const GroupedArgs &a, const LpCall &c, hipStream_t s);
 // Few rows an expert: tiles of 16 rows.
-void launch_few(const GroupedArgs &a, bool bf16, bool fp4, bool b_contiguous, int cu_count, hipStream_t s);
-void launch_route(const RouteArgs &a, bool bf16, bool grad, hipStream_t s);
+int launch_few(const GroupedArgs &a, bool bf16, bool fp4, bool b_contiguous, int cu_count, hipStream_t s);
+int launch_route(const RouteArgs &a, bool bf16, bool grad, hipStream_t s);
 
 }  // namespace gemmf32

@@ -23,12 +23,6 @@ int64_t padded(int64_t k) { return (k + 127) / 128 * 128; }
 
 hipStream_t stream_of(void *s) { return reinterpret_cast<hipStream_t>(s); }
 
-int launched()
-{
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? GEMM_F32_SUCCESS : record_hip_error(e);
-}
-
 // Whether rows of C can be stored 16 bytes at a time.
 bool wide_rows(const void *c, int64_t row_bytes, int64_t n, int64_t size)
 {
@@ -91,13 +85,13 @@ int64_t tiles_of(const GroupedArgs &a, int64_t rows, int bm, int bn)
 // 24, 256 rows 58 / 33 / 25, 512 rows 57 / 34 / 37; k = 2048, n = 1024, 16
 // experts, 64 rows each 31 / 21 / 18, 256 rows 34 / 32 / 40, 512 rows 42 / 57 /
 // 72; 4 bits, k = n = 4096, 192 rows 17 / 15 / 13.
-void launch_tiles(const GroupedArgs &a, const LpCall &c, int64_t rows, hipStream_t s)
+int launch_tiles(const GroupedArgs &a, const LpCall &c, int64_t rows, hipStream_t s)
 {
-    if (tiles_of(a, rows, 64, 64) <= c.cu_count) launch_lp64_square(a, c, s);
-    else if (tiles_of(a, rows, 64, 128) <= 2 * c.cu_count) launch_lp64_ring(a, c, s);
-    else if (rows <= kSmallTileRows) launch_lp64(a, c, s);
-    else if (large_tiles(rows, a.m, a.n, a.groups, c.cu_count)) launch_lp256(a, c, s);
-    else launch_lp128(a, c, s);
+    if (tiles_of(a, rows, 64, 64) <= c.cu_count) return launch_lp64_square(a, c, s);
+    if (tiles_of(a, rows, 64, 128) <= 2 * c.cu_count) return launch_lp64_ring(a, c, s);
+    if (rows <= kSmallTileRows) return launch_lp64(a, c, s);
+    if (large_tiles(rows, a.m, a.n, a.groups, c.cu_count)) return launch_lp256(a, c, s);
+    return launch_lp128(a, c, s);
 }
 
 // Up to this many rows an expert on average, the few-row kernels: one tile of
@@ -176,16 +170,11 @@ int expert_grouped_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t gr
     // The copies of the bfloat16 tiles need 4-byte aligned rows.
     const bool copies = dtype == EXPERT_F32 || (aligned(A, 4) && aligned(B, 4) && a.lda % 4 == 0 && a.ldb % 4 == 0 &&
                                                 a.expert_stride % 4 == 0);
-    if (few_rows(dtype == EXPERT_F32, col, rows, n, groups, cus)) {
-        launch_few(a, dtype == EXPERT_BF16, false, col, cus, s);
-    } else if (dtype == EXPERT_F32) {
-        launch_f32_grouped(a, col, cus, s);
-    } else {
-        const LpCall c{false, true, col, false, wide_rows(C, a.ldc, n, size), cus};
-        if (copies) launch_tiles(a, c, rows, s);
-        else launch_lp128_unaligned(a, c, s);
-    }
-    return launched();
+    if (few_rows(dtype == EXPERT_F32, col, rows, n, groups, cus))
+        return launch_few(a, dtype == EXPERT_BF16, false, col, cus, s);
+    if (dtype == EXPERT_F32) return launch_f32_grouped(a, col, cus, s);
+    const LpCall c{false, true, col, false, wide_rows(C, a.ldc, n, size), cus};
+    return copies ? launch_tiles(a, c, rows, s) : launch_lp128_unaligned(a, c, s);
 }
 
 int expert_grouped_weight_grad(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups, const void *A, int64_t lda,
@@ -220,25 +209,21 @@ int expert_grouped_weight_grad(int dtype, int64_t m, int64_t n, int64_t k, int64
     a.expert_stride = expert_stride * size;
     a.group_m = 8;
     const hipStream_t s = stream_of(stream);
-    if (dtype == EXPERT_F32) {
-        launch_f32_weight_grad(a, cus, s);
-    } else {
-        const LpCall c{false, true, false, true, wide_rows(dB, a.ldc, n, size) && a.expert_stride % 16 == 0, cus};
-        const bool copies = aligned(A, 4) && aligned(G, 4) && a.lda % 4 == 0 && a.ldb % 4 == 0;
-        if (!copies) launch_lp128_unaligned(a, c, s);
-        // Few tiles: 64 x 64 in four stages (one expert, k = n = 1024, 128 x 128 / 64 x
-        // 64: 64 rows 4.5 / 3.9 us, 1024 rows 12.4 / 9.0, 4096 rows 43 / 26; at 2 to 4
-        // such tiles a CU, 64 x 128 in three stages gave nothing: k = n = 2048, 1024 rows
-        // 14.8 / 17.3).
-        else if (groups * ((k + 63) / 64) * ((n + 63) / 64) <= cus) launch_lp64_square_grad(a, c, s);
-        // The larger tiles from 384 rows on, the length of the contraction, where there
-        // is one for every CU (k = 2048, n = 4096, 256 / 128: 256 rows 139 / 128 us, 512
-        // rows 194 / 208, 1024 rows 287 / 346).
-        else if (mean_rows(m, groups) >= 384 && groups * ((k + 255) / 256) * ((n + 255) / 256) >= cus)
-            launch_lp256(a, c, s);
-        else launch_lp128(a, c, s);
-    }
-    return launched();
+    if (dtype == EXPERT_F32) return launch_f32_weight_grad(a, cus, s);
+    const LpCall c{false, true, false, true, wide_rows(dB, a.ldc, n, size) && a.expert_stride % 16 == 0, cus};
+    const bool copies = aligned(A, 4) && aligned(G, 4) && a.lda % 4 == 0 && a.ldb % 4 == 0;
+    if (!copies) return launch_lp128_unaligned(a, c, s);
+    // Few tiles: 64 x 64 in four stages (one expert, k = n = 1024, 128 x 128 / 64 x
+    // 64: 64 rows 4.5 / 3.9 us, 1024 rows 12.4 / 9.0, 4096 rows 43 / 26; at 2 to 4
+    // such tiles a CU, 64 x 128 in three stages gave nothing: k = n = 2048, 1024 rows
+    // 14.8 / 17.3).
+    if (groups * ((k + 63) / 64) * ((n + 63) / 64) <= cus) return launch_lp64_square_grad(a, c, s);
+    // The larger tiles from 384 rows on, the length of the contraction, where there
+    // is one for every CU (k = 2048, n = 4096, 256 / 128: 256 rows 139 / 128 us, 512
+    // rows 194 / 208, 1024 rows 287 / 346).
+    if (mean_rows(m, groups) >= 384 && groups * ((k + 255) / 256) * ((n + 255) / 256) >= cus)
+        return launch_lp256(a, c, s);
+    return launch_lp128(a, c, s);
 }
 
 int expert_mx4_quantize(int dtype, int64_t rows, int64_t k, const void *X, int layout, int64_t ld, void *codes,
@@ -254,8 +239,7 @@ int expert_mx4_quantize(int dtype, int64_t rows, int64_t k, const void *X, int l
     if (rows == 0) return GEMM_F32_SUCCESS;
     const Mx4Args a{static_cast<const char *>(X), static_cast<u8 *>(codes), static_cast<u8 *>(scales), ld, (int)rows,
                     (int)k, (int)padded(k)};
-    launch_mx4_quantize(a, dtype == EXPERT_BF16, layout == GEMM_F32_COL_MAJOR, stream_of(stream));
-    return launched();
+    return launch_mx4_quantize(a, dtype == EXPERT_BF16, layout == GEMM_F32_COL_MAJOR, stream_of(stream));
 }
 
 int expert_mx4_dequantize(int dtype, int64_t rows, int64_t k, const void *codes, const void *scales, void *X,
@@ -270,8 +254,7 @@ int expert_mx4_dequantize(int dtype, int64_t rows, int64_t k, const void *codes,
     if (rows == 0) return GEMM_F32_SUCCESS;
     const Mx4Args a{static_cast<const char *>(X), static_cast<u8 *>(const_cast<void *>(codes)),
                     static_cast<u8 *>(const_cast<void *>(scales)), ld, (int)rows, (int)k, (int)padded(k)};
-    launch_mx4_dequantize(a, dtype == EXPERT_BF16, stream_of(stream));
-    return launched();
+    return launch_mx4_dequantize(a, dtype == EXPERT_BF16, stream_of(stream));
 }
 
 int64_t expert_mx4_workspace(int64_t m, int64_t n, int64_t k, int64_t groups)
@@ -325,18 +308,16 @@ int expert_mx4_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups
     const hipStream_t s = stream_of(stream);
     const bool bf16 = dtype == EXPERT_BF16;
     const int64_t rows = mean_rows(m, groups);
-    if (few_rows(false, true, rows, n, groups, cus)) {
-        launch_few(a, bf16, true, true, cus, s);
-        return launched();
-    }
+    if (few_rows(false, true, rows, n, groups, cus)) return launch_few(a, bf16, true, true, cus, s);
     u8 *const xc = static_cast<u8 *>(workspace), *const xs = xc + m * (kp / 2);
-    launch_mx4_quantize(Mx4Args{static_cast<const char *>(X), xc, xs, ldx, (int)m, (int)k, (int)kp}, bf16, false, s);
+    const int quantised =
+        launch_mx4_quantize(Mx4Args{static_cast<const char *>(X), xc, xs, ldx, (int)m, (int)k, (int)kp}, bf16, false, s);
+    if (quantised != GEMM_F32_SUCCESS) return quantised;
     a.A = reinterpret_cast<const char *>(xc);
     a.a_scales = xs;
     a.lda = kp / 2;
     const LpCall c{true, bf16, true, false, wide_rows(Y, a.ldc, n, size), cus};
-    launch_tiles(a, c, rows, s);
-    return launched();
+    return launch_tiles(a, c, rows, s);
 }
 
 int64_t expert_route_workspace(int64_t tokens, int64_t groups)
@@ -372,8 +353,7 @@ int expert_route(int dtype, int64_t tokens, int64_t groups, int64_t choices, int
     a.groups = (int)groups;
     a.choices = (int)choices;
     a.normalize = normalize;
-    launch_route(a, dtype == EXPERT_BF16, false, stream_of(stream));
-    return launched();
+    return launch_route(a, dtype == EXPERT_BF16, false, stream_of(stream));
 }
 
 int expert_route_grad(int dtype, int64_t tokens, int64_t groups, int64_t choices, int normalize, const void *logits,
@@ -402,8 +382,7 @@ int expert_route_grad(int dtype, int64_t tokens, int64_t groups, int64_t choices
     a.grad = grad;
     a.dlogits = dlogits;
     a.ldd = ldd;
-    launch_route(a, dtype == EXPERT_BF16, true, stream_of(stream));
-    return launched();
+    return launch_route(a, dtype == EXPERT_BF16, true, stream_of(stream));
 }
 
 }  // extern "C"

@@ -31,26 +31,25 @@ bool few_tiles(int groups, int rows, int n, int cu_count)
 }
 
 template <class T>
-void launch_tile(GroupedArgs a, bool b_contiguous, hipStream_t s)
+int launch_tile(GroupedArgs a, bool b_contiguous, hipStream_t s)
 {
     a.tiles_m = grouped_row_tiles(a, T::BM);
     a.tiles_n = (a.n + T::BN - 1) / T::BN;
-    const unsigned grid = (unsigned)a.tiles_m * a.tiles_n;
-    if (b_contiguous) f32_grouped_kernel<T, true><<<grid, T::THREADS, 0, s>>>(a);
-    else f32_grouped_kernel<T, false><<<grid, T::THREADS, 0, s>>>(a);
+    return launch(b_contiguous ? f32_grouped_kernel<T, true> : f32_grouped_kernel<T, false>,
+                  (long long)a.tiles_m * a.tiles_n, T::THREADS, 0, s, a);
 }
 
 template <class T>
-void launch_grad(GroupedArgs a, hipStream_t s)
+int launch_grad(GroupedArgs a, hipStream_t s)
 {
     a.tiles_m = (a.k + T::BM - 1) / T::BM;
     a.tiles_n = (a.n + T::BN - 1) / T::BN;
-    f32_weight_grad_kernel<T><<<(unsigned)grad_workgroups(a), T::THREADS, 0, s>>>(a);
+    return launch(f32_weight_grad_kernel<T>, grad_workgroups(a), T::THREADS, 0, s, a);
 }
 
 }  // namespace
 
-void launch_f32_grouped(const GroupedArgs &a, bool b_contiguous, int cu_count, hipStream_t s)
+int launch_f32_grouped(const GroupedArgs &a, bool b_contiguous, int cu_count, hipStream_t s)
 {
     const int rows = (a.m + a.groups - 1) / a.groups;
     if (few_tiles(a.groups, rows, a.n, cu_count)) return launch_tile<Tile64Ring>(a, b_contiguous, s);
@@ -63,7 +62,7 @@ void launch_f32_grouped(const GroupedArgs &a, bool b_contiguous, int cu_count, h
 
 // Here the expert's rows are the contraction: smaller tiles where it is short
 // (the same sizes, us: 250 / 241 / 239; 161 / 133 / 138; 1904 / 1946 / 1993).
-void launch_f32_weight_grad(const GroupedArgs &a, int cu_count, hipStream_t s)
+int launch_f32_weight_grad(const GroupedArgs &a, int cu_count, hipStream_t s)
 {
     if (few_tiles(a.groups, a.k, a.n, cu_count)) return launch_grad<Tile64Ring>(a, s);
     switch (tile_of((a.m + a.groups - 1) / a.groups, a.n)) {

@@ -7,15 +7,15 @@ namespace gemmf32 {
 namespace {
 
 template <int KIND, bool B_KS, class T>
-void launch_tile(GroupedArgs a, hipStream_t s)
+int launch_tile(GroupedArgs a, hipStream_t s)
 {
     a.tiles_m = grouped_row_tiles(a, T::BM);
     a.tiles_n = (a.n + T::BN - 1) / T::BN;
-    few_grouped_kernel<KIND, B_KS, T><<<(unsigned)a.tiles_m * a.tiles_n, T::THREADS, 0, s>>>(a);
+    return launch(few_grouped_kernel<KIND, B_KS, T>, (long long)a.tiles_m * a.tiles_n, T::THREADS, 0, s, a);
 }
 
 template <int KIND, bool B_KS, class X>
-void launch_kind(const GroupedArgs &a, int cu_count, hipStream_t s)
+int launch_kind(const GroupedArgs &a, int cu_count, hipStream_t s)
 {
     using Large = FewTile<KIND, B_KS, X, 4, 2>;
     using Small = FewTile<KIND, B_KS, X, 8, 1>;
@@ -28,24 +28,22 @@ void launch_kind(const GroupedArgs &a, int cu_count, hipStream_t s)
     // columns, k = 4096: 10.4 / 12.0).
     constexpr long long least = KIND == kFewFp4 ? 1 : 4;
     const long long rows = (a.m + 15) / 16, used = rows > a.groups ? rows : a.m < a.groups ? a.m : a.groups;
-    if (used * ((a.n + Large::BN - 1) / Large::BN) < least * cu_count) launch_tile<KIND, B_KS, Small>(a, s);
-    else launch_tile<KIND, B_KS, Large>(a, s);
+    return used * ((a.n + Large::BN - 1) / Large::BN) < least * cu_count ? launch_tile<KIND, B_KS, Small>(a, s)
+                                                                         : launch_tile<KIND, B_KS, Large>(a, s);
 }
 
 }  // namespace
 
-void launch_few(const GroupedArgs &a, bool bf16, bool fp4, bool b_contiguous, int cu_count, hipStream_t s)
+int launch_few(const GroupedArgs &a, bool bf16, bool fp4, bool b_contiguous, int cu_count, hipStream_t s)
 {
-    if (fp4) {
-        if (bf16) launch_kind<kFewFp4, false, __bf16>(a, cu_count, s);
-        else launch_kind<kFewFp4, false, float>(a, cu_count, s);
-    } else if (b_contiguous) {
-        if (bf16) launch_kind<kFewBf16, false, __bf16>(a, cu_count, s);
-        else launch_kind<kFewF32, false, float>(a, cu_count, s);
-    } else {
-        if (bf16) launch_kind<kFewBf16, true, __bf16>(a, cu_count, s);
-        else launch_kind<kFewF32, true, float>(a, cu_count, s);
-    }
+    if (fp4)
+        return bf16 ? launch_kind<kFewFp4, false, __bf16>(a, cu_count, s)
+                    : launch_kind<kFewFp4, false, float>(a, cu_count, s);
+    if (b_contiguous)
+        return bf16 ? launch_kind<kFewBf16, false, __bf16>(a, cu_count, s)
+                    : launch_kind<kFewF32, false, float>(a, cu_count, s);
+    return bf16 ? launch_kind<kFewBf16, true, __bf16>(a, cu_count, s)
+                : launch_kind<kFewF32, true, float>(a, cu_count, s);
 }
 
 }  // namespace gemmf32

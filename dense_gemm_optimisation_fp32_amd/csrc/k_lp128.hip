@@ -5,11 +5,10 @@ namespace gemmf32 {
 
 using Tile = LpTile<128, 128, 2, 2, 2>;
 
-void launch_lp128(const GroupedArgs &a, const LpCall &c, hipStream_t s)
+int launch_lp128(const GroupedArgs &a, const LpCall &c, hipStream_t s)
 {
-    if (c.weight_grad) launch_lp_grad<Tile>(a, c, s);
-    else launch_lp<Tile>(a, c, s);
+    return c.weight_grad ? launch_lp_grad<Tile>(a, c, s) : launch_lp<Tile>(a, c, s);
 }
-void launch_lp128_unaligned(const GroupedArgs &a, const LpCall &c, hipStream_t s) { launch_lp_unaligned<Tile>(a, c, s); }
+int launch_lp128_unaligned(const GroupedArgs &a, const LpCall &c, hipStream_t s) { return launch_lp_unaligned<Tile>(a, c, s); }
 
 }  // namespace gemmf32

@@ -4,13 +4,13 @@
 
 namespace gemmf32 {
 
-void launch_lp64(const GroupedArgs &a, const LpCall &c, hipStream_t s) { launch_lp<LpTile<64, 128, 2, 2, 2>>(a, c, s); }
-void launch_lp64_ring(const GroupedArgs &a, const LpCall &c, hipStream_t s) { launch_lp<LpTile<64, 128, 2, 2, 3>>(a, c, s); }
-void launch_lp64_square(const GroupedArgs &a, const LpCall &c, hipStream_t s) { launch_lp<LpTile<64, 64, 2, 2, 4>>(a, c, s); }
+int launch_lp64(const GroupedArgs &a, const LpCall &c, hipStream_t s) { return launch_lp<LpTile<64, 128, 2, 2, 2>>(a, c, s); }
+int launch_lp64_ring(const GroupedArgs &a, const LpCall &c, hipStream_t s) { return launch_lp<LpTile<64, 128, 2, 2, 3>>(a, c, s); }
+int launch_lp64_square(const GroupedArgs &a, const LpCall &c, hipStream_t s) { return launch_lp<LpTile<64, 64, 2, 2, 4>>(a, c, s); }
 
-void launch_lp64_square_grad(const GroupedArgs &a, const LpCall &c, hipStream_t s)
+int launch_lp64_square_grad(const GroupedArgs &a, const LpCall &c, hipStream_t s)
 {
-    launch_lp_grad<LpTile<64, 64, 2, 2, 4>>(a, c, s);
+    return launch_lp_grad<LpTile<64, 64, 2, 2, 4>>(a, c, s);
 }
 
 }  // namespace gemmf32

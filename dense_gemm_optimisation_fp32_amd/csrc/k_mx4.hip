@@ -4,24 +4,20 @@
 
 namespace gemmf32 {
 
-void launch_mx4_quantize(const Mx4Args &a, bool bf16, bool columns, hipStream_t s)
+int launch_mx4_quantize(const Mx4Args &a, bool bf16, bool columns, hipStream_t s)
 {
     if (columns) {
         const long long grid = (long long)((a.rows + 63) / 64) * (a.kp / 128);
-        if (bf16) mx4_quantize_columns_kernel<__bf16><<<(unsigned)grid, 256, 0, s>>>(a);
-        else mx4_quantize_columns_kernel<float><<<(unsigned)grid, 256, 0, s>>>(a);
-    } else {
-        const long long grid = ((long long)a.rows * ((a.kp + 511) / 512) + 3) / 4;
-        if (bf16) mx4_quantize_rows_kernel<__bf16><<<(unsigned)grid, 256, 0, s>>>(a);
-        else mx4_quantize_rows_kernel<float><<<(unsigned)grid, 256, 0, s>>>(a);
+        return launch(bf16 ? mx4_quantize_columns_kernel<__bf16> : mx4_quantize_columns_kernel<float>, grid, 256, 0, s, a);
     }
+    const long long grid = ((long long)a.rows * ((a.kp + 511) / 512) + 3) / 4;
+    return launch(bf16 ? mx4_quantize_rows_kernel<__bf16> : mx4_quantize_rows_kernel<float>, grid, 256, 0, s, a);
 }
 
-void launch_mx4_dequantize(const Mx4Args &a, bool bf16, hipStream_t s)
+int launch_mx4_dequantize(const Mx4Args &a, bool bf16, hipStream_t s)
 {
     const long long grid = ((long long)a.rows * ((a.k + 511) / 512) + 3) / 4;
-    if (bf16) mx4_dequantize_kernel<__bf16><<<(unsigned)grid, 256, 0, s>>>(a);
-    else mx4_dequantize_kernel<float><<<(unsigned)grid, 256, 0, s>>>(a);
+    return launch(bf16 ? mx4_dequantize_kernel<__bf16> : mx4_dequantize_kernel<float>, grid, 256, 0, s, a);
 }
 
 }  // namespace gemmf32
