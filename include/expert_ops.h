@@ -27,6 +27,12 @@
  *    2^31, with m / 16 where an expert has 16 rows or fewer on average
  *    (GEMM_F32_ERR_INVALID_VALUE otherwise); the whole of A, B or C may be
  *    larger.
+ *  - A launch holds less than 2^32 threads, or the call is refused
+ *    (GEMM_F32_ERR_INVALID_VALUE): route takes up to 2^29 - 128 tokens, its
+ *    gradient 2^28 - 16; a 4-bit operand of rows of k columns has
+ *    rows ceil(k / 512) up to 2^26 - 4; a product's tiles of 16 rows (up to 16
+ *    rows an expert on average, else 64 or 128) and 32 to 128 columns, those
+ *    of empty experts among them, are below 2^24.
  *  - Errors: GEMM_F32_ERR_INVALID_VALUE (an argument outside the above),
  *    GEMM_F32_ERR_NO_DEVICE, GEMM_F32_ERR_UNSUPPORTED_DEVICE,
  *    GEMM_F32_ERR_HIP (a launch failed; gemm_f32_last_hip_error),

@@ -2,10 +2,13 @@
 count in 32 bits has to fit, or the call is refused before anything is
 launched (no GPU compute: without a device an accepted call ends at the device
 check)."""
+import subprocess
+
 import pytest
 import torch
 
 import dense_gemm_optimisation_fp32_amd as g
+from dense_gemm_optimisation_fp32_amd import build as b
 from dense_gemm_optimisation_fp32_amd import expert_ops as x
 
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not real")
@@ -42,3 +45,53 @@ def test_weight_gradient_workgroups_are_counted_in_32_bits(groups):
     workgroups an expert, also where it has one tile."""
     assert weight_grad(groups) == BAD
     assert weight_grad(1 << 16) == ACCEPTED
+
+
+def test_launches_hold_less_than_2_to_the_32_threads(tmp_path):
+    """HIP launches no more; csrc/launch.hpp in front of a runtime that only
+    writes down what it is asked to launch."""
+    src = tmp_path / "t.cpp"
+    src.write_text(r"""
+#include "launch.hpp"
+#include <cstdio>
+
+static long long threads_asked;
+static hipError_t answer = hipSuccess, recorded = hipSuccess;
+hipError_t hipLaunchKernel(const void *, dim3 grid, dim3 block, void **, size_t, hipStream_t)
+{
+    threads_asked = (long long)grid.x * block.x;
+    return answer;
+}
+namespace gemmf32 { int record_hip_error(hipError_t e) { recorded = e; return GEMM_F32_ERR_HIP; } }
+
+struct Args { int x; };
+static void kernel(Args) {}
+
+static int go(long long workgroups, int threads)
+{
+    threads_asked = 0;
+    return gemmf32::launch(kernel, workgroups, threads, 0, nullptr, Args{1});
+}
+
+int main()
+{
+    for (int threads : {256, 512, 1024}) {
+        const long long most = 0xffffffffll / threads;
+        int st = go(most, threads);
+        std::printf("%d %d ", st == GEMM_F32_SUCCESS, threads_asked == most * threads);
+        for (long long too_many : {most + 1, (1ll << 32) + 1, 1ll << 40}) {
+            st = go(too_many, threads);
+            std::printf("%d %d ", st == GEMM_F32_ERR_INVALID_VALUE, threads_asked == 0);
+        }
+    }
+    answer = hipErrorInvalidValue;
+    const int st = go(1, 64);
+    std::printf("%d %d", st == GEMM_F32_ERR_HIP, recorded == hipErrorInvalidValue);
+}
+""")
+    exe = tmp_path / "t"
+    r = subprocess.run(["g++", "-std=c++17", "-D__HIP_PLATFORM_AMD__", "-I", b.INCLUDE, "-I", b.CSRC, "-I", "/opt/rocm/include",
+                        "-o", str(exe), str(src)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    found = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
+    assert found == ["1"] * (3 * 8 + 2)
