@@ -193,6 +193,9 @@ PyObject *grouped_weight_grad(PyObject *const *args)
     const Tensor c = result(out, {groups, k, n}, a.scalar_type(), device);
     const int64_t ldd = k > 1 ? c.stride(1) : n;
     if ((n > 1 && c.stride(2) != 1) || ldd < n) wrong_value("out needs unit stride along its rows");
+    const int64_t se = c.stride(0);
+    if (groups > 1 && se < (k - 1) * ldd + n && (se < n || ldd < (groups - 1) * se + n))
+        wrong_value("out has overlapping experts");
     const int st = call(device, [&] {
         return ENTRY(WEIGHT_GRAD, expert_grouped_weight_grad)(dt, m, n, k, groups, a.const_data_ptr(), lda,
                                                               grad.const_data_ptr(), ldg, off, c.mutable_data_ptr(), ldd,

@@ -43,6 +43,14 @@ bool grad_ok(int64_t n, int64_t k, int64_t groups)
     return (tiles + 7) / 8 * 8 <= kMaxInt / groups;
 }
 
+// Whether the experts' k x n matrices share no element: one after the other,
+// or the experts' rows in turn.  (The workgroups of two experts would write to
+// the same place.)
+bool apart(int64_t n, int64_t k, int64_t groups, int64_t ld, int64_t stride)
+{
+    return groups == 1 || stride >= (k - 1) * ld + n || (stride >= n && ld >= (groups - 1) * stride + n);
+}
+
 // A workgroup of the routing kernels steps its slot counters by up to 1024 past
 // the last slot: more slots than this could wrap them.
 constexpr int64_t kMaxSlots = kMaxInt - 2047;
@@ -190,7 +198,7 @@ int expert_grouped_weight_grad(int dtype, int64_t m, int64_t n, int64_t k, int64
     if (!here(offsets, 4) || !here(dB, size) || (m > 0 && (!here(A, size) || !here(G, size))))
         return GEMM_F32_ERR_INVALID_VALUE;
     if (dtype == EXPERT_F32 && ((k - 1) * ldd + n) * size > kMaxInt - 3) return GEMM_F32_ERR_INVALID_VALUE;
-    if (!grad_ok(n, k, groups)) return GEMM_F32_ERR_INVALID_VALUE;
+    if (!apart(n, k, groups, ldd, expert_stride) || !grad_ok(n, k, groups)) return GEMM_F32_ERR_INVALID_VALUE;
     GroupedArgs a{};
     int cus = 0;
     const int st = current_device(&cus, &a.num_xcd);

@@ -69,6 +69,9 @@ int expert_grouped_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t gr
 /*
  * dB_e = A_e^T . G_e: A m x k, G m x n; dB: groups matrices k x n,
  * expert_stride apart, rows ldd apart, of dtype; zero for an empty expert.
+ * The experts share no element: their matrices lie one after the other
+ * (expert_stride >= (k - 1) ldd + n) or their rows in turn (expert_stride >= n,
+ * ldd >= (groups - 1) expert_stride + n).
  * ceil(k / 64) ceil(n / 64), rounded up to a multiple of 8, times groups is
  * below 2^31.
  */

@@ -95,3 +95,17 @@ int main()
     assert r.returncode == 0, r.stderr
     found = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
     assert found == ["1"] * (3 * 8 + 2)
+
+
+@pytest.mark.parametrize("stride,ldd,accepted", [
+    (512, 16, True), (600, 16, True), (16, 64, True), (20, 80, True), (16, 65, True),
+    (0, 16, False), (511, 16, False), (16, 16, False), (16, 63, False), (15, 64, False),
+])
+def test_weight_gradients_of_experts_do_not_overlap(stride, ldd, accepted):
+    """Four experts' 32 x 16 matrices one after the other, or their rows in turn."""
+    status = x._functions()["expert_grouped_weight_grad"](0, 8, 16, 32, 4, OK, 32, OK, 16, OK, OK, ldd, stride, None)
+    assert status == (ACCEPTED if accepted else BAD)
+
+
+def test_one_weight_gradient_needs_no_stride():
+    assert x._functions()["expert_grouped_weight_grad"](0, 8, 16, 32, 1, OK, 32, OK, 16, OK, OK, 16, 0, None) == ACCEPTED

@@ -46,3 +46,15 @@ def test_an_error_left_by_another_call_is_not_theirs():
         hip.hipGetLastError()
     assert left != 0
     assert all(torch.equal(p, q) for p, q in zip(want, got))
+
+
+def test_weight_gradients_that_overlap_are_refused():
+    a, off = torch.randn((8, 32), device=DEV), torch.tensor([0, 3, 5, 6, 8], dtype=torch.int32, device=DEV)
+    grad = torch.randn((8, 16), device=DEV)
+    with pytest.raises(ValueError, match="overlapping"):
+        g.grouped_weight_grad(a, grad, off, out=torch.empty((1, 32, 16), device=DEV).expand(4, 32, 16))
+    with pytest.raises(ValueError, match="overlapping"):
+        g.grouped_weight_grad(a, grad, off, out=torch.empty(4096, device=DEV).as_strided((4, 32, 16), (500, 16, 1)))
+    want = g.grouped_weight_grad(a, grad, off)
+    for out in (torch.empty((32, 4, 16), device=DEV).transpose(0, 1), torch.empty((4, 33, 17), device=DEV)[:, :32, :16]):
+        assert torch.equal(g.grouped_weight_grad(a, grad, off, out=out), want)
