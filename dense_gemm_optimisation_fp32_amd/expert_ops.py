@@ -34,7 +34,9 @@ EXPERT_FUNCTIONS = (
 
 _fns = None
 _module = None
-_raw_stream = torch._C._cuda_getCurrentRawStream     # current_stream(device).cuda_stream in a tenth of its time
+# current_stream(device).cuda_stream in a tenth of its time (None: a torch
+# without GPU support, which has no tensors to ask for).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _functions():
