@@ -145,16 +145,32 @@ def build(verbose: bool = False) -> str:
         _fail("link", p.stderr)
     os.replace(tmp, LIB_PATH)
 
-    # The Python module in front of the expert-layer entry points.
+    build_binding(verbose)
+    return LIB_PATH
+
+
+def build_binding(verbose: bool = False) -> None:
+    """The Python module in front of the expert-layer entry points.  The library
+    itself needs neither Python's nor torch's C++ headers: where they are not
+    installed it stays without the module, which the operators then name as
+    missing when they are called."""
     import torch
 
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     include = os.path.join(os.path.dirname(torch.__file__), "include")
+    python_include = sysconfig.get_paths()["include"]
+    missing = [h for h in (os.path.join(python_include, "Python.h"), os.path.join(include, "torch", "csrc", "Exceptions.h"))
+               if not os.path.exists(h)]
+    if missing:
+        if os.path.exists(BINDING_PATH):
+            os.remove(BINDING_PATH)
+        print(f"{os.path.basename(BINDING_PATH)} is not built: no {', '.join(missing)}", file=sys.stderr)
+        return
     tmp = BINDING_PATH + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_paths()["include"], "-o", tmp, BINDING_SOURCE,
+           "-isystem", python_include, "-o", tmp, BINDING_SOURCE,
            "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -162,7 +178,6 @@ def build(verbose: bool = False) -> str:
     if p.returncode != 0:
         _fail("expert_binding.cpp", p.stderr)
     os.replace(tmp, BINDING_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":
