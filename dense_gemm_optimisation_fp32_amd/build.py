@@ -1,4 +1,4 @@
-"""Build libgemm_f32.so, and the Python module _expert_binding.so in front of its
+"""Build libgemm_f32.so, and the Python module _expert_binding in front of its
 expert-layer entry points, in-tree with hipcc for gfx950.
 
 Usage: ``python -m dense_gemm_optimisation_fp32_amd.build`` (or call
@@ -29,7 +29,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libgemm_f32.so")
 BINDING_SOURCE = os.path.join(CSRC, "expert_binding.cpp")
-BINDING_PATH = os.path.join(PKG_DIR, "_expert_binding.so")
+BINDING_PATH = os.path.join(PKG_DIR, "_expert_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 HOST_SOURCES = [os.path.join(CSRC, "gemm_f32.hip"), os.path.join(CSRC, "expert_ops.hip")]
 

@@ -74,7 +74,7 @@ def _binding():
         try:
             from . import _expert_binding
         except ImportError as e:
-            raise RuntimeError("_expert_binding.so is not built or does not load; run __graft_entry__.build() or "
+            raise RuntimeError("_expert_binding is not built for this Python or does not load; run __graft_entry__.build() or "
                                "python -m dense_gemm_optimisation_fp32_amd.build") from e
         _expert_binding.bind(addresses)
         _module = _expert_binding

@@ -69,3 +69,11 @@ def test_build_of_the_library_needs_no_python_headers(stand_in_build, monkeypatc
     assert b.build() == b.LIB_PATH
     assert os.path.exists(b.LIB_PATH) and not os.path.exists(b.BINDING_PATH)
     assert "Python.h" in capsys.readouterr().err
+
+
+def test_binding_is_named_for_its_interpreter():
+    """Another version of Python does not load it (its types have another layout)."""
+    from importlib.machinery import EXTENSION_SUFFIXES
+
+    assert b.BINDING_PATH.endswith("_expert_binding" + EXTENSION_SUFFIXES[0])
+    assert sys.implementation.cache_tag.replace("-", "") in b.BINDING_PATH.replace("-", "")
