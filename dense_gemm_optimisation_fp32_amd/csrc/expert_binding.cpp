@@ -189,6 +189,7 @@ PyObject *grouped_weight_grad(PyObject *const *args)
     const at::Device device = a.device();
     on(device, grad, "grad");
     const int64_t groups = offsets.numel() - 1, m = a.size(0), k = a.size(1), n = grad.size(1);
+    if (groups < 1) wrong_value("offsets must be groups + 1 contiguous int32 values");
     const int *const off = offsets_of(offsets, groups, device);
     const Tensor c = result(out, {groups, k, n}, a.scalar_type(), device);
     const int64_t ldd = k > 1 ? c.stride(1) : n;

@@ -58,3 +58,11 @@ def test_weight_gradients_that_overlap_are_refused():
     want = g.grouped_weight_grad(a, grad, off)
     for out in (torch.empty((32, 4, 16), device=DEV).transpose(0, 1), torch.empty((4, 33, 17), device=DEV)[:, :32, :16]):
         assert torch.equal(g.grouped_weight_grad(a, grad, off, out=out), want)
+
+
+@pytest.mark.parametrize("offsets", [[], [0]])
+def test_weight_gradients_of_no_expert_are_refused(offsets):
+    """Two offsets are the least: ValueError, as for every wrong argument."""
+    a, off = torch.randn((8, 32), device=DEV), torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match="offsets"):
+        g.grouped_weight_grad(a, a, off)
