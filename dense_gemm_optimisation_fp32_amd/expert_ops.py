@@ -5,8 +5,12 @@ quantisation and products.
 Argument marshalling only, as in the package's ``matmul`` and ``linear`` (in C++,
 csrc/expert_binding.cpp, because the calls are short): every step runs in the
 library's HIP kernels on the current stream, results and workspaces come from
-PyTorch's allocator, wrong arguments raise ``TypeError`` or ``ValueError``, a
-failed call ``GemmF32Error``, and there is no fallback.
+PyTorch's allocator, and there is no fallback.  Wrong arguments raise
+``TypeError`` or ``ValueError``, an activation that there is not ``KeyError``;
+``GemmF32Error`` is what the library itself refuses (sizes outside the limits of
+expert_ops.h, more than 32 choices among them) or fails at.  Results carry no
+autograd history, whatever the operands' ``requires_grad``: the gradients are
+the calls below.
 
     r = g.route(logits, choices=2)                      # tokens -> experts
     a = x[r.order.clamp(min=0) // 2]                    # rows sorted by expert

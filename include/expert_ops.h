@@ -10,23 +10,25 @@
  *    (a hipStream_t; NULL = the null stream) and may be captured in a graph.
  *  - Pointers are device pointers of the current device, owned by the caller.
  *    Outputs overlap no other operand.  Operands of `dtype` EXPERT_F32 are
- *    4-byte, of EXPERT_BF16 2-byte aligned; int32, float and workspace
- *    pointers 4-byte, codes 16-byte aligned.
+ *    4-byte, of EXPERT_BF16 2-byte aligned; int32 and float pointers, scales
+ *    and route's workspace 4-byte, codes and expert_mx4_linear's workspace
+ *    16-byte aligned.
  *  - Sizes and leading dimensions are in elements; sums, softmax statistics
  *    and products are held in 32 bits; a result of dtype EXPERT_BF16 is
  *    rounded once.  The same call on the same inputs gives the same bits.
  *  - Rows sorted by expert: expert e owns rows offsets[e] .. offsets[e + 1] of
  *    A and C.  offsets holds groups + 1 int32, not decreasing, within 0 .. m;
  *    it is read on the device, where values outside are clamped (wrong
- *    offsets give wrong results, no access outside the operands).  Experts
- *    may be empty.  Rows before offsets[0] and from offsets[groups] on belong
+ *    offsets give wrong results or leave rows of C as they were, and access
+ *    nothing outside the operands).  Experts may be empty.  Rows before offsets[0] and from offsets[groups] on belong
  *    to no expert: their rows of C are zero.
- *  - m may be 0 (no rows); groups, n and k are at least 1.  One row of an
- *    operand is below 8 MiB, an expert's matrix and C's tile rows in 32-bit
- *    precision below 2 GiB, and (m / 64 + 1) (groups + 2) of a product below
- *    2^31, with m / 16 where an expert has 16 rows or fewer on average
- *    (GEMM_F32_ERR_INVALID_VALUE otherwise); the whole of A, B or C may be
- *    larger.
+ *  - m may be 0 (no rows); groups, n and k are at least 1; sizes are below
+ *    2^31.  One row of a product's operand is below 8 MiB, an expert's matrix
+ *    and C's tile rows in 32-bit precision below 2 GiB; the whole of A, B or C
+ *    may be larger.  Counted in 32 bits, so below 2^31: of a product
+ *    (m / 64 + 1) (groups + 2), with m / 16 where an expert has 16 rows or fewer
+ *    on average, and (m / 16 + groups + 2) ceil(n / 32); of a 4-bit operand
+ *    rows ceil(k / 32).
  *  - A launch holds less than 2^32 threads, or the call is refused
  *    (GEMM_F32_ERR_INVALID_VALUE): route takes up to 2^29 - 128 tokens, its
  *    gradient 2^28 - 16; a 4-bit operand of rows of k columns has
