@@ -20,8 +20,9 @@
  *    A and C.  offsets holds groups + 1 int32, not decreasing, within 0 .. m;
  *    it is read on the device, where values outside are clamped (wrong
  *    offsets give wrong results or leave rows of C as they were, and access
- *    nothing outside the operands).  Experts may be empty.  Rows before offsets[0] and from offsets[groups] on belong
- *    to no expert: their rows of C are zero.
+ *    nothing outside the operands).  Experts may be empty.  Rows before
+ *    offsets[0] and from offsets[groups] on belong to no expert: their rows
+ *    of C are zero.
  *  - m may be 0 (no rows); groups, n and k are at least 1; sizes are below
  *    2^31.  One row of a product's operand is below 8 MiB, an expert's matrix
  *    and C's tile rows in 32-bit precision below 2 GiB; the whole of A, B or C
