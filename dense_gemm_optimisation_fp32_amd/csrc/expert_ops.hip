@@ -64,8 +64,10 @@ constexpr int64_t kPipeGroups = 1022;
 // Whether the products of `rows` rows an expert take 256 x 256 tiles (one
 // workgroup a CU) rather than 128 x 128 (two): where a tile is mostly full and
 // there is a tile for every CU.  Measured, us, 16 experts, k = 2048, n = 4096,
-// 256 / 128: 128 rows 69 / 56, 256 rows 76 / 101, 1024 rows 259 / 334; 512
-// rows, k = n = 1024 (160 tiles) 32 / 24.
+// 256 / 128: 128 rows 59 / 53, 160 rows 67 / 89, 192 rows 66 / 92, 256 rows 70 /
+// 97, 1024 rows 259 / 334; rows uneven by a deviation of 0.3 in their logarithm:
+// 160 rows 62 / 85, 176 rows 92 / 90, 192 rows 92 / 109; 512 rows, k = n = 1024 (160
+// tiles) 32 / 24.
 bool large_tiles(int64_t rows, int64_t m, int64_t n, int64_t groups, int cus)
 {
     return rows >= 192 && groups <= kPipeGroups && (m / 256 + groups / 2 + 1) * ((n + 255) / 256) >= cus;
@@ -227,8 +229,9 @@ int expert_grouped_weight_grad(int dtype, int64_t m, int64_t n, int64_t k, int64
     // 14.8 / 17.3).
     if (groups * ((k + 63) / 64) * ((n + 63) / 64) <= cus) return launch_lp64_square_grad(a, c, s);
     // The larger tiles from 384 rows on, the length of the contraction, where there
-    // is one for every CU (k = 2048, n = 4096, 256 / 128: 256 rows 139 / 128 us, 512
-    // rows 194 / 208, 1024 rows 287 / 346).
+    // is one for every CU (k = 2048, n = 4096, 256 / 128, us: 256 rows 137 / 135, 352 rows
+    // 159 / 159, 384 rows 163 / 155, 416 rows 171 / 186, 512 rows 186 / 216, 1024 rows 287 /
+    // 346; uneven ones 384 rows 173 / 159, 416 rows 177 / 186: the two meet near 400).
     if (mean_rows(m, groups) >= 384 && groups * ((k + 255) / 256) * ((n + 255) / 256) >= cus)
         return launch_lp256(a, c, s);
     return launch_lp128(a, c, s);

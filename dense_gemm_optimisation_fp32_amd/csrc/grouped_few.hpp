@@ -24,7 +24,8 @@
 // wavefront waits for another.  Loads come back in order: the next iteration's
 // blocks of X are loaded ahead of its weights, else they would wait for those
 // (4 rows, 14336 columns, k = 4096: 11.9 us with the workgroup's rows quantised
-// together behind a barrier, 8.9 so).
+// together behind a barrier, 8.9 so).  16 rows over 8 experts of that size: 53 us,
+// 4.7 TB/s of 4-bit weights.
 //
 // Small calls are bound by latency: they take strips of 16 columns and eight
 // wavefronts, so that all of B is under way at once (see the launch).

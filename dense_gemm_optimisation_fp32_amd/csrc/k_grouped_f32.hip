@@ -17,7 +17,11 @@ using Tile64Ring = DmaTile<64, 64, 16, 2, 2, 4>;
 // half full.  Measured, 16 experts, us for 128 x 128 / 64 x 128 / 64 x 64: 5003
 // rows, k = 2049, n = 1027: 288 / 291 / 237 (B contiguous: 283 / 248 / 254);
 // 8192 rows, k = n = 1024: 139 / 134 / 146; 8 experts of 1024 rows, k = n =
-// 4096: 1982 / 2098 / 2207.
+// 4096: 1982 / 2098 / 2207.  Near 608 rows an expert the two larger tiles change
+// places with every step in the number of tiles, 128 x 128 / 64 x 128: k = 2048,
+// n = 4096, 576 rows 1185 / 1156, 608 rows 1190 / 1253, 640 rows 1206 / 1279, 704
+// rows 1420 / 1411, uneven experts 576 rows 1301 / 1247, 640 rows 1308 / 1327; k = n =
+// 1024, 608 rows 182 / 161, 704 rows 183 / 190, uneven 704 rows 244 / 198.
 int tile_of(int rows, int n) { return rows >= 608 ? 0 : n % 128 > 64 || n % 128 == 0 ? 1 : 2; }
 
 // Few tiles are bound by the latency of one slab after the other: 64 x 64 in four
@@ -61,7 +65,10 @@ int launch_f32_grouped(const GroupedArgs &a, bool b_contiguous, int cu_count, hi
 }
 
 // Here the expert's rows are the contraction: smaller tiles where it is short
-// (the same sizes, us: 250 / 241 / 239; 161 / 133 / 138; 1904 / 1946 / 1993).
+// (the same sizes, us: 250 / 241 / 239; 161 / 133 / 138; 1904 / 1946 / 1993).  By
+// rows an expert, 128 x 128 / 64 x 128: k = 2048, n = 4096, 512 rows 1003 / 1018, 608
+// rows 1164 / 1201, 704 rows 1336 / 1377; k = n = 1024, where the large tiles leave CUs
+// idle, 608 rows 186 / 156, 768 rows 231 / 193, uneven 170 / 168 and 208 / 207.
 int launch_f32_weight_grad(const GroupedArgs &a, int cu_count, hipStream_t s)
 {
     if (few_tiles(a.groups, a.k, a.n, cu_count)) return launch_grad<Tile64Ring>(a, s);

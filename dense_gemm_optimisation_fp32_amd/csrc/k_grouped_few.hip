@@ -21,9 +21,9 @@ int launch_kind(const GroupedArgs &a, int cu_count, hipStream_t s)
     using Small = FewTile<KIND, B_KS, X, 8, 1>;
     // Strips of the larger kind that there are about.  Few of them are bound by
     // latency, many by bandwidth (16 rows over 8 experts, 14336 columns, k =
-    // 4096, bfloat16: 137 us, 6.1 TB/s): fewer than four a CU take the smaller
-    // strips (2 of 8 experts, 4096 columns, k = 1024, 32 bits: 12.0 us with the
-    // larger, 8.9 so).  In 4 bits, where a strip also quantises its rows, fewer
+    // 4096, bfloat16: 137 to 157 us from card to card, 5.3 to 6.1 TB/s): fewer
+    // than four a CU take the smaller strips (2 of 8 experts, 4096 columns, k =
+    // 1024, 32 bits: 12.0 us with the larger, 8.9 so).  In 4 bits, where a strip also quantises its rows, fewer
     // than one a CU (4 rows, 4096 columns, k = 14336: 16.5 / 10.2 us; 14336
     // columns, k = 4096: 10.4 / 12.0).
     constexpr long long least = KIND == kFewFp4 ? 1 : 4;

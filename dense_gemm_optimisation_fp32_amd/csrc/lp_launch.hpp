@@ -1,6 +1,10 @@
 // Launches of the low-precision tile kernels for one tile shape (each
 // shape's translation unit instantiates it).  Operands whose rows are not
-// 4-byte aligned take the 128 x 128 tile's kernels with register copies.
+// 4-byte aligned take the 128 x 128 tile's kernels with register copies, whatever
+// their size: the three products of 8192 rows over 16 experts take 1310 us at
+// k = 2049, n = 4099 (410 + 357 + 543), 544 at 2048 x 4096 (178 + 173 + 193).  Of that,
+// C's stores of single elements cost where its rows are not whole 16 bytes: 955
+// at 2048 x 4098, where all copies are direct.
 #pragma once
 
 #include "expert_launch.hpp"

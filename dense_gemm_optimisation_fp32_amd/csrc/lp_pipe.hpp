@@ -13,15 +13,17 @@
 // instead of 128 bytes a row, four stages deep, 1054; 4 instead of 8
 // wavefronts 1046; touching lines two slabs ahead of their copies 1139.
 //
-// What bounds it: the matrix cores are busy two thirds of the time, and the
-// clock falls with the operands' bits (a library product of the same sizes
-// 1339 with normal values, 2062 with zeros; this kernel with one expert 1266
-// and 1406).  The rest is the copies: the same products without them ran at
-// 1331 and 1944 (n = 8192).  It is not LDS reads (a CU gave 215 bytes a cycle
-// of the 96 that a tile asks for), nor conflicts of banks (none counted), nor
-// the rate of the copies alone (64 bytes a cycle and CU, of which a tile
-// needs 32).  Rows that are not a power of two of bytes apart run 6 % faster
-// (k = 4160 for 4096).
+// What bounds it: by the counters (profiles/expert_layer_counters.md) the matrix
+// cores are busy 63 % of the time there, 50 and 44 % in the two products of a
+// training step of 8192 rows over 16 uneven experts (k = 2048, n = 4096), 40 % in
+// its weight gradient and 50 % in 4 bits (8192 rows, one matrix).  The clock falls
+// with the operands' bits (a library product of the same sizes 1339 with normal
+// values, 2062 with zeros; this kernel with one expert 1266 and 1406).  The
+// copies cost: the same products without them ran at 1331 and 1944 (n = 8192).
+// It is not LDS reads (LDS serves them a quarter of the time), nor conflicts of
+// banks (none counted).  One expert takes 1520 us, eight 1800: their half-empty
+// last tiles explain about 6 %, the rest is not explained.  Rows that are not a
+// power of two of bytes apart run 6 % faster (k = 4160 for 4096).
 //
 // Every slab issues the same number of copies, so one count of copies in
 // flight serves every wait: past the last tile they read nothing (a
