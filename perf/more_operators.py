@@ -213,9 +213,10 @@ def prepare(case, seed):
 def _quantised(x):
     """Scales and (as 32-bit numbers) codes of x's rows, x in 32 bits."""
     largest = x.abs().amax(1)
-    some = largest > 0
-    inverse = torch.where(some, 127.0 / largest, torch.zeros_like(largest))
-    return largest / 127.0, torch.round(x * inverse.unsqueeze(1))
+    # (Tensor by tensor: by a number, the division would be a product with a rounded inverse.)
+    most = torch.full_like(largest, 127.0)
+    inverse = torch.where(largest > 0, most / largest, torch.zeros_like(largest))
+    return largest / most, torch.round(x * inverse.unsqueeze(1))
 
 
 def _plain_pack(s):
