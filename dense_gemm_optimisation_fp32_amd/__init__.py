@@ -389,5 +389,6 @@ def linear(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor | None = None, a
 
 # The expert-layer operators (include/expert_ops.h).
 from .expert_ops import (  # noqa: E402
-    EXPERT_BF16, EXPERT_F32, EXPERT_FUNCTIONS, Mx4Tensor, Routing, grouped_linear, grouped_weight_grad,
-    mx4_dequantize, mx4_linear, mx4_quantize, route, route_grad)
+    EXPERT_BF16, EXPERT_F32, EXPERT_FUNCTIONS, EXPERT_SIGMOID, EXPERT_SOFTMAX, BalancedRouting, Int8Tensor, Mx4Tensor, Routing,
+    grouped_linear, grouped_weight_grad, int8_dequantize, int8_linear, int8_quantize, mx4_dequantize, mx4_linear, mx4_quantize,
+    orthogonalize, route, route_balanced, route_balanced_grad, route_grad)

@@ -1,0 +1,391 @@
+// Balanced routing: scores, a bias for the choice, sets of experts.
+//
+//   score    s = sigmoid(x), or softmax(x) over the token's experts.
+//   key      c = s + bias: what is chosen by.  An expert at x = -inf or NaN has
+//            none (-inf) and is never chosen.
+//   sets     groups / sets neighbouring experts each.  A set's value is the sum
+//            of its two largest keys (the one it has; -inf for none); the
+//            `kept` largest values stay, equal ones by the lower set.
+//   choose   the `choices` largest keys of those sets, equal ones by the lower
+//            expert.  weight_j = scale s_j / sum of the chosen s (normalize) or
+//            scale s_j.
+//   grad     sigmoid  d_j = w_j (1 - s_j) (g_j - dot)   (not normalize: no dot)
+//            softmax  d_j = w_j (g_j - dot)             (not normalize: below)
+//            dot = sum_j w_j g_j / scale, at the chosen experts, zero elsewhere;
+//            softmax as it is: d_e = (w g at the chosen) - s_e sum_j w_j g_j.
+//
+// The slots are then sorted as in route.hpp, by the same kernels.
+//
+// Scores and keys are 64-bit: which expert is chosen goes by differences of
+// scores, and in 32 bits the last bits of an exponential decided one choice in
+// about twenty thousand tokens (256 experts).
+//
+// A token is held by LANES lanes.  A set takes a power of two of them
+// (`lanes`), each `each` neighbouring experts, so that a set's two largest are
+// found by exchanges between its own lanes whatever its size; the lanes hold
+// the experts in order.
+#pragma once
+
+#include "route.hpp"
+
+namespace gemmf32 {
+
+struct BalanceArgs {
+    RouteArgs route;         // (normalize as there)
+    const float *bias;       // groups, or NULL
+    int softmax, sets, kept;
+    int lanes, each;         // lanes a set; experts a lane
+    float scale;
+};
+
+constexpr int kBalanceMaxSets = 64;
+
+__device__ __forceinline__ double no_key() { return -__builtin_inf(); }
+
+// x moved between lanes by a DPP control.
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double x)
+{
+    const u32x2 v = __builtin_bit_cast(u32x2, x);
+    const u32x2 r = {(unsigned)__builtin_amdgcn_update_dpp(0, (int)v.x, CTRL, 0xf, 0xf, true),
+                     (unsigned)__builtin_amdgcn_update_dpp(0, (int)v.y, CTRL, 0xf, 0xf, true)};
+    return __builtin_bit_cast(double, r);
+}
+
+// From the other half of 2 D lanes whose halves of D hold one value each (below
+// 4 lanes: lane by lane).
+template <int D>
+__device__ __forceinline__ double other_half(double x)
+{
+    if constexpr (D == 1) return dpp64<0xb1>(x);
+    else if constexpr (D == 2) return dpp64<0x4e>(x);
+    else if constexpr (D == 4) return dpp64<0x141>(x);
+    else if constexpr (D == 8) return dpp64<0x140>(x);
+    else return __shfl_xor(x, D);
+}
+
+template <int LANES>
+__device__ __forceinline__ double lanes_max(double x)
+{
+    x = fmax(x, other_half<1>(x));
+    x = fmax(x, other_half<2>(x));
+    x = fmax(x, other_half<4>(x));
+    x = fmax(x, other_half<8>(x));
+    if constexpr (LANES == 64) {
+        x = fmax(x, other_half<16>(x));
+        x = fmax(x, other_half<32>(x));
+    }
+    return x;
+}
+
+template <int LANES>
+__device__ __forceinline__ double lanes_sum(double x)
+{
+    x += other_half<1>(x);
+    x += other_half<2>(x);
+    x += other_half<4>(x);
+    x += other_half<8>(x);
+    if constexpr (LANES == 64) {
+        x += other_half<16>(x);
+        x += other_half<32>(x);
+    }
+    return x;
+}
+
+// The two largest of a set, as its lanes join.
+struct Two {
+    double first, second;
+
+    __device__ __forceinline__ void add(double x)
+    {
+        second = fmax(second, fmin(first, x));
+        first = fmax(first, x);
+    }
+    template <int D>
+    __device__ __forceinline__ void join()
+    {
+        const double f = other_half<D>(first), s = other_half<D>(second);
+        second = fmax(fmin(first, f), fmax(second, s));
+        first = fmax(first, f);
+    }
+};
+
+__device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
+
+// How many sets of the token come before this lane's.
+template <int N, int LANES>
+__device__ __forceinline__ int sets_before(double value, int set, int lanes)
+{
+    // Sets in other lanes of the row, from N lanes on.
+    int n = 0;
+    if constexpr (N < 16) {
+        if (N % lanes == 0) {
+            const double v = dpp64<0x120 + N>(value);
+            const int u = __builtin_amdgcn_update_dpp(0, set, 0x120 + N, 0xf, 0xf, true);
+            n = v > value || (v == value && u < set) ? 1 : 0;
+        }
+        n += sets_before<N + 1, LANES>(value, set, lanes);
+    }
+    return n;
+}
+
+// Chooses for the workgroup's tokens and counts the experts in LDS.  `found`
+// (LDS): `choices` experts for every LANES lanes.
+template <class E, int LANES, int V, int THREADS>
+__device__ __forceinline__ void balance_choose(const BalanceArgs &b, int first, int *counts, int *found)
+{
+    const RouteArgs &a = b.route;
+    constexpr int PER = 64 / LANES;                       // tokens a wavefront
+    const int lane = threadIdx.x & 63, sub = lane % LANES, group = lane / LANES;
+    const int last = min(first + kRouteTokens, a.tokens);
+    const int size = a.groups / b.sets;                   // experts of a set
+    const int set = sub / b.lanes, inner = sub % b.lanes * b.each;
+    const int e0 = set * size + inner;
+    const int count = set < b.sets ? max(0, min(b.each, size - inner)) : 0;
+    int *const mine = found + (threadIdx.x / LANES) * a.choices;
+    for (int t0 = first + (threadIdx.x >> 6) * PER; t0 < last; t0 += THREADS / LANES) {
+        const int token = t0 + group;
+        const bool live = token < last;
+        const E *const row = reinterpret_cast<const E *>(a.logits) + (long long)(live ? token : last - 1) * a.ld;
+        float x[V];
+        if constexpr (V % 8 == 0) {
+#pragma unroll
+            for (int i = 0; i < V; i += 8) {
+                float v[8];
+                load8(row + e0 + i, count - i, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[i + j] = i + j < count ? v[j] : -__builtin_inff();
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = i < count ? to_f32(row[e0 + i]) : -__builtin_inff();
+        }
+        // Scores, then keys.
+        double c[V], top = 0.0, sum = 1.0;
+        if (b.softmax) {
+            float most = -__builtin_inff();
+#pragma unroll
+            for (int i = 0; i < V; ++i) most = fmaxf(most, x[i]);
+            top = lanes_max<LANES>((double)most);
+            top = top > no_key() ? top : 0.0;
+            sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                c[i] = exp((double)x[i] - top);
+                sum += x[i] == x[i] ? c[i] : 0.0;
+            }
+            sum = lanes_sum<LANES>(sum);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                c[i] /= sum;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                c[i] = sigmoid64((double)x[i]);
+            }
+        }
+        // (Opaque: the biases would else be held in registers for all tokens.)
+        int eb = e0;
+        asm volatile("" : "+v"(eb));
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (b.bias) c[i] += (double)(i < count ? b.bias[eb + i] : 0.0f);
+            c[i] = x[i] > -__builtin_inff() && c[i] == c[i] ? c[i] : no_key();
+        }
+        if (b.kept < b.sets) {
+            Two two{no_key(), no_key()};
+#pragma unroll
+            for (int i = 0; i < V; ++i) two.add(c[i]);
+            if (b.lanes > 1) two.join<1>();
+            if (b.lanes > 2) two.join<2>();
+            if (b.lanes > 4) two.join<4>();
+            if (b.lanes > 8) two.join<8>();
+            if constexpr (LANES == 64) {
+                if (b.lanes > 16) two.join<16>();
+                if (b.lanes > 32) two.join<32>();
+            }
+            const double value = two.second > no_key() ? two.first + two.second : two.first;
+            int before = 0;
+            if constexpr (LANES == 16) {
+                before = sets_before<1, LANES>(value, set, b.lanes);
+            } else {
+                for (int u = 0; u < b.sets; ++u) {
+                    const double v = __shfl(value, u * b.lanes);
+                    before += v > value || (v == value && u < set) ? 1 : 0;
+                }
+            }
+            if (before >= b.kept)
+#pragma unroll
+                for (int i = 0; i < V; ++i) c[i] = no_key();
+        }
+        for (int j = 0; j < a.choices; ++j) {
+            double best = c[0];
+            int at = 0;
+#pragma unroll
+            for (int i = 1; i < V; ++i) {
+                const bool more = c[i] > best;
+                best = more ? c[i] : best;
+                at = more ? i : at;
+            }
+            const double m = lanes_max<LANES>(best);
+            const bool used = m > no_key();
+            const unsigned long long hit = __ballot(best == m);
+            int who;
+            if constexpr (LANES == 16) who = __builtin_ctz((unsigned)(hit >> (16 * group)) & 0xffffu);
+            else who = __builtin_ctzll(hit);
+            if (sub == who) {
+                mine[j] = used ? e0 + at : -1;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (i == at) c[i] = no_key();
+            }
+        }
+        wave_sync();
+        // A lane a slot (two past LANES choices); their scores again.
+        double w[2] = {};
+        int e[2] = {-1, -1};
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            if (sub + LANES * q < a.choices) {
+                e[q] = mine[sub + LANES * q];
+                if (e[q] >= 0) {
+                    const double v = (double)to_f32(row[e[q]]);
+                    w[q] = b.softmax ? exp(v - top) / sum : sigmoid64(v);
+                }
+            }
+        const double total = a.normalize ? lanes_sum<LANES>(w[0] + w[1]) : 1.0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int j = sub + LANES * q;
+            if (live && j < a.choices) {
+                const long long s = (long long)token * a.choices + j;
+                a.weights[s] = w[q] > 0.0 ? (float)(w[q] / total * (double)b.scale) : 0.0f;
+                a.experts[s] = e[q];
+                if (e[q] >= 0) atomicAdd(counts + e[q], 1);
+            }
+        }
+        wave_sync();
+    }
+}
+
+// LDS words for the choices found.
+constexpr int balance_found_words(int lanes, int threads, int choices) { return threads / lanes * choices; }
+
+// Every token in one workgroup: choose, count, place.
+template <class E, int LANES, int V>
+__global__ __launch_bounds__(kRouteThreads) void balance_one_kernel(BalanceArgs b)
+{
+    extern __shared__ int lds[];
+    const RouteArgs &a = b.route;
+    int *const base = lds, *const carry = lds + a.groups, *const held = lds + a.groups + 2;
+    for (int e = threadIdx.x; e < a.groups; e += kRouteThreads) base[e] = 0;
+    __syncthreads();
+    balance_choose<E, LANES, V, kRouteThreads>(b, 0, base, held);
+    // The chosen experts are read back by other lanes of this workgroup.
+    __threadfence_block();
+    __syncthreads();
+    route_offsets(a, base, carry, true);
+    if (a.groups <= 512) route_place<kRouteWaves>(a, 0, base, held);
+    else route_place<kRouteFewWaves>(a, 0, base, held);
+}
+
+// First of two launches (the second is route_place_kernel): choose and count.
+template <class E, int LANES, int V, int THREADS>
+__global__ __launch_bounds__(THREADS) void balance_choose_kernel(BalanceArgs b)
+{
+    extern __shared__ int lds[];
+    const RouteArgs &a = b.route;
+    for (int e = threadIdx.x; e < a.groups; e += THREADS) lds[e] = 0;
+    __syncthreads();
+    balance_choose<E, LANES, V, THREADS>(b, blockIdx.x * kRouteTokens, lds, lds + a.groups);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.groups; e += THREADS) a.counts[(long long)blockIdx.x * a.groups + e] = lds[e];
+}
+
+template <class E, int V>
+__global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(BalanceArgs b)
+{
+    // What each slot adds to its expert's gradient, for the 16 lanes that
+    // hold the token.
+    __shared__ Choice adds[kGradThreads / 16][kRouteMaxChoices];
+    const RouteArgs &a = b.route;
+    const int sub = threadIdx.x & 15;
+    const int token = blockIdx.x * (kGradThreads / 16) + (threadIdx.x >> 4);
+    if (token >= a.tokens) return;
+    Choice *const mine = adds[threadIdx.x >> 4];
+    const long long s0 = (long long)token * a.choices;
+    const E *const row = reinterpret_cast<const E *>(a.logits) + (long long)token * a.ld;
+    float w[2] = {}, g[2] = {};
+    int e[2] = {-1, -1};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int j = sub + 16 * q;
+        if (j < a.choices) {
+            e[q] = a.experts[s0 + j];
+            if (e[q] < 0 || e[q] >= a.groups) e[q] = -1;
+            w[q] = e[q] >= 0 ? a.weights[s0 + j] : 0.0f;
+            g[q] = e[q] >= 0 ? a.grad[s0 + j] : 0.0f;
+        }
+    }
+    const float dot = row_sum(w[0] * g[0] + w[1] * g[1]);        // scale times the mean gradient
+    const float mean = a.normalize ? dot / b.scale : 0.0f;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        if (sub + 16 * q < a.choices) {
+            float d = w[q] * (g[q] - mean);
+            // 1 - s = sigmoid(-x), without the difference of two near ones.
+            if (!b.softmax && e[q] >= 0) d /= 1.0f + expf(to_f32(row[e[q]]));
+            mine[sub + 16 * q] = Choice{d, e[q]};
+        }
+    float d[V];
+    if (b.softmax && !a.normalize) {
+        float x[V], top = -__builtin_inff(), sum = 0.0f;
+        route_load<E, V>(a, token, sub, x);
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = fmaxf(top, x[i]);
+        top = row_max(top);
+        top = top > -__builtin_inff() ? top : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i] = expf(x[i] - top);
+            sum += x[i];
+        }
+        sum = row_sum(sum);
+        const float each = sum > 0.0f ? dot / sum : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = -x[i] * each;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = 0.0f;
+    }
+    wave_sync();
+    for (int j = 0; j < a.choices; ++j) {
+        const Choice c = mine[j];
+        const int i0 = c.expert - sub * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (c.expert >= 0 && i == i0) d[i] += c.logit;
+    }
+    E *p = reinterpret_cast<E *>(a.dlogits) + (long long)token * a.ldd + sub * V;
+    const int left = a.groups - sub * V;
+    constexpr int N = 16 / sizeof(E);                       // elements of a 16-byte store
+    struct __attribute__((packed, aligned(sizeof(E)))) Some {
+        E e[N];
+    };
+#pragma unroll
+    for (int i0 = 0; i0 < V; i0 += N) {
+        if (V % N == 0 && left >= i0 + N) {
+            Some t;
+#pragma unroll
+            for (int i = 0; i < N; ++i) t.e[i] = (E)d[(i0 + i) % V];
+            *reinterpret_cast<Some *>(p + i0) = t;
+        } else {
+#pragma unroll
+            for (int i = i0; i < i0 + N && i < V; ++i)
+                if (i < left) p[i] = (E)d[i];
+        }
+    }
+}
+
+}  // namespace gemmf32

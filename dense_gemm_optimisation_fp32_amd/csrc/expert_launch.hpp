@@ -8,7 +8,11 @@
 
 namespace gemmf32 {
 
+struct BalanceArgs;
+struct Int8Args;
 struct Mx4Args;
+struct OrthoArgs;
+struct OrthoStartArgs;
 struct RouteArgs;
 
 // Bound on the row tiles of bm rows: each run of rows (the experts' and the
@@ -35,6 +39,14 @@ struct LpCall {
     int cu_count;
 };
 
+// Which of a tile shape's orthogonalising products a call takes: X X^T and A A,
+// B X, the last B X, or its transposed.
+enum OrthoProduct { kOrthoGram, kOrthoStep, kOrthoLast, kOrthoTurned };
+struct OrthoCall {
+    OrthoProduct what;
+    bool bf16, wide;        // of the result
+};
+
 // Status of the current device (a gemm_f32_status) and its facts.  In
 // gemm_f32.hip.
 int current_device(int *cu_count, int *num_xcd);
@@ -54,5 +66,20 @@ int launch_lp128_unaligned(const GroupedArgs &a, const LpCall &c, hipStream_t s)
 // Few rows an expert: tiles of 16 rows.
 int launch_few(const GroupedArgs &a, bool bf16, bool fp4, bool b_contiguous, int cu_count, hipStream_t s);
 int launch_route(const RouteArgs &a, bool bf16, bool grad, hipStream_t s);
+int launch_balance(const BalanceArgs &b, bool bf16, bool grad, hipStream_t s);
+int launch_int8_quantize(const Int8Args &a, bool bf16, bool columns, hipStream_t s);
+int launch_int8_dequantize(const Int8Args &a, bool bf16, hipStream_t s);
+// 8-bit products, by tile as above.
+int launch_int8_256(GroupedArgs a, const LpCall &c, hipStream_t s);
+int launch_int8_128(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+int launch_int8_64(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+int launch_int8_64_ring(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+int launch_int8_64_square(const GroupedArgs &a, const LpCall &c, hipStream_t s);
+int launch_int8_few(const GroupedArgs &a, bool bf16, int cu_count, hipStream_t s);
+int launch_ortho_start(const OrthoStartArgs &a, bool bf16, int batch, hipStream_t s);
+int launch_ortho_64_square(const OrthoArgs &a, const OrthoCall &c, hipStream_t s);
+int launch_ortho_64(const OrthoArgs &a, const OrthoCall &c, hipStream_t s);
+int launch_ortho_128(const OrthoArgs &a, const OrthoCall &c, hipStream_t s);
+int launch_ortho_256(const OrthoArgs &a, const OrthoCall &c, hipStream_t s);
 
 }  // namespace gemmf32

@@ -2,8 +2,13 @@
 // kernel, and its launch.  No kernel is compiled in this unit.
 #include "expert_ops.h"
 
+#include <cmath>
+
+#include "balance.hpp"
 #include "expert_launch.hpp"
+#include "int8.hpp"
 #include "mx4.hpp"
+#include "orthogonal.hpp"
 #include "route.hpp"
 
 using namespace gemmf32;
@@ -131,6 +136,105 @@ bool counts_ok(int64_t m, int64_t groups)
 {
     const int64_t least = mean_rows(m, groups) <= kFewRows ? 16 : 64;      // rows of a tile
     return m / least + 1 <= kMaxInt / (groups + 2);
+}
+
+// Longest contraction of 8-bit products: 127 * 127 * k stays below 2^31.
+constexpr int64_t kInt8MaxK = 131072;
+
+int64_t padded16(int64_t k) { return (k + 15) / 16 * 16; }
+
+// The 8-bit tiles of `rows` rows an expert, by launch_tiles' rules (an
+// instruction takes as long, and a slab has as many bytes).
+int launch_int8_tiles(const GroupedArgs &a, const LpCall &c, int64_t rows, hipStream_t s)
+{
+    if (tiles_of(a, rows, 64, 64) <= c.cu_count) return launch_int8_64_square(a, c, s);
+    if (tiles_of(a, rows, 64, 128) <= 2 * c.cu_count) return launch_int8_64_ring(a, c, s);
+    if (rows <= kSmallTileRows) return launch_int8_64(a, c, s);
+    if (large_tiles(rows, a.m, a.n, a.groups, c.cu_count)) return launch_int8_256(a, c, s);
+    return launch_int8_128(a, c, s);
+}
+
+// --- orthogonalising -----------------------------------------------------------
+
+int64_t padded64(int64_t k) { return (k + 63) / 64 * 64; }
+
+constexpr int kOrthoParts = 64;            // workgroups that sum a matrix's squares, at most
+constexpr int kOrthoMaxSteps = 64;
+constexpr int64_t kOrthoSpace = (int64_t)2 << 30;
+constexpr double kOrthoMost = 31.0;        // of a plane's entries
+
+// How a batch is worked on: its planes, and as many matrices at a time as 2 GiB
+// hold (one at least).
+struct OrthoPlan {
+    int64_t m, n, m_pad, n_pad;            // m <= n
+    int planes;                            // of A and B
+    int64_t x_plane, g_plane;              // bytes
+    int64_t matrix;                        // bytes of workspace a matrix
+    int64_t chunk;
+
+    OrthoPlan(int dtype, int64_t batch, int64_t rows, int64_t cols)
+    {
+        m = rows < cols ? rows : cols;
+        n = rows < cols ? cols : rows;
+        m_pad = padded64(m);
+        n_pad = padded64(n);
+        planes = dtype == EXPERT_BF16 ? 1 : 2;
+        x_plane = m_pad * n_pad * 2;
+        g_plane = m_pad * m_pad * 2;
+        matrix = 4 * x_plane + 2 * planes * g_plane + kOrthoParts * 8;
+        chunk = kOrthoSpace / matrix;
+        chunk = chunk < 1 ? 1 : chunk > batch ? batch : chunk;
+    }
+};
+
+bool ortho_sizes_ok(int dtype, int64_t batch, int64_t rows, int64_t cols)
+{
+    const int64_t most = rows < cols ? cols : rows;
+    return dtype_ok(dtype) && size_ok(batch, 0) && size_ok(rows, 1) && size_ok(cols, 1) && padded64(most) * 2 < kMaxRowBytes;
+}
+
+// Whether what the steps make of singular values of 0 .. 1 keeps the entries that
+// planes hold, of X, A and B, below kOrthoMost (an entry is at most the largest singular value).
+bool ortho_bounded(const float *coefficients, int steps)
+{
+    double top = 1.0;
+    for (int i = 0; i < steps; ++i) {
+        const double a = coefficients[3 * i], b = coefficients[3 * i + 1], c = coefficients[3 * i + 2];
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
+        const double end = top * top;
+        const auto q = [&](double u) { return std::fabs(a + b * u + c * u * u); };
+        // B: a + b u + c u^2, largest at an end or where b + 2 c u = 0.
+        double most = std::fmax(q(0.0), q(end));
+        const double turn = c != 0.0 ? -b / (2.0 * c) : -1.0;
+        if (turn > 0.0 && turn < end) most = std::fmax(most, q(turn));
+        // X: sqrt(u) (a + b u + c u^2), largest at the end or where a + 3 b u + 5 c u^2 = 0.
+        double next = top * q(end);
+        const double root = 9.0 * b * b - 20.0 * a * c;
+        if (c != 0.0 && root >= 0.0) {
+            for (double sign : {-1.0, 1.0}) {
+                const double u = (-3.0 * b + sign * std::sqrt(root)) / (10.0 * c);
+                if (u > 0.0 && u < end) next = std::fmax(next, std::sqrt(u) * q(u));
+            }
+        } else if (c == 0.0 && b != 0.0) {
+            const double u = -a / (3.0 * b);
+            if (u > 0.0 && u < end) next = std::fmax(next, std::sqrt(u) * q(u));
+        }
+        // (The last step's X is the result, in its own type.)
+        if (!(end < kOrthoMost && most < kOrthoMost && (next < kOrthoMost || i + 1 == steps))) return false;
+        top = next * 1.001;                // (rounding)
+    }
+    return true;
+}
+
+int launch_ortho(const OrthoArgs &a, const OrthoCall &c, int cus, hipStream_t s)
+{
+    const auto tiles = [&](int64_t bm, int64_t bn) {
+        return (int64_t)a.batch * ((a.rows + bm - 1) / bm) * ((a.cols + bn - 1) / bn);
+    };
+    if (tiles(64, 64) <= cus) return launch_ortho_64_square(a, c, s);
+    if (tiles(64, 128) <= 2 * cus) return launch_ortho_64(a, c, s);
+    if (tiles(256, 256) >= cus) return launch_ortho_256(a, c, s);
+    return launch_ortho_128(a, c, s);
 }
 
 }  // namespace
@@ -394,6 +498,312 @@ int expert_route_grad(int dtype, int64_t tokens, int64_t groups, int64_t choices
     a.dlogits = dlogits;
     a.ldd = ldd;
     return launch_route(a, dtype == EXPERT_BF16, true, stream_of(stream));
+}
+
+int64_t expert_route_balanced_workspace(int64_t tokens, int64_t groups)
+{
+    if (!size_ok(tokens, 1) || !size_ok(groups, 1) || (tokens <= kRouteTokens && groups <= 256)) return 0;
+    return (tokens + kRouteTokens - 1) / kRouteTokens * groups * 4;
+}
+
+int expert_route_balanced(int dtype, int64_t tokens, int64_t groups, int64_t choices, int scores, int64_t sets,
+                          int64_t kept_sets, int normalize, float scale, const void *logits, int64_t ld,
+                          const float *bias, float *weights, int *experts, int *offsets, int *order, void *workspace,
+                          int64_t workspace_bytes, void *stream)
+{
+    if (!dtype_ok(dtype) || !size_ok(tokens, 0) || groups < 1 || groups > kRouteMaxExperts || sets < 1 ||
+        sets > kBalanceMaxSets || groups % sets != 0 || kept_sets < 1 || kept_sets > sets || choices < 1 ||
+        choices > groups / sets * kept_sets || choices > kRouteMaxChoices || tokens * choices > kMaxSlots || ld < groups ||
+        (scores != EXPERT_SIGMOID && scores != EXPERT_SOFTMAX) || (normalize != 0 && normalize != 1) ||
+        !(scale > 0.0f && std::isfinite(scale)) || !here(offsets, 4) || (bias && !aligned(bias, 4)))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (tokens > 0 && (!here(logits, elem(dtype)) || !here(weights, 4) || !here(experts, 4) || !here(order, 4)))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    const int64_t need = expert_route_balanced_workspace(tokens, groups);
+    if (need > 0 && !here(workspace, 4)) return GEMM_F32_ERR_INVALID_VALUE;
+    if (workspace_bytes < need) return GEMM_F32_ERR_SCRATCH_TOO_SMALL;
+    const int st = current_device(nullptr, nullptr);
+    if (st != GEMM_F32_SUCCESS) return st;
+    BalanceArgs b{};
+    b.route.logits = logits;
+    b.route.ld = ld;
+    b.route.weights = weights;
+    b.route.experts = experts;
+    b.route.offsets = offsets;
+    b.route.order = order;
+    b.route.counts = static_cast<int *>(workspace);
+    b.route.tokens = (int)tokens;
+    b.route.groups = (int)groups;
+    b.route.choices = (int)choices;
+    b.route.normalize = normalize;
+    // No token: the offsets alone, as of any other call.
+    if (tokens == 0) return launch_route(b.route, dtype == EXPERT_BF16, false, stream_of(stream));
+    b.bias = bias;
+    b.softmax = scores == EXPERT_SOFTMAX;
+    b.sets = (int)sets;
+    b.kept = (int)kept_sets;
+    b.scale = scale;
+    return launch_balance(b, dtype == EXPERT_BF16, false, stream_of(stream));
+}
+
+int expert_route_balanced_grad(int dtype, int64_t tokens, int64_t groups, int64_t choices, int scores, int normalize,
+                               float scale, const void *logits, int64_t ld, const float *weights, const int *experts,
+                               const float *grad, void *dlogits, int64_t ldd, void *stream)
+{
+    if (!dtype_ok(dtype) || !size_ok(tokens, 0) || groups < 1 || groups > kRouteMaxExperts || choices < 1 ||
+        choices > groups || choices > kRouteMaxChoices || tokens * choices > kMaxInt || ld < groups || ldd < groups ||
+        (scores != EXPERT_SIGMOID && scores != EXPERT_SOFTMAX) || (normalize != 0 && normalize != 1) ||
+        !(scale > 0.0f && std::isfinite(scale)))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (tokens > 0 && (!here(logits, elem(dtype)) || !here(weights, 4) || !here(experts, 4) || !here(grad, 4) ||
+                       !here(dlogits, elem(dtype))))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    const int st = current_device(nullptr, nullptr);
+    if (st != GEMM_F32_SUCCESS) return st;
+    if (tokens == 0) return GEMM_F32_SUCCESS;
+    BalanceArgs b{};
+    b.route.logits = logits;
+    b.route.ld = ld;
+    b.route.weights = const_cast<float *>(weights);
+    b.route.experts = const_cast<int *>(experts);
+    b.route.tokens = (int)tokens;
+    b.route.groups = (int)groups;
+    b.route.choices = (int)choices;
+    b.route.normalize = normalize;
+    b.route.grad = grad;
+    b.route.dlogits = dlogits;
+    b.route.ldd = ldd;
+    b.softmax = scores == EXPERT_SOFTMAX;
+    b.scale = scale;
+    return launch_balance(b, dtype == EXPERT_BF16, true, stream_of(stream));
+}
+
+int expert_int8_quantize(int dtype, int64_t rows, int64_t k, const void *X, int layout, int64_t ld, void *codes,
+                         float *scales, void *stream)
+{
+    if (!dtype_ok(dtype) || !layout_ok(layout) || !size_ok(rows, 0) || !size_ok(k, 1) || k > kMaxInt - 1024 ||
+        ld < (layout == GEMM_F32_COL_MAJOR ? rows : k))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (rows > 0 && (!here(X, elem(dtype)) || !here(codes, 16) || !here(scales, 4))) return GEMM_F32_ERR_INVALID_VALUE;
+    const int st = current_device(nullptr, nullptr);
+    if (st != GEMM_F32_SUCCESS) return st;
+    if (rows == 0) return GEMM_F32_SUCCESS;
+    const Int8Args a{static_cast<const char *>(X), static_cast<char *>(codes), scales, ld, (int)rows, (int)k, (int)padded16(k)};
+    return launch_int8_quantize(a, dtype == EXPERT_BF16, layout == GEMM_F32_COL_MAJOR, stream_of(stream));
+}
+
+int expert_int8_dequantize(int dtype, int64_t rows, int64_t k, const void *codes, const float *scales, void *X,
+                           int64_t ld, void *stream)
+{
+    if (!dtype_ok(dtype) || !size_ok(rows, 0) || !size_ok(k, 1) || k > kMaxInt - 1024 || ld < k)
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (rows > 0 && (!here(X, elem(dtype)) || !here(codes, 16) || !here(scales, 4))) return GEMM_F32_ERR_INVALID_VALUE;
+    const int st = current_device(nullptr, nullptr);
+    if (st != GEMM_F32_SUCCESS) return st;
+    if (rows == 0) return GEMM_F32_SUCCESS;
+    const Int8Args a{static_cast<const char *>(X), static_cast<char *>(const_cast<void *>(codes)), const_cast<float *>(scales), ld,
+                     (int)rows, (int)k, (int)padded16(k)};
+    return launch_int8_dequantize(a, dtype == EXPERT_BF16, stream_of(stream));
+}
+
+int64_t expert_int8_workspace(int64_t m, int64_t k)
+{
+    if (!size_ok(m, 1) || !size_ok(k, 1)) return 0;
+    // X's codes and scales.
+    return m * (padded(k) + 4);
+}
+
+int expert_int8_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups, const void *X, int64_t ldx,
+                       const void *codes, const float *scales, const int *offsets, const float *bias, int activation,
+                       void *Y, int64_t ldy, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (!dtype_ok(dtype) || !size_ok(m, 0) || !size_ok(n, 1) || !size_ok(k, 1) || k > kInt8MaxK || !size_ok(groups, 1) ||
+        ldx < k || ldy < n || activation < 0 || activation > 2 || (!offsets && groups != 1))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    const int64_t size = elem(dtype), kp = padded16(k), kpx = padded(k);
+    if (ldx * size >= kMaxRowBytes || ldy * size >= kMaxRowBytes) return GEMM_F32_ERR_INVALID_VALUE;
+    if ((offsets && !aligned(offsets, 4)) || !here(codes, 16) || !here(scales, 4) || (bias && !aligned(bias, 4)) ||
+        (m > 0 && (!here(X, size) || !here(Y, size))))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (!grid_ok(m, n, 16, 16, groups + 2) || !counts_ok(m, groups)) return GEMM_F32_ERR_INVALID_VALUE;
+    const int64_t need = expert_int8_workspace(m, k);
+    if (need > 0 && !here(workspace, 16)) return GEMM_F32_ERR_INVALID_VALUE;
+    if (workspace_bytes < need) return GEMM_F32_ERR_SCRATCH_TOO_SMALL;
+    GroupedArgs a{};
+    int cus = 0;
+    const int st = current_device(&cus, &a.num_xcd);
+    if (st != GEMM_F32_SUCCESS) return st;
+    if (m == 0) return GEMM_F32_SUCCESS;
+    char *const xc = static_cast<char *>(workspace);
+    float *const xs = reinterpret_cast<float *>(xc + m * kpx);
+    a.A = xc;
+    a.B = static_cast<const char *>(codes);
+    a.C = static_cast<char *>(Y);
+    a.a_scales = reinterpret_cast<const u8 *>(xs);
+    a.b_scales = reinterpret_cast<const u8 *>(scales);
+    a.bias = bias;
+    a.offsets = offsets;
+    a.m = (int)m;
+    a.n = (int)n;
+    a.k = (int)k;
+    a.groups = (int)groups;
+    a.lda = kpx;
+    a.ldb = kp;
+    a.ldc = ldy * size;
+    a.expert_stride = n * kp;
+    a.bias_stride = n;
+    a.group_m = 8;
+    a.act = activation;
+    a.a_kblocks = (int)(kpx / 128);
+    const hipStream_t s = stream_of(stream);
+    const bool bf16 = dtype == EXPERT_BF16;
+    const int64_t rows = mean_rows(m, groups);
+    const int quantised =
+        launch_int8_quantize(Int8Args{static_cast<const char *>(X), xc, xs, ldx, (int)m, (int)k, (int)kpx}, bf16, false, s);
+    if (quantised != GEMM_F32_SUCCESS) return quantised;
+    if (few_rows(false, true, rows, n, groups, cus)) return launch_int8_few(a, bf16, cus, s);
+    const LpCall c{false, bf16, true, false, wide_rows(Y, a.ldc, n, size), cus};
+    return launch_int8_tiles(a, c, rows, s);
+}
+
+int64_t expert_orthogonalize_workspace(int dtype, int64_t batch, int64_t rows, int64_t cols)
+{
+    if (!ortho_sizes_ok(dtype, batch, rows, cols) || batch == 0) return 0;
+    const OrthoPlan p(dtype, batch, rows, cols);
+    return p.chunk * p.matrix;
+}
+
+int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, const void *X, int64_t ldx,
+                         int64_t stride_x, int steps, const float *coefficients, float scale, void *Y, int64_t ldy,
+                         int64_t stride_y, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (!ortho_sizes_ok(dtype, batch, rows, cols) || ldx < cols || ldy < cols || stride_x < 0 || steps < 1 ||
+        steps > kOrthoMaxSteps || !coefficients || !std::isfinite(scale) || !ortho_bounded(coefficients, steps))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    const int64_t size = elem(dtype);
+    if (ldx * size >= kMaxRowBytes || ldy * size >= kMaxRowBytes) return GEMM_F32_ERR_INVALID_VALUE;
+    if (batch > 1 && (stride_y < (rows - 1) * ldy + cols)) return GEMM_F32_ERR_INVALID_VALUE;
+    if (batch > 0 && (!here(X, size) || !here(Y, size))) return GEMM_F32_ERR_INVALID_VALUE;
+    const OrthoPlan p(dtype, batch, rows, cols);
+    // Workgroups, of 64 x 64 at least, are counted in 32 bits.
+    if (p.m_pad / 64 > kMaxInt / (p.n_pad / 64) || p.m_pad / 64 * (p.n_pad / 64) > kMaxInt / (p.chunk ? p.chunk : 1))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    const int64_t need = expert_orthogonalize_workspace(dtype, batch, rows, cols);
+    if (need > 0 && !here(workspace, 16)) return GEMM_F32_ERR_INVALID_VALUE;
+    if (workspace_bytes < need) return GEMM_F32_ERR_SCRATCH_TOO_SMALL;
+    int cus = 0, num_xcd = 0;
+    const int st = current_device(&cus, &num_xcd);
+    if (st != GEMM_F32_SUCCESS) return st;
+    const hipStream_t s = stream_of(stream);
+    const bool bf16 = dtype == EXPERT_BF16, turned = rows > cols;
+    for (int64_t first = 0; first < batch; first += p.chunk) {
+        const int64_t here_ = batch - first < p.chunk ? batch - first : p.chunk;
+        char *const x0 = static_cast<char *>(workspace), *const x1 = x0 + p.chunk * 2 * p.x_plane;
+        char *const g0 = x1 + p.chunk * 2 * p.x_plane, *const g1 = g0 + p.chunk * p.planes * p.g_plane;
+        OrthoStartArgs o{};
+        o.x = static_cast<const char *>(X) + first * stride_x * size;
+        o.ld = ldx;
+        o.stride = stride_x;
+        o.rows = (int)rows;
+        o.cols = (int)cols;
+        o.m_pad = (int)p.m_pad;
+        o.n_pad = (int)p.n_pad;
+        o.turned = turned;
+        const int64_t parts = (rows * ((cols + 7) / 8) + 1023) / 1024;       // four chunks of eight a thread
+        o.parts = (int)(parts < kOrthoParts ? parts : kOrthoParts);
+        o.sums = reinterpret_cast<double *>(g1 + p.chunk * p.planes * p.g_plane);
+        o.planes = x0;
+        o.plane = p.x_plane;
+        o.matrix = 2 * p.x_plane;
+        int status = launch_ortho_start(o, bf16, (int)here_, s);
+        if (status != GEMM_F32_SUCCESS) return status;
+
+        OrthoArgs gram{};                                                    // A = X X^T
+        gram.a_stride = gram.b_stride = 2 * p.x_plane;
+        gram.c_stride = p.planes * p.g_plane;
+        gram.lda = gram.ldb = (int)(p.n_pad * 2);
+        gram.a_bytes = gram.b_bytes = 2 * p.x_plane;
+        gram.k = (int)p.n_pad;
+        gram.rows = gram.cols = (int)p.m_pad;
+        gram.group_m = 8;
+        gram.batch = (int)here_;
+        gram.num_xcd = num_xcd;
+        gram.segments = p.planes == 2 ? 3 : 1;
+        gram.b_second = gram.a_third = p.x_plane;
+        gram.C = g0;
+        gram.ldc = p.m_pad * 2;
+        gram.c_plane = p.g_plane;
+        gram.c_planes = p.planes;
+        gram.c = kPlaneBack;
+
+        OrthoArgs poly = gram;                                               // B = a I + b A + c A A
+        poly.A = poly.B = poly.G = g0;
+        poly.a_stride = poly.b_stride = p.planes * p.g_plane;
+        poly.lda = poly.ldb = (int)(p.m_pad * 2);
+        poly.a_bytes = poly.b_bytes = p.planes * p.g_plane;
+        poly.k = (int)p.m_pad;
+        poly.b_second = poly.a_third = p.g_plane;
+        poly.C = g1;
+        poly.order = (int)p.m;
+
+        OrthoArgs step = poly;                                               // B X
+        step.G = nullptr;
+        step.A = g1;
+        step.b_stride = step.c_stride = 2 * p.x_plane;
+        step.ldb = (int)(p.n_pad * 2);
+        step.b_bytes = 2 * p.x_plane;
+        step.segments = p.planes == 2 ? 3 : 2;
+        step.b_second = p.x_plane;
+        step.cols = (int)p.n_pad;
+        step.ldc = p.n_pad * 2;
+        step.c_plane = p.x_plane;
+        step.c_planes = 2;
+        step.c = kPlaneBack;
+
+        char *now = x0, *then = x1;
+        for (int i = 0; i < steps; ++i) {
+            const float *const f = coefficients + 3 * i;
+            gram.A = gram.B = now;
+            status = launch_ortho(gram, OrthoCall{kOrthoGram, bf16, true}, cus, s);
+            if (status != GEMM_F32_SUCCESS) return status;
+            poly.a = f[0] * kPlaneScale;
+            poly.b = f[1];
+            poly.c = f[2] * kPlaneBack;
+            status = launch_ortho(poly, OrthoCall{kOrthoGram, bf16, true}, cus, s);
+            if (status != GEMM_F32_SUCCESS) return status;
+            if (i + 1 < steps) {
+                step.B = now;
+                step.C = then;
+                status = launch_ortho(step, OrthoCall{kOrthoStep, bf16, true}, cus, s);
+                if (status != GEMM_F32_SUCCESS) return status;
+                char *const t = now;
+                now = then, then = t;
+                continue;
+            }
+            OrthoArgs last = step;
+            last.C = static_cast<char *>(Y) + first * stride_y * size;
+            last.ldc = ldy * size;
+            last.c_stride = stride_y * size;
+            last.rows = (int)rows;
+            last.cols = (int)cols;
+            last.c = scale * kPlaneBack * kPlaneBack;
+            const bool wide = wide_rows(last.C, last.ldc, cols, size) && (here_ == 1 || last.c_stride % 16 == 0);
+            if (turned) {
+                // X^T B: X is the first operand, along its rows.
+                last.A = now;
+                last.a_stride = step.b_stride, last.lda = step.ldb, last.a_bytes = step.b_bytes;
+                last.B = g1;
+                last.b_stride = step.a_stride, last.ldb = step.lda, last.b_bytes = step.a_bytes;
+                last.a_second = step.b_second, last.a_third = step.b_third;
+                last.b_second = step.a_second, last.b_third = step.a_third;
+            } else {
+                last.B = now;
+            }
+            status = launch_ortho(last, OrthoCall{turned ? kOrthoTurned : kOrthoLast, bf16, wide}, cus, s);
+            if (status != GEMM_F32_SUCCESS) return status;
+        }
+    }
+    return GEMM_F32_SUCCESS;
 }
 
 }  // extern "C"

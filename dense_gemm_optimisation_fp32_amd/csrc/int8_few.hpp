@@ -1,0 +1,108 @@
+// 8-bit products where an expert has few rows (decoding): bound by the bytes of
+// the experts' codes, each read once.
+//
+// A workgroup takes 16 rows of one expert and a strip of columns, its
+// wavefronts split k, as in grouped_few.hpp.  Codes go straight from memory into
+// registers, 16 bytes a lane, one iteration's loads ahead of the products
+// (v_mfma_i32_16x16x64_i8: four lanes share a column's 64 bytes).  The
+// wavefronts' sums meet in LDS as integers: any order gives the same bits.
+#pragma once
+
+#include "lp_gemm.hpp"
+
+namespace gemmf32 {
+
+template <class X, int WAVES_, int NB_>
+struct Int8FewTile {
+    using E = X;
+    static constexpr int WAVES = WAVES_, THREADS = WAVES * 64, NB = NB_;
+    static constexpr int BM = 16, BN = 16 * NB, KI = 256;       // k of an iteration
+};
+
+template <class T>
+struct Int8FewRegs {
+    i32x4 a[4], b[4 * T::NB];
+};
+
+template <class T>
+__global__ __launch_bounds__(T::THREADS) void int8_few_kernel(GroupedArgs g)
+{
+    using E = typename T::E;
+    constexpr int BM = T::BM, BN = T::BN, ROW = BN + 4;
+    __shared__ int red[T::WAVES][BM * ROW];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    RowTile rt;
+    int tn;
+    if (!find_tile<BM>(g, blockIdx.x, lane, rt, tn)) return;
+    const int col0 = tn * BN;
+    const int l16 = lane & 15, grp = lane >> 4;
+    const int rows = min(rt.rows, BM);
+    i32x4 acc[T::NB];
+#pragma unroll
+    for (int nb = 0; nb < T::NB; ++nb) acc[nb] = i32x4{};
+    if (rt.expert >= 0) {
+        const char *const pa = g.A + (rt.row + min(l16, rows - 1)) * g.lda + grp * 16;
+        const char *const bx = g.B + rt.expert * g.expert_stride + grp * 16;
+        const char *pb[T::NB];
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb) pb[nb] = bx + min(col0 + nb * 16 + l16, g.n - 1) * g.ldb;
+        const int held = (int)g.ldb - grp * 16;               // bytes of B's rows from this lane's first on
+        const int kp = g.a_kblocks * 128;                     // of A's rows
+        auto load = [&](int it, Int8FewRegs<T> &r) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int k0 = it * T::KI + s * 64;
+                r.a[s] = k0 < kp ? *reinterpret_cast<const i32x4 *>(pa + k0) : i32x4{};
+#pragma unroll
+                for (int nb = 0; nb < T::NB; ++nb)
+                    r.b[s * T::NB + nb] = k0 < held ? *reinterpret_cast<const i32x4 *>(pb[nb] + k0) : i32x4{};
+            }
+        };
+        auto multiply = [&](const Int8FewRegs<T> &r) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int nb = 0; nb < T::NB; ++nb)
+                    acc[nb] = __builtin_amdgcn_mfma_i32_16x16x64_i8(r.b[s * T::NB + nb], r.a[s], acc[nb], 0, 0, 0);
+        };
+        const int its = (g.k + T::KI - 1) / T::KI;
+        Int8FewRegs<T> r[2];
+        if (wave < its) load(wave, r[0]);
+        int it = wave;
+        while (it < its) {
+            if (it + T::WAVES < its) load(it + T::WAVES, r[1]);
+            multiply(r[0]);
+            it += T::WAVES;
+            if (it >= its) continue;
+            if (it + T::WAVES < its) load(it + T::WAVES, r[0]);
+            multiply(r[1]);
+            it += T::WAVES;
+        }
+    }
+    // Lane (l16, grp) holds row l16 and columns 4 grp + v of each block.
+#pragma unroll
+    for (int nb = 0; nb < T::NB; ++nb)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) red[wave][l16 * ROW + nb * 16 + 4 * grp + v] = acc[nb][v];
+    __syncthreads();
+    const float *const sa = reinterpret_cast<const float *>(g.a_scales) + rt.row;
+    const float *const sb = reinterpret_cast<const float *>(g.b_scales) + (long long)max(rt.expert, 0) * g.n + col0;
+    const float *const bias = g.bias && rt.expert >= 0 ? g.bias + rt.expert * g.bias_stride + col0 : nullptr;
+    for (int e = tid; e < rows * BN; e += T::THREADS) {
+        const int row = e / BN, col = e % BN;
+        if (col0 + col >= g.n) continue;
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < T::WAVES; ++w) sum += red[w][row * ROW + col];
+        float x = 0.0f;
+        if (rt.expert >= 0) {
+            x = (float)sum * sa[row] * sb[col];
+            if (bias) x += bias[col];
+            x = activate(x, g.act);
+        }
+        *(reinterpret_cast<E *>(g.C + (rt.row + row) * g.ldc) + col0 + col) = (E)x;
+    }
+}
+
+}  // namespace gemmf32

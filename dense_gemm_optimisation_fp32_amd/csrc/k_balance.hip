@@ -1,0 +1,77 @@
+// Kernel translation unit: balanced routing and its launches.
+#include "balance.hpp"
+#include "expert_launch.hpp"
+
+namespace gemmf32 {
+
+namespace {
+
+template <class E, int LANES, int V>
+int launch_choose(const BalanceArgs &b, hipStream_t s)
+{
+    const RouteArgs &a = b.route;
+    // Half the threads where a lane's keys would not fit the registers of all.
+    constexpr int THREADS = V > 8 ? 512 : kRouteThreads;
+    const int found = balance_found_words(LANES, THREADS, a.choices), place = route_place_words(a.groups);
+    if constexpr (V <= 8)
+        if (a.tokens <= kRouteTokens)
+            return launch(balance_one_kernel<E, LANES, V>, 1, kRouteThreads,
+                          (a.groups + 2 + (found > place ? found : place)) * 4, s, b);
+    const long long parts = (a.tokens + kRouteTokens - 1ll) / kRouteTokens;
+    const int st = launch(balance_choose_kernel<E, LANES, V, THREADS>, parts, THREADS, (a.groups + found) * 4, s, b);
+    if (st != GEMM_F32_SUCCESS) return st;
+    return launch(route_place_kernel, parts, kRouteThreads, (a.groups + 2 + place) * 4, s, a);
+}
+
+// Lanes of a set: the largest power of two that leaves every set its own.
+int lanes_of(int sets, int all)
+{
+    int n = 1;
+    while (2 * n * sets <= all) n *= 2;
+    return n;
+}
+
+template <class E>
+int launch_choose_e(BalanceArgs b, hipStream_t s)
+{
+    const int size = b.route.groups / b.sets;
+    if (b.sets <= 16) {
+        b.lanes = lanes_of(b.sets, 16);
+        b.each = (size + b.lanes - 1) / b.lanes;
+        if (b.each <= 1) return launch_choose<E, 16, 1>(b, s);
+        if (b.each <= 2) return launch_choose<E, 16, 2>(b, s);
+        if (b.each <= 4) return launch_choose<E, 16, 4>(b, s);
+        if (b.each <= 8) return launch_choose<E, 16, 8>(b, s);
+        // (Few tokens: a wavefront each, in one workgroup.)
+        if (b.each <= 16 && b.route.tokens > kRouteTokens) return launch_choose<E, 16, 16>(b, s);
+    }
+    b.lanes = lanes_of(b.sets, 64);
+    b.each = (size + b.lanes - 1) / b.lanes;
+    if (b.each <= 8) return launch_choose<E, 64, 8>(b, s);
+    if (b.each <= 16) return launch_choose<E, 64, 16>(b, s);
+    return launch_choose<E, 64, 32>(b, s);
+}
+
+template <class E>
+int launch_grad_e(const BalanceArgs &b, hipStream_t s)
+{
+    const long long grid = (b.route.tokens + 15ll) / 16;
+    const int groups = b.route.groups;
+    if (groups <= 16) return launch(balance_grad_kernel<E, 1>, grid, kGradThreads, 0, s, b);
+    if (groups <= 32) return launch(balance_grad_kernel<E, 2>, grid, kGradThreads, 0, s, b);
+    if (groups <= 64) return launch(balance_grad_kernel<E, 4>, grid, kGradThreads, 0, s, b);
+    if (groups <= 128) return launch(balance_grad_kernel<E, 8>, grid, kGradThreads, 0, s, b);
+    if (groups <= 256) return launch(balance_grad_kernel<E, 16>, grid, kGradThreads, 0, s, b);
+    if (groups <= 512) return launch(balance_grad_kernel<E, 32>, grid, kGradThreads, 0, s, b);
+    return launch(balance_grad_kernel<E, 64>, grid, kGradThreads, 0, s, b);
+}
+
+}  // namespace
+
+int launch_balance(const BalanceArgs &b, bool bf16, bool grad, hipStream_t s)
+{
+    if (grad) return bf16 ? launch_grad_e<__bf16>(b, s) : launch_grad_e<float>(b, s);
+    return bf16 ? launch_choose_e<__bf16>(b, s) : launch_choose_e<float>(b, s);
+}
+
+}  // namespace gemmf32

@@ -1,15 +1,16 @@
 // Products grouped by expert on the low-precision matrix cores: bfloat16
 // (v_mfma_f32_32x32x16_bf16) and microscaled 4-bit operands
-// (v_mfma_scale_f32_32x32x64_f8f6f4), accumulated in 32 bits.
+// (v_mfma_scale_f32_32x32x64_f8f6f4), accumulated in 32 bits, and 8-bit
+// integers (v_mfma_i32_32x32x32_i8), accumulated exactly in 32-bit integers.
 //
 //   C_e = act(A_e . B_e + bias_e)   A_e: the rows of expert e
 //   dB_e = A_e^T . G_e              (A_KS: the contraction runs over A's rows)
 //
-// The two types share one kernel because they share its data flow: a lane's
-// operand of one matrix instruction is 16 contiguous bytes, 8 bfloat16 or 32
-// 4-bit values of one row, an instruction covers 32 bytes of each row, and
-// takes as long (32 cycles).  A slab is 128 bytes along k: 64 bfloat16, 256
-// 4-bit values; four k-steps.
+// The types share one kernel because they share its data flow: a lane's
+// operand of one matrix instruction is 16 contiguous bytes, 8 bfloat16, 16
+// integers or 32 4-bit values of one row, an instruction covers 32 bytes of each
+// row, and takes as long (32 cycles).  A slab is 128 bytes along k: 64 bfloat16,
+// 128 integers, 256 4-bit values; four k-steps.
 //
 // Operands travel from memory straight into LDS (buffer_load ... lds, 16
 // bytes a lane) into a ring of STAGES slabs.  The last k-step of a slab comes
@@ -37,6 +38,8 @@
 // last row again): they only feed rows of C that are not stored.  Elements
 // past k are made zero in both operands: k-rows past the end by the buffer's
 // range check, the tail of contiguous rows in LDS after the copy has landed.
+// (Integers: A's rows are whole slabs, with zeros past k; what B has there, the
+// next row's codes, is finite and counts nothing.)
 #pragma once
 
 #include "expert_common.hpp"
@@ -44,11 +47,17 @@
 namespace gemmf32 {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 *lds_s16x4_t;
 typedef __attribute__((address_space(3))) void *lds_void_t;
 
-enum LpKind { kBf16 = 0, kFp4 = 1 };
+// (kF16: half-precision planes of 32-bit numbers, see orthogonal.hpp; whole slabs.)
+enum LpKind { kBf16 = 0, kFp4 = 1, kInt8 = 2, kF16 = 3 };
+
+// Values of a 16-byte chunk.
+constexpr int lp_values(int kind) { return kind == kFp4 ? 32 : kind == kInt8 ? 16 : 8; }
 
 template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_>
 struct LpTile {
@@ -272,6 +281,14 @@ __device__ __forceinline__ void lp_mfma(int i, int p, const LpFrags<T, KIND> &f,
     if constexpr (KIND == kBf16) {
         acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b),
                                                               __builtin_bit_cast(bf16x8, a), acc[mb][nb], 0, 0, 0);
+    } else if constexpr (KIND == kF16) {
+        acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a),
+                                                             acc[mb][nb], 0, 0, 0);
+    } else if constexpr (KIND == kInt8) {
+        // (The sums' bits, in the registers of the other kinds: lp_scale makes
+        // numbers of them.)
+        acc[mb][nb] = __builtin_bit_cast(f32x16, __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, __builtin_bit_cast(i32x16, acc[mb][nb]),
+                                                                                      0, 0, 0));
     } else {
         const i32x8 a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
         if (p & 1)
@@ -283,13 +300,24 @@ __device__ __forceinline__ void lp_mfma(int i, int p, const LpFrags<T, KIND> &f,
     }
 }
 
+// Bytes of a row of B (and, but for integers, of A) that are its own.
+template <int KIND>
+__device__ __forceinline__ long long lp_row_bytes(const GroupedArgs &g)
+{
+    return KIND == kFp4 ? (long long)g.a_kblocks * 64 : KIND == kInt8 ? g.ldb : (long long)g.k * 2;
+}
+
 // What a tile needs of its operands.
 struct LpProblem {
     LpOperand a, b;
     const u8 *a_scales, *b_scales;     // of the tile's first rows, k-block 0
     long long a_scale_bytes, b_scale_bytes;   // extents
     long long a_scale_step, b_scale_step;     // bytes from k-block to k-block
-    int k;                             // contraction (4-bit: kp)
+    int k;                             // contraction (4-bit: kp; planes: of all segments)
+    // Planes: the contraction goes over up to three pairs of planes in turn, `segment`
+    // slabs each; where the second and the third lie from p on.
+    int segment;
+    long long a_second, a_third, b_second, b_third;
 };
 
 // REG: operands whose rows are not 4-byte aligned (bfloat16 rows of odd
@@ -298,7 +326,7 @@ struct LpProblem {
 template <class T, int KIND, bool A_KS, bool B_KS, int RUN, bool REG = false>
 struct LpLoop {
     static_assert(!REG || (KIND == kBf16 && T::STAGES == 2), "register copies: bfloat16, two stages");
-    static constexpr int KSLAB = T::CPR * (KIND == kFp4 ? 32 : 8);
+    static constexpr int KSLAB = T::CPR * lp_values(KIND);
     // Scale words of a slab: [A, B][k-block][row], four a chunk.  The first
     // wavefronts copy A's, the next ones B's, and further ones the same again:
     // a branch around the copy would split the slab's schedule.
@@ -346,8 +374,14 @@ struct LpLoop {
         Source c;
         c.st = stage(kt % T::STAGES);
         c.left = q.k - kt * KSLAB;
-        const long long sa = A_KS ? (long long)kt * KSLAB * q.a.ld : (long long)kt * (T::CPR * 16);
-        const long long sb = B_KS ? (long long)kt * KSLAB * q.b.ld : (long long)kt * (T::CPR * 16);
+        int at = kt;
+        long long pa = 0, pb = 0;
+        if constexpr (KIND == kF16) {
+            if (at >= q.segment) at -= q.segment, pa = q.a_second, pb = q.b_second;
+            if (at >= q.segment) at -= q.segment, pa = q.a_third, pb = q.b_third;
+        }
+        const long long sa = pa + (A_KS ? (long long)at * KSLAB * q.a.ld : (long long)at * (T::CPR * 16));
+        const long long sb = pb + (B_KS ? (long long)at * KSLAB * q.b.ld : (long long)at * (T::CPR * 16));
         c.a = lp_rsrc(q.a.p + sa, q.a.bytes - sa);
         c.b = lp_rsrc(q.b.p + sb, q.b.bytes - sb);
         if constexpr (KIND == kFp4) {
@@ -585,6 +619,32 @@ __device__ __forceinline__ void lp_store(char *c, long long ldc, int rows, int c
     }
 }
 
+// Integer sums times their rows' and columns' scales, as 32-bit numbers.
+template <class T, class E>
+__device__ __forceinline__ void lp_scale(const GroupedArgs &g, int expert, int row, int rows, int col, int wr, int wc, int lane,
+                                         f32x16 (&acc)[T::MB][T::NB])
+{
+    constexpr int RUN = 16 / sizeof(E);
+    const float *const sa = reinterpret_cast<const float *>(g.a_scales) + row;
+    const float *const sb = reinterpret_cast<const float *>(g.b_scales) + (long long)expert * g.n;
+    float of_row[T::MB];
+#pragma unroll
+    for (int mb = 0; mb < T::MB; ++mb) of_row[mb] = sa[min(wr * T::WM + mb * 32 + (lane & 31), rows - 1)];
+    const int col0 = col + wc * T::WN + (lane >> 5) * RUN;
+#pragma unroll
+    for (int nb = 0; nb < T::NB; ++nb) {
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const float b = sb[min(col0 + nb * 32 + v / RUN * (2 * RUN) + v % RUN, g.n - 1)];
+#pragma unroll
+            for (int mb = 0; mb < T::MB; ++mb) acc[mb][nb][v] = (float)__float_as_int(acc[mb][nb][v]) * of_row[mb] * b;
+            if (v % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int mb = 0; mb < T::MB; ++mb) asm volatile("" : "+v"(acc[mb][nb]));
+    }
+}
+
 // One tile of C_e = act(A_e . B_e + bias_e): rows from `row` on, of which the
 // expert has `rows`, columns from col on.  Expert -1: zeros.
 template <class T, int KIND, bool B_KS, class E, bool WIDE, bool REG = false>
@@ -600,16 +660,15 @@ __device__ __forceinline__ void lp_tile(const GroupedArgs &g, i32x4 *lds, int ti
         for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] = f32x16{};
     if (expert >= 0) {
         LpProblem q;
-        const long long row_bytes = KIND == kFp4 ? (long long)g.a_kblocks * 64 : (long long)g.k * 2;
-        q.a = {g.A + row * g.lda, (g.m - 1 - row) * g.lda + row_bytes, (int)g.lda, g.m - row};
+        const long long row_bytes = lp_row_bytes<KIND>(g);
+        q.a = {g.A + row * g.lda, (g.m - 1 - row) * g.lda + (KIND == kInt8 ? g.lda : row_bytes), (int)g.lda, g.m - row};
         const char *const b = g.B + expert * g.expert_stride;
         if constexpr (B_KS)
             q.b = {b + (long long)col * 2, (long long)(g.k - 1) * g.ldb + (long long)cols * 2, (int)g.ldb, cols};
         else
             q.b = {b + col * g.ldb, (cols - 1) * g.ldb + row_bytes, (int)g.ldb, cols};
-        q.k = g.k;
+        q.k = KIND == kBf16 ? g.k : g.a_kblocks * 128;
         if constexpr (KIND == kFp4) {
-            q.k = g.a_kblocks * 128;
             q.a_scales = g.a_scales + (long long)row * 4;
             q.a_scale_step = (long long)g.m * 4;
             q.a_scale_bytes = g.a_kblocks * q.a_scale_step - (long long)row * 4;
@@ -619,6 +678,7 @@ __device__ __forceinline__ void lp_tile(const GroupedArgs &g, i32x4 *lds, int ti
         }
         LpLoop<T, KIND, false, B_KS, 16 / sizeof(E), REG> loop{q, lds, tid, lane, wave, wr, wc};
         loop.run(acc);
+        if constexpr (KIND == kInt8) lp_scale<T, E>(g, expert, row, rows, col, wr, wc, lane, acc);
     }
     const float *bias = g.bias && expert >= 0 ? g.bias + expert * g.bias_stride + col : nullptr;
     lp_store<T, E, WIDE>(g.C + row * g.ldc + (long long)col * sizeof(E), g.ldc, rows, cols, bias, expert < 0 ? 0 : g.act,

@@ -93,7 +93,7 @@ template <class T, int KIND, bool GRAD, bool B_KS, class E, bool WIDE>
 struct LpPipe {
     static constexpr bool A_KS = GRAD;
     static constexpr int RUN = 16 / sizeof(E);
-    static constexpr int S = T::STAGES, KSLAB = T::CPR * (KIND == kFp4 ? 32 : 8);
+    static constexpr int S = T::STAGES, KSLAB = T::CPR * lp_values(KIND);
     static constexpr int STAGE = T::stage_chunks(KIND);              // chunks
     static constexpr int COPIES = T::PIECES + (KIND == kFp4 ? 1 : 0);
     static constexpr int FIRST = COPIES * 3 / 4;                     // copies right behind the barrier
@@ -139,7 +139,7 @@ struct LpPipe {
             j.row = __builtin_amdgcn_readfirstlane(table[entries + at]) + skip;
             j.rows = __builtin_amdgcn_readfirstlane(table[2 * entries + at]) - skip;
             j.expert = g.offsets && at >= g.groups ? -1 : at;
-            j.k = j.expert < 0 ? 0 : KIND == kFp4 ? g.a_kblocks * 128 : g.k;
+            j.k = j.expert < 0 ? 0 : KIND == kBf16 ? g.k : g.a_kblocks * 128;
         }
         return j;
     }
@@ -165,10 +165,10 @@ struct LpPipe {
             a = {g.A + j.row * g.lda + (long long)j.rows * 2, last * g.lda + (long long)(g.k - j.rows) * 2, (int)g.lda, 0};
             b = {g.B + j.row * g.ldb + (long long)j.col * 2, last * g.ldb + (long long)(g.n - j.col) * 2, (int)g.ldb, 0};
         } else {
-            const long long row_bytes = KIND == kFp4 ? (long long)g.a_kblocks * 64 : (long long)g.k * 2;
+            const long long row_bytes = lp_row_bytes<KIND>(g);
             const int cols = g.n - j.col;
             const char *const w = g.B + j.expert * g.expert_stride;
-            a = {g.A + j.row * g.lda, (g.m - 1 - j.row) * g.lda + row_bytes, (int)g.lda, g.m - j.row};
+            a = {g.A + j.row * g.lda, (g.m - 1 - j.row) * g.lda + (KIND == kInt8 ? g.lda : row_bytes), (int)g.lda, g.m - j.row};
             if constexpr (B_KS)
                 b = {w + (long long)j.col * 2, (long long)(g.k - 1) * g.ldb + (long long)cols * 2, (int)g.ldb, cols};
             else
@@ -289,7 +289,7 @@ struct LpPipe {
             // Half a slab: zero codes in A, for B's are finite, and so are the
             // scales that are read past the last k-block (as zero).
             lp_zero_tail4<T>(lds + at, t, elements);
-        } else {
+        } else if constexpr (KIND == kBf16) {
             if constexpr (!A_KS) lp_zero_tail<T, false>(lds + at, t, elements);
             if constexpr (!B_KS) lp_zero_tail<T, true>(lds + at + T::A_CHUNKS, t, elements);
         }
@@ -428,7 +428,7 @@ struct LpPipe {
         for (int tile = first; tile < tile_end; tile += tile_step) {
             const LpJob j = job(tile);
             const int slabs = (j.k + KSLAB - 1) / KSLAB;
-            const int tail = A_KS && B_KS ? 0 : j.k % KSLAB;
+            const int tail = (A_KS && B_KS) || KIND == kInt8 ? 0 : j.k % KSLAB;
             if (slabs > 0 && !started) {
                 started = true;
                 lp_wait<(S - 1) * COPIES>();
@@ -476,6 +476,8 @@ struct LpPipe {
             } else {
                 const int cols = g.n - j.col;
                 char *const out = g.C + j.row * g.ldc + (long long)j.col * (long long)sizeof(E);
+                if constexpr (KIND == kInt8)
+                    if (j.expert >= 0) lp_scale<T, E>(g, j.expert, j.row, j.rows, j.col, wr, wc, lane_e, acc);
                 if (j.expert >= 0)
                     lp_epilogue<T, E>(cols, g.bias ? g.bias + j.expert * g.bias_stride + j.col : nullptr, g.act, wc, lane_e,
                                       acc);

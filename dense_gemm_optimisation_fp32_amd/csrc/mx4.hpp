@@ -69,6 +69,11 @@ struct Mx8<float> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
     }
+    __device__ __forceinline__ void values(float (&out)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] = v[i];
+    }
     __device__ __forceinline__ unsigned largest() const
     {
         unsigned m = 0;
@@ -92,6 +97,14 @@ struct Mx8<__bf16> {
     i32x4 v;
 
     __device__ __forceinline__ void load(const __bf16 *p, int left) { v = load_chunk(p, left); }
+    __device__ __forceinline__ void values(float (&out)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            out[2 * i] = __uint_as_float((unsigned)v[i] << 16);
+            out[2 * i + 1] = __uint_as_float((unsigned)v[i] & 0xffff0000u);
+        }
+    }
     __device__ __forceinline__ unsigned largest() const
     {
         typedef unsigned short Pair __attribute__((ext_vector_type(2)));

@@ -1,0 +1,244 @@
+// Orthogonalising a matrix: all its singular values brought near one, its
+// singular vectors kept.
+//
+//   X <- X / |X|,  then in every step  A = X X^T,  X <- (a I + b A + c A A) X
+//
+// (Newton-Schulz steps of degree five: a singular value s becomes a s + b s^3 +
+// c s^5.)  X is m x n with m <= n; of a taller matrix the transposed is taken.
+//
+// Precision.  The steps multiply what is small in X by up to a each (3.4^5 = 480
+// in five), X's roundings among it: with X in bfloat16 between the steps results
+// are 1 to 30 % off, in half precision 0.2 to 4 % (the more, the faster the
+// singular values fall).  Every matrix is therefore held as two half-precision
+// planes, v * 2^11 = hi + lo: 22 bits, and products run on the matrix cores as
+// hi hi + hi lo + lo hi, accumulated in 32 bits (v_mfma_f32_32x32x16_f16, three
+// times the work of one plane, yet 5 times the rate of 32-bit products).  The
+// factor 2^11 keeps lo above the subnormals; entries stay below 2^15.9 / 2^11 = 31,
+// which the host derives from the coefficients.
+// bfloat16 results are rounded to 2^-9 at the end: for them A and B = a I + b A +
+// c A A are one plane and X two; A = hi hi^T, A A one product, B X two.  Measured in
+// the 2-norm against 64 bits: 0.0017 off with all planes (what the last rounding
+// gives), 0.0018 to 0.0024 so.
+//
+// A plane is rows of whole 64 columns, rows a multiple of 64, zeros outside the
+// matrix; a matrix's planes lie one after the other.  The contraction goes over the
+// pairs of planes in turn: to the tile it is one longer contraction.
+#pragma once
+
+#include "lp_gemm.hpp"
+#include "mx4.hpp"
+
+namespace gemmf32 {
+
+constexpr float kPlaneScale = 2048.0f, kPlaneBack = 1.0f / 2048.0f;
+
+struct OrthoArgs {
+    // The product C = A . B (planes): matrix 0's, and bytes from matrix to matrix.
+    const char *A, *B;
+    long long a_stride, b_stride, c_stride;
+    int lda, ldb;                      // bytes from row to row
+    long long a_bytes, b_bytes;        // of a matrix's planes
+    int segments, k;                   // pairs of planes; contraction of each, whole slabs
+    long long a_second, a_third, b_second, b_third;     // where the second and third pair lie
+    int rows, cols;                    // of C
+    int tiles_m, tiles_n, group_m, batch, num_xcd;
+    // What becomes of the sums.
+    char *C;                           // planes, or the result
+    long long ldc, c_plane;            // bytes; from hi to lo
+    int c_planes;
+    const char *G;                     // A's planes in B = a I + b A + c A A (else NULL)
+    int order;                         // rows of the matrix that I has
+    float a, b, c;                     // (c: the factor of the sums in every product)
+};
+
+struct OrthoStartArgs {
+    const char *x;
+    long long ld, stride;              // elements
+    int rows, cols;                    // of x
+    int m_pad, n_pad;                  // of the planes
+    int turned;                        // planes of the transposed
+    int parts;
+    double *sums;                      // (batch, parts): squares
+    char *planes;
+    long long plane, matrix;           // bytes
+};
+
+// Sums of squares, in 64 bits: neither leaves the range for any 32-bit values.
+template <class E>
+__global__ __launch_bounds__(256) void ortho_squares_kernel(OrthoStartArgs a)
+{
+    __shared__ double sums[4];
+    const int part = blockIdx.x % a.parts, matrix = blockIdx.x / a.parts;
+    const E *const x = reinterpret_cast<const E *>(a.x) + matrix * a.stride;
+    const int chunks = (a.cols + 7) / 8;
+    const long long all = (long long)a.rows * chunks;
+    double sum = 0.0;
+    for (long long i = (long long)part * 256 + threadIdx.x; i < all; i += (long long)a.parts * 256) {
+        const int row = (int)(i / chunks), col = (int)(i % chunks) * 8;
+        float v[8];
+        load8(x + row * a.ld + col, a.cols - col, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += (double)v[j] * (double)v[j];
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+    if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) a.sums[blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+}
+
+// A 32-bit number's planes (scaled already).
+struct Planes {
+    _Float16 hi, lo;
+
+    __device__ __forceinline__ explicit Planes(float t)
+    {
+        hi = (_Float16)t;
+        lo = (_Float16)(t - (float)hi);
+    }
+};
+
+// x / |x| as planes, a block of 64 x 64 a workgroup.
+template <class E>
+__global__ __launch_bounds__(256) void ortho_start_kernel(OrthoStartArgs a)
+{
+    __shared__ float block[64][65];
+    __shared__ double factor_of;
+    const int tiles_n = a.n_pad / 64, tiles = a.m_pad / 64 * tiles_n;
+    const int matrix = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+    const int row0 = tile / tiles_n * 64, col0 = tile % tiles_n * 64;
+    if (threadIdx.x < 64) {
+        double sum = 0.0;
+        for (int i = threadIdx.x; i < a.parts; i += 64) sum += a.sums[(long long)matrix * a.parts + i];
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+        // (A matrix of zeros stays one.)
+        if (threadIdx.x == 0) factor_of = sum == 0.0 ? 0.0 : (double)kPlaneScale / sqrt(sum);
+    }
+    const E *const x = reinterpret_cast<const E *>(a.x) + matrix * a.stride;
+    const int r0 = a.turned ? col0 : row0, c0 = a.turned ? row0 : col0;      // in x
+    float v[2][8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = r0 + (threadIdx.x >> 3) + 32 * i, c = c0 + (threadIdx.x & 7) * 8;
+        load8(x + r * a.ld + c, r < a.rows ? a.cols - c : 0, v[i]);
+    }
+    __syncthreads();
+    const double factor = factor_of;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = (threadIdx.x >> 3) + 32 * i, c = (threadIdx.x & 7) * 8 + j;
+            const float t = (float)((double)v[i][j] * factor);
+            if (a.turned) block[c][r] = t;
+            else block[r][c] = t;
+        }
+    __syncthreads();
+    char *const out = a.planes + matrix * a.matrix;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = (threadIdx.x >> 3) + 32 * i, c = (threadIdx.x & 7) * 8;
+        f16x8 hi, lo;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const Planes p(block[r][c + j]);
+            hi[j] = p.hi;
+            lo[j] = p.lo;
+        }
+        char *const q = out + ((long long)(row0 + r) * a.n_pad + col0 + c) * 2;
+        *reinterpret_cast<f16x8 *>(q) = hi;
+        *reinterpret_cast<f16x8 *>(q + a.plane) = lo;
+    }
+}
+
+// The sums' planes, whole runs of eight columns.  G: a I + b G + c sums.
+template <class T>
+__device__ __forceinline__ void ortho_store(const OrthoArgs &g, int matrix, int row0, int col0, int wr, int wc, int lane,
+                                            f32x16 (&acc)[T::MB][T::NB])
+{
+    const int l32 = lane & 31, half = lane >> 5;
+#pragma unroll
+    for (int mb = 0; mb < T::MB; ++mb) {
+        const int row = row0 + wr * T::WM + mb * 32 + l32;
+        if (row >= g.rows) continue;
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb)
+#pragma unroll
+            for (int v0 = 0; v0 < 16; v0 += 8) {
+                const int col = col0 + wc * T::WN + nb * 32 + half * 8 + v0 * 2;
+                if (col >= g.cols) continue;
+                const long long at = row * g.ldc + (long long)col * 2;
+                float t[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) t[i] = acc[mb][nb][v0 + i] * g.c;
+                if (g.G) {
+                    const char *const p = g.G + matrix * g.c_stride + at;
+                    const f16x8 hi = *reinterpret_cast<const f16x8 *>(p);
+                    f16x8 lo = {};
+                    if (g.c_planes > 1) lo = *reinterpret_cast<const f16x8 *>(p + g.c_plane);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        t[i] += g.b * ((float)hi[i] + (float)lo[i]);
+                        if (col + i == row && row < g.order) t[i] += g.a;
+                    }
+                }
+                f16x8 hi, lo;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const Planes p(t[i]);
+                    hi[i] = p.hi;
+                    lo[i] = p.lo;
+                }
+                char *const q = g.C + matrix * g.c_stride + at;
+                *reinterpret_cast<f16x8 *>(q) = hi;
+                if (g.c_planes > 1) *reinterpret_cast<f16x8 *>(q + g.c_plane) = lo;
+            }
+    }
+}
+
+// E: what C holds, planes (_Float16) or the result's type.
+template <class T, bool A_KS, bool B_KS, class E, bool WIDE>
+__global__ __launch_bounds__(T::THREADS) void ortho_kernel(OrthoArgs g)
+{
+    __shared__ i32x4 lds[T::STAGES * T::stage_chunks(kF16)];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = wave % T::WAVES_M, wc = wave / T::WAVES_M;
+    const int tiles = g.tiles_m * g.tiles_n;
+    const int logical = xcd_contiguous(blockIdx.x, tiles * g.batch, g.num_xcd);
+    // (In scalar registers: the copies' descriptors come from them.)
+    const int matrix = __builtin_amdgcn_readfirstlane(logical / tiles), in = logical % tiles;
+    const int width = g.group_m * g.tiles_n, first = in / width * g.group_m;
+    const int size = min(g.tiles_m - first, g.group_m);
+    const int row = __builtin_amdgcn_readfirstlane((first + in % width % size) * T::BM);
+    const int col = __builtin_amdgcn_readfirstlane(in % width / size * T::BN);
+    LpProblem q{};
+    const long long skip_a = A_KS ? (long long)row * 2 : (long long)row * g.lda;
+    const long long skip_b = B_KS ? (long long)col * 2 : (long long)col * g.ldb;
+    q.a = {g.A + matrix * g.a_stride + skip_a, g.a_bytes - skip_a, g.lda, g.rows - row};
+    q.b = {g.B + matrix * g.b_stride + skip_b, g.b_bytes - skip_b, g.ldb, g.cols - col};
+    q.k = g.segments * g.k;
+    q.segment = g.k / 64;
+    q.a_second = g.a_second, q.a_third = g.a_third;
+    q.b_second = g.b_second, q.b_third = g.b_third;
+    f32x16 acc[T::MB][T::NB];
+#pragma unroll
+    for (int mb = 0; mb < T::MB; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] = f32x16{};
+    LpLoop<T, kF16, A_KS, B_KS, 16 / sizeof(E)> loop{q, lds, tid, lane, wave, wr, wc};
+    loop.run(acc);
+    if constexpr (sizeof(E) == 2 && __is_same(E, _Float16)) {
+        ortho_store<T>(g, matrix, row, col, wr, wc, lane, acc);
+    } else {
+#pragma unroll
+        for (int mb = 0; mb < T::MB; ++mb)
+#pragma unroll
+            for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] *= g.c;
+        lp_store<T, E, WIDE>(g.C + matrix * g.c_stride + row * g.ldc + (long long)col * sizeof(E), g.ldc, g.rows - row,
+                             g.cols - col, nullptr, 0, wr, wc, lane, acc);
+    }
+}
+
+}  // namespace gemmf32

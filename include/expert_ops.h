@@ -1,8 +1,8 @@
 /*
  * expert_ops.h - C ABI of the expert-layer operators of libgemm_f32.so
  * (MI355X, gfx950): routing tokens to experts, products grouped by expert in
- * 32-bit and bfloat16 precision with their gradients, and microscaled 4-bit
- * quantisation and products.
+ * 32-bit and bfloat16 precision with their gradients, microscaled 4-bit and
+ * 8-bit integer quantisation and products, and orthogonalised updates.
  *
  * Conventions, as in gemm_f32.h:
  *  - Return value: a gemm_f32_status code.  Nothing here throws, prints or
@@ -11,8 +11,8 @@
  *  - Pointers are device pointers of the current device, owned by the caller.
  *    Outputs overlap no other operand.  Operands of `dtype` EXPERT_F32 are
  *    4-byte, of EXPERT_BF16 2-byte aligned; int32 and float pointers, scales
- *    and route's workspace 4-byte, codes and expert_mx4_linear's workspace
- *    16-byte aligned.
+ *    and the routings' workspace 4-byte, codes and the other workspaces 16-byte
+ *    aligned.
  *  - Sizes and leading dimensions are in elements; sums, softmax statistics
  *    and products are held in 32 bits; a result of dtype EXPERT_BF16 is
  *    rounded once.  The same call on the same inputs gives the same bits.
@@ -33,7 +33,8 @@
  *  - A launch holds less than 2^32 threads, or the call is refused
  *    (GEMM_F32_ERR_INVALID_VALUE): route takes up to 2^29 - 128 tokens, its
  *    gradient 2^28 - 16; a 4-bit operand of rows of k columns has
- *    rows ceil(k / 512) up to 2^26 - 4; a product's tiles of 16 rows (up to 16
+ *    rows ceil(k / 512) up to 2^26 - 4; an 8-bit operand up to 2^26 - 4 rows of
+ *    2048 columns, 2^24 - 1 longer ones; a product's tiles of 16 rows (up to 16
  *    rows an expert on average, else 64 or 128) and 32 to 128 columns, those
  *    of empty experts among them, are below 2^24.
  *  - Errors: GEMM_F32_ERR_INVALID_VALUE (an argument outside the above),
@@ -142,6 +143,98 @@ int expert_route(int dtype, int64_t tokens, int64_t groups, int64_t choices, int
 int expert_route_grad(int dtype, int64_t tokens, int64_t groups, int64_t choices, int normalize, const void *logits,
                       int64_t ld, const float *weights, const int *experts, const float *grad, void *dlogits,
                       int64_t ldd, void *stream);
+
+/*
+ * Routing by scores, with a bias for balance and sets of experts.
+ *   score s: sigmoid(logit), or softmax over the token's logits.
+ *   key c = s + bias[expert] (bias NULL: 0), in 64 bits: what is chosen by.  An
+ *   expert whose logit is -inf or NaN, or whose bias is -inf or NaN, is never
+ *   chosen (+inf logits: not supported with softmax scores).
+ *   The experts lie in `sets` sets of groups / sets neighbouring ones.  A set's
+ *   value is the sum of its two largest keys (of one, where it has one); the
+ *   `kept_sets` sets with the largest values stay, equal ones by the lower set.
+ *   Chosen are the `choices` largest keys in them, equal ones by the lower
+ *   expert.
+ *   weights: scale s / (sum of the chosen s) (normalize 1; 0 where the sum is 0) or
+ *   scale s (0), without the bias.
+ * experts, offsets, order and the slots that find no expert: as expert_route.
+ *   groups <= 1024, a multiple of sets; sets <= 64; 1 <= kept_sets <= sets;
+ *   1 <= choices <= min(32, kept_sets groups / sets); scale > 0 and finite; tokens
+ *   as for expert_route.
+ * workspace: expert_route_balanced_workspace bytes.
+ */
+enum expert_scores {
+    EXPERT_SIGMOID = 0,
+    EXPERT_SOFTMAX = 1
+};
+
+int64_t expert_route_balanced_workspace(int64_t tokens, int64_t groups);
+int expert_route_balanced(int dtype, int64_t tokens, int64_t groups, int64_t choices, int scores, int64_t sets,
+                          int64_t kept_sets, int normalize, float scale, const void *logits, int64_t ld,
+                          const float *bias, float *weights, int *experts, int *offsets, int *order, void *workspace,
+                          int64_t workspace_bytes, void *stream);
+
+/*
+ * The logits' gradient from g, that of the weights of the same
+ * expert_route_balanced call, (tokens, choices) floats; the choice and the bias
+ * have none.  With dot = sum_j w_j g_j / scale over the token's slots (0 unless
+ * normalize) a chosen expert's is w (g - dot) (1 - s) (sigmoid) or w (g - dot)
+ * (softmax), another's 0; softmax without normalize adds -s sum_j w_j g_j to
+ * every expert's.
+ */
+int expert_route_balanced_grad(int dtype, int64_t tokens, int64_t groups, int64_t choices, int scores, int normalize,
+                               float scale, const void *logits, int64_t ld, const float *weights, const int *experts,
+                               const float *grad, void *dlogits, int64_t ldd, void *stream);
+
+/*
+ * 8-bit integers with a scale for each row: scale = largest magnitude / 127,
+ * code = the whole number nearest to x * (127 / largest magnitude), ties to
+ * even, each step rounded in 32 bits.  A row whose largest magnitude is below
+ * 2^-119 gets scale 0 and codes 0, one with an infinity or a NaN scale NaN and
+ * codes 0.  With kp = k rounded up to 16: codes (rows, kp) bytes, zero past k;
+ * scales (rows) floats.  quantize reads X as expert_mx4_quantize does; dequantize
+ * writes X[r*ld + c] = codes * scale, rounded once.
+ */
+int expert_int8_quantize(int dtype, int64_t rows, int64_t k, const void *X, int layout, int64_t ld, void *codes,
+                         float *scales, void *stream);
+int expert_int8_dequantize(int dtype, int64_t rows, int64_t k, const void *codes, const float *scales, void *X,
+                           int64_t ld, void *stream);
+
+/*
+ * Y_e = act(Q(X_e) . Q(W_e)^T + bias_e): X m x k of dtype is quantised on the way,
+ * a scale for each row (token); W_e is held as n x kp codes, kp as above, and n
+ * scales (a scale for each row, channel), the experts' one after the other.  The
+ * sums of the codes' products are exact; times X's scale, times W's, plus bias,
+ * each rounded in 32 bits.  k is at most 131072.  offsets NULL: groups is 1 and W_0
+ * takes every row.
+ * workspace: expert_int8_workspace bytes, free for reuse when the call's work on
+ * the stream is done.
+ */
+int64_t expert_int8_workspace(int64_t m, int64_t k);
+int expert_int8_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t groups, const void *X, int64_t ldx,
+                       const void *codes, const float *scales, const int *offsets, const float *bias, int activation,
+                       void *Y, int64_t ldy, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Y = scale * X orthogonalised, for each of `batch` matrices of rows x cols, rows
+ * ldx (ldy) and matrices stride_x (stride_y) elements apart: X / |X| (2-norm of the
+ * entries; a matrix of zeros stays one), then `steps` times, with A = X X^T and the
+ * step's three coefficients a, b, c (in host memory, 3 * steps floats, read before
+ * the call returns),
+ *   X <- (a I + b A + c A A) X      (of a matrix with rows > cols its transposed),
+ * which takes every singular value s to a s + b s^3 + c s^5.  Held in 22 bits between
+ * the steps (bfloat16: A and a I + b A + c A A in 11), sums in 32.  Y may be X.
+ *   steps 1 .. 64; coefficients that could let an entry of A, a I + b A + c A A or,
+ *   before the last step, X pass 31 are refused; cols and rows below 2^22 - 64, and workgroups of 64 x 64
+ *   in all below 2^24.
+ * workspace: expert_orthogonalize_workspace bytes (for as many matrices at a time as
+ * 2 GiB hold, one at least: about 8 bytes an entry, and of the smaller square 8, in
+ * bfloat16 4).
+ */
+int64_t expert_orthogonalize_workspace(int dtype, int64_t batch, int64_t rows, int64_t cols);
+int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, const void *X, int64_t ldx,
+                         int64_t stride_x, int steps, const float *coefficients, float scale, void *Y, int64_t ldy,
+                         int64_t stride_y, void *workspace, int64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
