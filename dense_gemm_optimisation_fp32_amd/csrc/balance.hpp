@@ -16,9 +16,11 @@
 //
 // The slots are then sorted as in route.hpp, by the same kernels.
 //
-// Scores and keys are 64-bit: which expert is chosen goes by differences of
-// scores, and in 32 bits the last bits of an exponential decided one choice in
-// about twenty thousand tokens (256 experts).
+// Which expert is chosen goes by differences of keys: in 32 bits the last bits
+// of an exponential decided one choice in about twenty thousand tokens (256
+// experts).  A choice is first made in 32 bits with bounds on their errors; where
+// two keys, or two sets, whose order matters are nearer than those (few tokens,
+// unless many logits are equal) the wavefront chooses again in 64 bits.
 //
 // A token is held by LANES lanes.  A set takes a power of two of them
 // (`lanes`), each `each` neighbouring experts, so that a set's two largest are
@@ -40,7 +42,9 @@ struct BalanceArgs {
 
 constexpr int kBalanceMaxSets = 64;
 
-__device__ __forceinline__ double no_key() { return -__builtin_inf(); }
+// Tokens of a workgroup where there are up to kBalanceFewTokens of them (else
+// kRouteTokens): a part for most CUs.
+constexpr int kBalancePart = 32, kBalanceFewTokens = 8192;
 
 // x moved between lanes by a DPP control.
 template <int CTRL>
@@ -50,6 +54,12 @@ __device__ __forceinline__ double dpp64(double x)
     const u32x2 r = {(unsigned)__builtin_amdgcn_update_dpp(0, (int)v.x, CTRL, 0xf, 0xf, true),
                      (unsigned)__builtin_amdgcn_update_dpp(0, (int)v.y, CTRL, 0xf, 0xf, true)};
     return __builtin_bit_cast(double, r);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float mx_lane_f(float x)
+{
+    return __uint_as_float(mx_lane<CTRL>(__float_as_uint(x)));
 }
 
 // From the other half of 2 D lanes whose halves of D hold one value each (below
@@ -64,22 +74,37 @@ __device__ __forceinline__ double other_half(double x)
     else return __shfl_xor(x, D);
 }
 
-template <int LANES>
-__device__ __forceinline__ double lanes_max(double x)
+template <int D>
+__device__ __forceinline__ float other_half(float x)
 {
-    x = fmax(x, other_half<1>(x));
-    x = fmax(x, other_half<2>(x));
-    x = fmax(x, other_half<4>(x));
-    x = fmax(x, other_half<8>(x));
+    if constexpr (D == 1) return mx_lane_f<0xb1>(x);
+    else if constexpr (D == 2) return mx_lane_f<0x4e>(x);
+    else if constexpr (D == 4) return mx_lane_f<0x141>(x);
+    else if constexpr (D == 8) return mx_lane_f<0x140>(x);
+    else return __shfl_xor(x, D);
+}
+
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return fmin(a, b); }
+
+template <int LANES, class K>
+__device__ __forceinline__ K lanes_max(K x)
+{
+    x = larger(x, other_half<1>(x));
+    x = larger(x, other_half<2>(x));
+    x = larger(x, other_half<4>(x));
+    x = larger(x, other_half<8>(x));
     if constexpr (LANES == 64) {
-        x = fmax(x, other_half<16>(x));
-        x = fmax(x, other_half<32>(x));
+        x = larger(x, other_half<16>(x));
+        x = larger(x, other_half<32>(x));
     }
     return x;
 }
 
-template <int LANES>
-__device__ __forceinline__ double lanes_sum(double x)
+template <int LANES, class K>
+__device__ __forceinline__ K lanes_sum(K x)
 {
     x += other_half<1>(x);
     x += other_half<2>(x);
@@ -93,51 +118,169 @@ __device__ __forceinline__ double lanes_sum(double x)
 }
 
 // The two largest of a set, as its lanes join.
+template <class K>
 struct Two {
-    double first, second;
+    K first, second;
 
-    __device__ __forceinline__ void add(double x)
+    __device__ __forceinline__ void add(K x)
     {
-        second = fmax(second, fmin(first, x));
-        first = fmax(first, x);
+        second = larger(second, smaller(first, x));
+        first = larger(first, x);
     }
     template <int D>
     __device__ __forceinline__ void join()
     {
-        const double f = other_half<D>(first), s = other_half<D>(second);
-        second = fmax(fmin(first, f), fmax(second, s));
-        first = fmax(first, f);
+        const K f = other_half<D>(first), s = other_half<D>(second);
+        second = larger(smaller(first, f), larger(second, s));
+        first = larger(first, f);
     }
 };
 
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
-// How many sets of the token come before this lane's.
-template <int N, int LANES>
-__device__ __forceinline__ int sets_before(double value, int set, int lanes)
+// How many sets of the token come before this lane's: those in other lanes of
+// the row, N lanes on and further.
+template <int N, class K>
+__device__ __forceinline__ int sets_before(K value, int set, int lanes)
 {
-    // Sets in other lanes of the row, from N lanes on.
     int n = 0;
     if constexpr (N < 16) {
         if (N % lanes == 0) {
-            const double v = dpp64<0x120 + N>(value);
+            K v;
+            if constexpr (sizeof(K) == 8) v = dpp64<0x120 + N>(value);
+            else v = mx_lane_f<0x120 + N>(value);
             const int u = __builtin_amdgcn_update_dpp(0, set, 0x120 + N, 0xf, 0xf, true);
             n = v > value || (v == value && u < set) ? 1 : 0;
         }
-        n += sets_before<N + 1, LANES>(value, set, lanes);
+        n += sets_before<N + 1>(value, set, lanes);
     }
     return n;
 }
 
-// Chooses for the workgroup's tokens and counts the experts in LDS.  `found`
-// (LDS): `choices` experts for every LANES lanes.
-template <class E, int LANES, int V, int THREADS>
+// One token's choice: its experts to `mine`.  K: float or double.  x: the lane's
+// logits, `count` of them from expert e0 on.  False: keys or sets whose order
+// decides are nearer than their errors (never for double).
+//
+// Errors of 32-bit keys.  sigmoid: e = 2^(-x log2 e) is off by (1.5 |x| + 2)
+// 2^-24 of itself, the sum and the reciprocal add 1.5 2^-23: the score's error is
+// below 2^-21 (|x| s (1 - s) stays below 0.3).  softmax: e^(x - top) as much, the sum of
+// up to 32 of them a lane and of 6 lane by lane 38 2^-24 more: below 2^-18 of the
+// score, which is at most 1 / sum.  The bias adds a rounding, 2^-24 of the key.
+// Twice that for two keys, four times for two sets of two.
+template <class K, int LANES, int V>
+__device__ __forceinline__ bool balance_pick(const BalanceArgs &b, const float (&x)[V], float top, int sub, int group, int set,
+                                             int e0, int count, int *mine)
+{
+    constexpr bool kWide = sizeof(K) == 8;
+    const K none = -__builtin_inff();
+    K c[V];
+    float near = 0x1p-20f;                                // twice a score's error
+    if (b.softmax) {
+        K sum = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if constexpr (kWide) c[i] = exp((double)x[i] - (double)top);
+            else c[i] = __builtin_amdgcn_exp2f((x[i] - top) * 1.44269504088896341f);
+            sum += x[i] == x[i] ? c[i] : (K)0;
+        }
+        sum = lanes_sum<LANES>(sum);
+        if constexpr (kWide) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) c[i] /= sum;
+        } else {
+            const float each = __builtin_amdgcn_rcpf(sum);
+            near = 0x1p-17f * each;
+#pragma unroll
+            for (int i = 0; i < V; ++i) c[i] *= each;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if constexpr (kWide) c[i] = sigmoid64((double)x[i]);
+            else c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[i] * -1.44269504088896341f));
+        }
+    }
+    // (Opaque: the biases would else be held in registers for all tokens.)
+    int eb = e0;
+    asm volatile("" : "+v"(eb));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (b.bias) c[i] += (K)(i < count ? b.bias[eb + i] : 0.0f);
+        c[i] = x[i] > -__builtin_inff() && c[i] == c[i] ? c[i] : none;
+    }
+    bool sure = true;
+    if (b.kept < b.sets) {
+        Two<K> two{none, none};
+#pragma unroll
+        for (int i = 0; i < V; ++i) two.add(c[i]);
+        if (b.lanes > 1) two.template join<1>();
+        if (b.lanes > 2) two.template join<2>();
+        if (b.lanes > 4) two.template join<4>();
+        if (b.lanes > 8) two.template join<8>();
+        if constexpr (LANES == 64) {
+            if (b.lanes > 16) two.template join<16>();
+            if (b.lanes > 32) two.template join<32>();
+        }
+        const K value = two.second > none ? two.first + two.second : two.first;
+        int before = 0;
+        if constexpr (LANES == 16) {
+            before = sets_before<1>(value, set, b.lanes);
+        } else {
+            for (int u = 0; u < b.sets; ++u) {
+                const K v = __shfl(value, u * b.lanes);
+                before += v > value || (v == value && u < set) ? 1 : 0;
+            }
+        }
+        const bool out = before >= b.kept;
+        if constexpr (!kWide) {
+            const float least = -lanes_max<LANES>(out ? none : -value), most = lanes_max<LANES>(out ? value : none);
+            sure = most == none || least - most > 2.0f * near + 0x1p-21f * (fabsf(least) + fabsf(most));
+        }
+        if (out)
+#pragma unroll
+            for (int i = 0; i < V; ++i) c[i] = none;
+    }
+    K last = none;
+    for (int j = 0;; ++j) {
+        K best = c[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < V; ++i) {
+            const bool more = c[i] > best;
+            best = more ? c[i] : best;
+            at = more ? i : at;
+        }
+        const K m = lanes_max<LANES>(best);
+        const bool used = m > none;
+        if constexpr (!kWide) {
+            if (j > 0) sure = sure && (!used || last - m > near + 0x1p-22f * (fabsf(last) + fabsf(m)));
+            last = m;
+        }
+        if (j == b.route.choices) break;
+        const unsigned long long hit = __ballot(best == m);
+        int who;
+        if constexpr (LANES == 16) who = __builtin_ctz((unsigned)(hit >> (16 * group)) & 0xffffu);
+        else who = __builtin_ctzll(hit);
+        if (sub == who) {
+            mine[j] = used ? e0 + at : -1;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i == at) c[i] = none;
+        }
+        if (kWide && j + 1 == b.route.choices) break;     // (what comes next only bounds errors)
+    }
+    return sure;
+}
+
+// Chooses for the workgroup's TOKENS tokens and counts the experts in LDS.
+// `found` (LDS): `choices` experts for every LANES lanes.
+template <class E, int LANES, int V, int THREADS, int TOKENS>
 __device__ __forceinline__ void balance_choose(const BalanceArgs &b, int first, int *counts, int *found)
 {
     const RouteArgs &a = b.route;
     constexpr int PER = 64 / LANES;                       // tokens a wavefront
     const int lane = threadIdx.x & 63, sub = lane % LANES, group = lane / LANES;
-    const int last = min(first + kRouteTokens, a.tokens);
+    const int last = min(first + TOKENS, a.tokens);
     const int size = a.groups / b.sets;                   // experts of a set
     const int set = sub / b.lanes, inner = sub % b.lanes * b.each;
     const int e0 = set * size + inner;
@@ -160,86 +303,22 @@ __device__ __forceinline__ void balance_choose(const BalanceArgs &b, int first, 
 #pragma unroll
             for (int i = 0; i < V; ++i) x[i] = i < count ? to_f32(row[e0 + i]) : -__builtin_inff();
         }
-        // Scores, then keys.
-        double c[V], top = 0.0, sum = 1.0;
+        float top = 0.0f;
         if (b.softmax) {
-            float most = -__builtin_inff();
+            top = -__builtin_inff();
 #pragma unroll
-            for (int i = 0; i < V; ++i) most = fmaxf(most, x[i]);
-            top = lanes_max<LANES>((double)most);
-            top = top > no_key() ? top : 0.0;
+            for (int i = 0; i < V; ++i) top = fmaxf(top, x[i]);
+            top = lanes_max<LANES>(top);
+            top = top > -__builtin_inff() ? top : 0.0f;
+        }
+        const bool sure = balance_pick<float, LANES, V>(b, x, top, sub, group, set, e0, count, mine);
+        if (__ballot(!sure)) balance_pick<double, LANES, V>(b, x, top, sub, group, set, e0, count, mine);
+        double sum = 1.0;
+        if (b.softmax && !a.normalize) {
             sum = 0.0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                c[i] = exp((double)x[i] - top);
-                sum += x[i] == x[i] ? c[i] : 0.0;
-            }
+            for (int i = 0; i < V; ++i) sum += x[i] == x[i] ? exp((double)x[i] - (double)top) : 0.0;
             sum = lanes_sum<LANES>(sum);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                c[i] /= sum;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                c[i] = sigmoid64((double)x[i]);
-            }
-        }
-        // (Opaque: the biases would else be held in registers for all tokens.)
-        int eb = e0;
-        asm volatile("" : "+v"(eb));
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (b.bias) c[i] += (double)(i < count ? b.bias[eb + i] : 0.0f);
-            c[i] = x[i] > -__builtin_inff() && c[i] == c[i] ? c[i] : no_key();
-        }
-        if (b.kept < b.sets) {
-            Two two{no_key(), no_key()};
-#pragma unroll
-            for (int i = 0; i < V; ++i) two.add(c[i]);
-            if (b.lanes > 1) two.join<1>();
-            if (b.lanes > 2) two.join<2>();
-            if (b.lanes > 4) two.join<4>();
-            if (b.lanes > 8) two.join<8>();
-            if constexpr (LANES == 64) {
-                if (b.lanes > 16) two.join<16>();
-                if (b.lanes > 32) two.join<32>();
-            }
-            const double value = two.second > no_key() ? two.first + two.second : two.first;
-            int before = 0;
-            if constexpr (LANES == 16) {
-                before = sets_before<1, LANES>(value, set, b.lanes);
-            } else {
-                for (int u = 0; u < b.sets; ++u) {
-                    const double v = __shfl(value, u * b.lanes);
-                    before += v > value || (v == value && u < set) ? 1 : 0;
-                }
-            }
-            if (before >= b.kept)
-#pragma unroll
-                for (int i = 0; i < V; ++i) c[i] = no_key();
-        }
-        for (int j = 0; j < a.choices; ++j) {
-            double best = c[0];
-            int at = 0;
-#pragma unroll
-            for (int i = 1; i < V; ++i) {
-                const bool more = c[i] > best;
-                best = more ? c[i] : best;
-                at = more ? i : at;
-            }
-            const double m = lanes_max<LANES>(best);
-            const bool used = m > no_key();
-            const unsigned long long hit = __ballot(best == m);
-            int who;
-            if constexpr (LANES == 16) who = __builtin_ctz((unsigned)(hit >> (16 * group)) & 0xffffu);
-            else who = __builtin_ctzll(hit);
-            if (sub == who) {
-                mine[j] = used ? e0 + at : -1;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (i == at) c[i] = no_key();
-            }
         }
         wave_sync();
         // A lane a slot (two past LANES choices); their scores again.
@@ -251,7 +330,7 @@ __device__ __forceinline__ void balance_choose(const BalanceArgs &b, int first, 
                 e[q] = mine[sub + LANES * q];
                 if (e[q] >= 0) {
                     const double v = (double)to_f32(row[e[q]]);
-                    w[q] = b.softmax ? exp(v - top) / sum : sigmoid64(v);
+                    w[q] = b.softmax ? exp(v - (double)top) / sum : sigmoid64(v);
                 }
             }
         const double total = a.normalize ? lanes_sum<LANES>(w[0] + w[1]) : 1.0;
@@ -281,7 +360,7 @@ __global__ __launch_bounds__(kRouteThreads) void balance_one_kernel(BalanceArgs 
     int *const base = lds, *const carry = lds + a.groups, *const held = lds + a.groups + 2;
     for (int e = threadIdx.x; e < a.groups; e += kRouteThreads) base[e] = 0;
     __syncthreads();
-    balance_choose<E, LANES, V, kRouteThreads>(b, 0, base, held);
+    balance_choose<E, LANES, V, kRouteThreads, kRouteTokens>(b, 0, base, held);
     // The chosen experts are read back by other lanes of this workgroup.
     __threadfence_block();
     __syncthreads();
@@ -290,17 +369,25 @@ __global__ __launch_bounds__(kRouteThreads) void balance_one_kernel(BalanceArgs 
     else route_place<kRouteFewWaves>(a, 0, base, held);
 }
 
-// First of two launches (the second is route_place_kernel): choose and count.
-template <class E, int LANES, int V, int THREADS>
+// First of two launches: choose and count.
+template <class E, int LANES, int V, int THREADS, int TOKENS>
 __global__ __launch_bounds__(THREADS) void balance_choose_kernel(BalanceArgs b)
 {
     extern __shared__ int lds[];
     const RouteArgs &a = b.route;
     for (int e = threadIdx.x; e < a.groups; e += THREADS) lds[e] = 0;
     __syncthreads();
-    balance_choose<E, LANES, V, THREADS>(b, blockIdx.x * kRouteTokens, lds, lds + a.groups);
+    balance_choose<E, LANES, V, THREADS, TOKENS>(b, blockIdx.x * TOKENS, lds, lds + a.groups);
     __syncthreads();
     for (int e = threadIdx.x; e < a.groups; e += THREADS) a.counts[(long long)blockIdx.x * a.groups + e] = lds[e];
+}
+
+// Second, of parts that route_place_kernel does not have.
+template <int TOKENS>
+__global__ __launch_bounds__(kRouteThreads) void balance_place_kernel(RouteArgs a)
+{
+    extern __shared__ int lds[];
+    route_place_part<TOKENS>(a, lds);
 }
 
 template <class E, int V>

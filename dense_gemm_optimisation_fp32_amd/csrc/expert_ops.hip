@@ -158,7 +158,7 @@ int launch_int8_tiles(const GroupedArgs &a, const LpCall &c, int64_t rows, hipSt
 
 int64_t padded64(int64_t k) { return (k + 63) / 64 * 64; }
 
-constexpr int kOrthoParts = 64;            // workgroups that sum a matrix's squares, at most
+constexpr int kOrthoParts = 512;           // workgroups that sum a matrix's squares, at most
 constexpr int kOrthoMaxSteps = 64;
 constexpr int64_t kOrthoSpace = (int64_t)2 << 30;
 constexpr double kOrthoMost = 31.0;        // of a plane's entries
@@ -502,8 +502,9 @@ int expert_route_grad(int dtype, int64_t tokens, int64_t groups, int64_t choices
 
 int64_t expert_route_balanced_workspace(int64_t tokens, int64_t groups)
 {
-    if (!size_ok(tokens, 1) || !size_ok(groups, 1) || (tokens <= kRouteTokens && groups <= 256)) return 0;
-    return (tokens + kRouteTokens - 1) / kRouteTokens * groups * 4;
+    if (!size_ok(tokens, 1) || !size_ok(groups, 1) || (tokens <= kRouteTokens && groups <= 512)) return 0;
+    const int64_t part = tokens <= kBalanceFewTokens ? kBalancePart : kRouteTokens;
+    return (tokens + part - 1) / part * groups * 4;
 }
 
 int expert_route_balanced(int dtype, int64_t tokens, int64_t groups, int64_t choices, int scores, int64_t sets,
@@ -709,7 +710,7 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
         o.m_pad = (int)p.m_pad;
         o.n_pad = (int)p.n_pad;
         o.turned = turned;
-        const int64_t parts = (rows * ((cols + 7) / 8) + 1023) / 1024;       // four chunks of eight a thread
+        const int64_t parts = (rows * ((cols + 7) / 8) + 1023) / 1024;       // four chunks of eight a thread, or more
         o.parts = (int)(parts < kOrthoParts ? parts : kOrthoParts);
         o.sums = reinterpret_cast<double *>(g1 + p.chunk * p.planes * p.g_plane);
         o.planes = x0;

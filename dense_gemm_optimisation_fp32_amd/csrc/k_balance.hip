@@ -11,14 +11,22 @@ int launch_choose(const BalanceArgs &b, hipStream_t s)
 {
     const RouteArgs &a = b.route;
     // Half the threads where a lane's keys would not fit the registers of all.
-    constexpr int THREADS = V > 8 ? 512 : kRouteThreads;
+    constexpr int THREADS = V > 16 ? 512 : kRouteThreads;
     const int found = balance_found_words(LANES, THREADS, a.choices), place = route_place_words(a.groups);
-    if constexpr (V <= 8)
+    if constexpr (V <= 16)
         if (a.tokens <= kRouteTokens)
             return launch(balance_one_kernel<E, LANES, V>, 1, kRouteThreads,
                           (a.groups + 2 + (found > place ? found : place)) * 4, s, b);
+    if (a.tokens <= kBalanceFewTokens) {
+        constexpr int FEW = kBalancePart * LANES < 512 ? kBalancePart * LANES : 512;
+        const long long parts = (a.tokens + kBalancePart - 1ll) / kBalancePart;
+        const int st = launch(balance_choose_kernel<E, LANES, V, FEW, kBalancePart>, parts, FEW,
+                              (a.groups + balance_found_words(LANES, FEW, a.choices)) * 4, s, b);
+        if (st != GEMM_F32_SUCCESS) return st;
+        return launch(balance_place_kernel<kBalancePart>, parts, kRouteThreads, (a.groups + 2 + place) * 4, s, a);
+    }
     const long long parts = (a.tokens + kRouteTokens - 1ll) / kRouteTokens;
-    const int st = launch(balance_choose_kernel<E, LANES, V, THREADS>, parts, THREADS, (a.groups + found) * 4, s, b);
+    const int st = launch(balance_choose_kernel<E, LANES, V, THREADS, kRouteTokens>, parts, THREADS, (a.groups + found) * 4, s, b);
     if (st != GEMM_F32_SUCCESS) return st;
     return launch(route_place_kernel, parts, kRouteThreads, (a.groups + 2 + place) * 4, s, a);
 }

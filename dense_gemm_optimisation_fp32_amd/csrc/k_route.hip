@@ -7,39 +7,7 @@ namespace gemmf32 {
 __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a)
 {
     extern __shared__ int lds[];
-    int *const base = lds, *const carry = lds + a.groups, *const held = lds + (a.groups + 2) / 2 * 2;
-    int *const totals = held;   // until the places are counted
-    const int parts = gridDim.x;
-    // Threads share an expert where there are more threads than experts, each
-    // every share-th workgroup's counts, eight loads at a time.
-    const int share = max(1, kRouteThreads / a.groups);
-    for (int e = threadIdx.x; e < a.groups; e += kRouteThreads) base[e] = totals[e] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.groups * share; i += kRouteThreads) {
-        const int e = i % a.groups;
-        int before = 0, all = 0;
-        for (int b0 = i / a.groups; b0 < parts; b0 += 8 * share) {
-            int n[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int b = b0 + u * share;
-                n[u] = b < parts ? a.counts[(long long)b * a.groups + e] : 0;
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                all += n[u];
-                before += b0 + u * share < (int)blockIdx.x ? n[u] : 0;
-            }
-        }
-        atomicAdd(base + e, before);
-        atomicAdd(totals + e, all);
-    }
-    __syncthreads();
-    route_offsets(a, totals, carry, blockIdx.x == gridDim.x - 1);
-    for (int e = threadIdx.x; e < a.groups; e += kRouteThreads) base[e] += totals[e];
-    __syncthreads();
-    if (a.groups <= 512) route_place<kRouteWaves>(a, blockIdx.x * kRouteTokens, base, held);
-    else route_place<kRouteFewWaves>(a, blockIdx.x * kRouteTokens, base, held);
+    route_place_part<kRouteTokens>(a, lds);
 }
 
 namespace {

@@ -185,12 +185,12 @@ __device__ __forceinline__ void route_choose(const RouteArgs &a, int first, int 
 
 // Places the workgroup's slots.  `base` (LDS): where its slots of each
 // expert begin; `held` (LDS): the wavefronts' own counts.  W wavefronts place.
-template <int W>
+template <int W, int TOKENS = kRouteTokens>
 __device__ __forceinline__ void route_place(const RouteArgs &a, int first, int *base, int *held)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = a.choices, last = min(first + kRouteTokens, a.tokens);
-    constexpr int kPart = kRouteTokens / W;
+    const int c = a.choices, last = min(first + TOKENS, a.tokens);
+    constexpr int kPart = TOKENS / W;
     // A wavefront's slots, in order: those of its part of the tokens.
     const int s0 = min(first + wave * kPart, last) * c, s1 = wave < W ? min(first + (wave + 1) * kPart, last) * c : s0;
     int *const mine = held + (wave < W ? wave : 0) * a.groups;
@@ -295,6 +295,44 @@ __global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RouteArgs a
 }
 
 // Second: where each workgroup's slots of an expert begin, and their places.
+template <int TOKENS>
+__device__ __forceinline__ void route_place_part(const RouteArgs &a, int *lds)
+{
+    int *const base = lds, *const carry = lds + a.groups, *const held = lds + (a.groups + 2) / 2 * 2;
+    int *const totals = held;   // until the places are counted
+    const int parts = gridDim.x;
+    // Threads share an expert where there are more threads than experts, each
+    // every share-th workgroup's counts, eight loads at a time.
+    const int share = max(1, kRouteThreads / a.groups);
+    for (int e = threadIdx.x; e < a.groups; e += kRouteThreads) base[e] = totals[e] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.groups * share; i += kRouteThreads) {
+        const int e = i % a.groups;
+        int before = 0, all = 0;
+        for (int b0 = i / a.groups; b0 < parts; b0 += 8 * share) {
+            int n[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int b = b0 + u * share;
+                n[u] = b < parts ? a.counts[(long long)b * a.groups + e] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                all += n[u];
+                before += b0 + u * share < (int)blockIdx.x ? n[u] : 0;
+            }
+        }
+        atomicAdd(base + e, before);
+        atomicAdd(totals + e, all);
+    }
+    __syncthreads();
+    route_offsets(a, totals, carry, blockIdx.x == gridDim.x - 1);
+    for (int e = threadIdx.x; e < a.groups; e += kRouteThreads) base[e] += totals[e];
+    __syncthreads();
+    if (a.groups <= 512) route_place<kRouteWaves, TOKENS>(a, blockIdx.x * TOKENS, base, held);
+    else route_place<kRouteFewWaves, TOKENS>(a, blockIdx.x * TOKENS, base, held);
+}
+
 __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a);
 
 constexpr int kGradThreads = 256;
