@@ -13,6 +13,7 @@ struct Int8Args;
 struct Mx4Args;
 struct OrthoArgs;
 struct OrthoStartArgs;
+struct OrthoStripArgs;
 struct RouteArgs;
 
 // Bound on the row tiles of bm rows: each run of rows (the experts' and the
@@ -76,6 +77,9 @@ int launch_int8_64(const GroupedArgs &a, const LpCall &c, hipStream_t s);
 int launch_int8_64_ring(const GroupedArgs &a, const LpCall &c, hipStream_t s);
 int launch_int8_64_square(const GroupedArgs &a, const LpCall &c, hipStream_t s);
 int launch_int8_few(const GroupedArgs &a, bool bf16, int cu_count, hipStream_t s);
+// Matrices of few rows: strips of `blocks` x 64 columns (1, 2 or 4; one strip: 1 to 4).
+int launch_ortho_strips(const OrthoStripArgs &a, int blocks, bool bf16, bool first, int batch, hipStream_t s);
+int launch_ortho_squares(const OrthoStartArgs &a, bool bf16, int batch, hipStream_t s);
 int launch_ortho_start(const OrthoStartArgs &a, bool bf16, int batch, hipStream_t s);
 int launch_ortho_64_square(const OrthoArgs &a, const OrthoCall &c, hipStream_t s);
 int launch_ortho_64(const OrthoArgs &a, const OrthoCall &c, hipStream_t s);

@@ -8,7 +8,7 @@
 #include "expert_launch.hpp"
 #include "int8.hpp"
 #include "mx4.hpp"
-#include "orthogonal.hpp"
+#include "ortho_small.hpp"
 #include "route.hpp"
 
 using namespace gemmf32;
@@ -159,7 +159,6 @@ int launch_int8_tiles(const GroupedArgs &a, const LpCall &c, int64_t rows, hipSt
 int64_t padded64(int64_t k) { return (k + 63) / 64 * 64; }
 
 constexpr int kOrthoParts = 512;           // workgroups that sum a matrix's squares, at most
-constexpr int kOrthoMaxSteps = 64;
 constexpr int64_t kOrthoSpace = (int64_t)2 << 30;
 constexpr double kOrthoMost = 31.0;        // of a plane's entries
 
@@ -169,6 +168,7 @@ struct OrthoPlan {
     int64_t m, n, m_pad, n_pad;            // m <= n
     int planes;                            // of A and B
     int64_t x_plane, g_plane;              // bytes
+    int64_t blocks, strips;                // up to 64 rows: 64-column blocks of a strip, strips (else 0)
     int64_t matrix;                        // bytes of workspace a matrix
     int64_t chunk;
 
@@ -182,7 +182,17 @@ struct OrthoPlan {
         x_plane = m_pad * n_pad * 2;
         g_plane = m_pad * m_pad * 2;
         matrix = 4 * x_plane + 2 * planes * g_plane + kOrthoParts * 8;
-        chunk = kOrthoSpace / matrix;
+        blocks = strips = 0;
+        if (m <= kStripRows) {
+            // One strip (up to 256 columns), else sixteen at most up to 4096 columns.
+            // Measured in 32 bits, us: 64 x 256 in one strip 28.8, 64 x 384 in one 40.4 and in
+            // six, a launch a step, 40; by the tiles 82 for four of 64 x 192 (23.9 here).
+            const int64_t all = n_pad / 64;
+            blocks = all <= 4 ? all : all <= 16 ? 1 : all <= 32 ? 2 : 4;
+            strips = (all + blocks - 1) / blocks;
+            matrix = strips == 1 ? 0 : 2 * x_plane + 2 * strips * kStripRows * kStripRows * 4 + kOrthoParts * 8;
+        }
+        chunk = matrix ? kOrthoSpace / matrix : batch;
         chunk = chunk < 1 ? 1 : chunk > batch ? batch : chunk;
     }
 };
@@ -224,6 +234,43 @@ bool ortho_bounded(const float *coefficients, int steps)
         top = next * 1.001;                // (rounding)
     }
     return true;
+}
+
+// `batch` matrices of up to 64 rows; o: x and the planes at the workspace's start.
+int ortho_few_rows(const OrthoPlan &p, OrthoStartArgs o, int steps, const float *coefficients, float scale, bool bf16,
+                   int batch, char *y, int64_t ldy, int64_t stride_y, hipStream_t s)
+{
+    OrthoStripArgs a{};
+    a.strips = (int)p.strips;
+    a.steps = steps;
+    a.order = (int)p.m;
+    a.width = (int)p.n;
+    a.scale = scale;
+    a.ldy = ldy;
+    a.stride_y = stride_y;
+    if (p.strips == 1) {
+        a.start = o;
+        a.y = y;
+        for (int i = 0; i < 3 * steps; ++i) a.f[i] = coefficients[i];
+        return launch_ortho_strips(a, (int)p.blocks, bf16, false, batch, s);
+    }
+    const int64_t shares = p.strips * kStripRows * kStripRows;       // floats a matrix
+    float *const g0 = reinterpret_cast<float *>(o.planes + p.chunk * 2 * p.x_plane), *const g1 = g0 + p.chunk * shares;
+    o.sums = reinterpret_cast<double *>(g1 + p.chunk * shares);
+    int status = launch_ortho_squares(o, bf16, batch, s);
+    if (status != GEMM_F32_SUCCESS) return status;
+    a.start = o;
+    a.planes_out = o.planes;
+    a.shares_out = g0;
+    status = launch_ortho_strips(a, (int)p.blocks, bf16, true, batch, s);
+    for (int i = 0; i < steps && status == GEMM_F32_SUCCESS; ++i) {
+        a.shares = i % 2 ? g1 : g0;
+        a.shares_out = i % 2 ? g0 : g1;
+        for (int j = 0; j < 3; ++j) a.f[j] = coefficients[3 * i + j];
+        a.y = i + 1 == steps ? y : nullptr;
+        status = launch_ortho_strips(a, (int)p.blocks, bf16, false, batch, s);
+    }
+    return status;
 }
 
 int launch_ortho(const OrthoArgs &a, const OrthoCall &c, int cus, hipStream_t s)
@@ -712,10 +759,16 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
         o.turned = turned;
         const int64_t parts = (rows * ((cols + 7) / 8) + 1023) / 1024;       // four chunks of eight a thread, or more
         o.parts = (int)(parts < kOrthoParts ? parts : kOrthoParts);
-        o.sums = reinterpret_cast<double *>(g1 + p.chunk * p.planes * p.g_plane);
         o.planes = x0;
         o.plane = p.x_plane;
         o.matrix = 2 * p.x_plane;
+        if (p.strips) {
+            const int status = ortho_few_rows(p, o, steps, coefficients, scale, bf16, (int)here_,
+                                              static_cast<char *>(Y) + first * stride_y * size, ldy, stride_y, s);
+            if (status != GEMM_F32_SUCCESS) return status;
+            continue;
+        }
+        o.sums = reinterpret_cast<double *>(g1 + p.chunk * p.planes * p.g_plane);
         int status = launch_ortho_start(o, bf16, (int)here_, s);
         if (status != GEMM_F32_SUCCESS) return status;
 

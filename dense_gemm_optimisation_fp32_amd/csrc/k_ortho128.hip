@@ -8,9 +8,14 @@ int launch_ortho_128(const OrthoArgs &a, const OrthoCall &c, hipStream_t s)
     return launch_ortho_tiles<LpTile<128, 128, 2, 2, 2>>(a, c, s);
 }
 
+int launch_ortho_squares(const OrthoStartArgs &a, bool bf16, int batch, hipStream_t s)
+{
+    return launch(bf16 ? ortho_squares_kernel<__bf16> : ortho_squares_kernel<float>, (long long)a.parts * batch, 256, 0, s, a);
+}
+
 int launch_ortho_start(const OrthoStartArgs &a, bool bf16, int batch, hipStream_t s)
 {
-    const int st = launch(bf16 ? ortho_squares_kernel<__bf16> : ortho_squares_kernel<float>, (long long)a.parts * batch, 256, 0, s, a);
+    const int st = launch_ortho_squares(a, bf16, batch, s);
     if (st != GEMM_F32_SUCCESS) return st;
     return launch(bf16 ? ortho_start_kernel<__bf16> : ortho_start_kernel<float>,
                   (long long)(a.m_pad / 64) * (a.n_pad / 64) * batch, 256, 0, s, a);

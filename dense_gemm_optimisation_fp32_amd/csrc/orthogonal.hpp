@@ -30,6 +30,7 @@
 
 namespace gemmf32 {
 
+constexpr int kOrthoMaxSteps = 64;
 constexpr float kPlaneScale = 2048.0f, kPlaneBack = 1.0f / 2048.0f;
 
 struct OrthoArgs {

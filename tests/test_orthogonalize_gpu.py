@@ -48,7 +48,8 @@ def off(got, want):
 
 
 SHAPES = [(1, 1), (1, 5), (7, 1), (2, 3), (16, 16), (31, 65), (64, 64), (65, 64), (64, 192), (100, 333), (129, 127), (200, 1000),
-          (1000, 70), (256, 256), (320, 640), (513, 300), (700, 1100), (1300, 520)]
+          (1000, 70), (64, 128), (40, 250), (64, 384), (300, 64), (64, 385), (450, 33), (50, 1024), (1100, 64), (64, 2050), (20, 4200),
+          (5000, 64), (256, 256), (320, 640), (513, 300), (700, 1100), (1300, 520)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -61,7 +62,7 @@ def test_one_matrix(rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("batch,rows,cols", [(0, 8, 8), (1, 20, 30), (5, 64, 96), (33, 70, 40), (3, 300, 200), (9, 260, 513), (70, 256, 256)])
+@pytest.mark.parametrize("batch,rows,cols", [(0, 8, 8), (1, 20, 30), (5, 64, 96), (33, 70, 40), (6, 64, 500), (3, 300, 200), (9, 260, 513), (70, 256, 256)])
 def test_stacks(batch, rows, cols, dtype):
     x = normal((batch, rows, cols), dtype, batch) * torch.exp(3 * normal((batch, 1, 1), torch.float32, 1)).to(dtype)
     got = g.orthogonalize(x, scale=0.5)
@@ -141,9 +142,33 @@ def test_strides_out_and_in_place(rows, cols, dtype):
     assert torch.equal(g.orthogonalize(one), want[:1].expand(4, rows, cols))
 
 
-def test_turned_matrices_agree():
-    x = normal((70, 200), torch.float32, 9)
+@pytest.mark.parametrize("rows,cols", [(70, 200), (30, 100), (60, 900)])
+def test_turned_matrices_agree(rows, cols):
+    x = normal((rows, cols), torch.float32, 9)
     assert off(g.orthogonalize(x.t().contiguous()).t(), definition(x)) <= 1e-5
+
+
+@pytest.mark.parametrize("cols", [60, 350, 800])
+def test_few_rows_zeros_magnitudes_and_strides(cols):
+    x = normal((5, 40, cols), torch.float32, 6)
+    x[1] = 0
+    x[2, 3, 4] = float("inf")
+    x[3] *= 1e-30
+    x[4] *= 1e30
+    got = g.orthogonalize(x)
+    assert (got[1] == 0).all() and got[2].isnan().any()
+    for i in (0, 3, 4):
+        assert off(got[i], definition(x[i])) <= 1e-5
+    full = normal((3, 42, cols + 5), torch.bfloat16, 8)
+    part = full[:, 1:41, 3:3 + cols]
+    want = g.orthogonalize(part.contiguous())
+    before = full.clone()
+    g.orthogonalize(part, out=part)
+    assert torch.equal(part, want)
+    full[:, 1:41, 3:3 + cols] = before[:, 1:41, 3:3 + cols]
+    assert torch.equal(full, before)
+    for steps in (1, 2, 3, 6):
+        assert off(g.orthogonalize(x[0], steps=steps), definition(x[0], steps)) <= 1e-5
 
 
 def test_refusals():
@@ -169,8 +194,9 @@ def test_refusals():
         g.orthogonalize(x.expand(2, 8, 8), out=torch.empty((8, 8), device="cuda").expand(2, 8, 8))
 
 
-def test_captured_replayed_and_on_two_streams():
-    x = normal((2, 96, 200), torch.float32, 3)
+@pytest.mark.parametrize("rows,cols", [(96, 200), (40, 100), (600, 50)])
+def test_captured_replayed_and_on_two_streams(rows, cols):
+    x = normal((2, rows, cols), torch.float32, 3)
     want = g.orthogonalize(x)
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
@@ -184,7 +210,7 @@ def test_captured_replayed_and_on_two_streams():
     with torch.cuda.graph(graph):
         held = g.orthogonalize(x)
     for seed in range(3):
-        x.copy_(normal((2, 96, 200), torch.float32, 30 + seed))
+        x.copy_(normal((2, rows, cols), torch.float32, 30 + seed))
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(held, g.orthogonalize(x))
