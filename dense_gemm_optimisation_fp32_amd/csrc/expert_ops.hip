@@ -160,6 +160,7 @@ int64_t padded64(int64_t k) { return (k + 63) / 64 * 64; }
 
 constexpr int kOrthoParts = 512;           // workgroups that sum a matrix's squares, at most
 constexpr int64_t kOrthoSpace = (int64_t)2 << 30;
+constexpr int64_t kOrthoShares = (int64_t)512 * 256 * 256 * 4;      // bytes for shared tiles' sums
 constexpr double kOrthoMost = 31.0;        // of a plane's entries
 
 // How a batch is worked on: its planes, and as many matrices at a time as 2 GiB
@@ -171,6 +172,7 @@ struct OrthoPlan {
     int64_t blocks, strips;                // up to 64 rows: 64-column blocks of a strip, strips (else 0)
     int64_t matrix;                        // bytes of workspace a matrix
     int64_t chunk;
+    int64_t shares;                        // bytes for shared tiles' sums
 
     OrthoPlan(int dtype, int64_t batch, int64_t rows, int64_t cols)
     {
@@ -181,7 +183,7 @@ struct OrthoPlan {
         planes = dtype == EXPERT_BF16 ? 1 : 2;
         x_plane = m_pad * n_pad * 2;
         g_plane = m_pad * m_pad * 2;
-        matrix = 4 * x_plane + 2 * planes * g_plane + kOrthoParts * 8;
+        matrix = 4 * x_plane + 2 * planes * g_plane + kOrthoParts * 8 + 8;
         blocks = strips = 0;
         if (m <= kStripRows) {
             // One strip (up to 256 columns), else sixteen at most up to 4096 columns.
@@ -194,6 +196,9 @@ struct OrthoPlan {
         }
         chunk = matrix ? kOrthoSpace / matrix : batch;
         chunk = chunk < 1 ? 1 : chunk > batch ? batch : chunk;
+        // (As launch_ortho has it: small tiles a workgroup's each where they are few.)
+        const int64_t side = m_pad / 64;
+        shares = !strips && chunk * (side * (side + 1) / 2) > 256 ? kOrthoShares : 0;
     }
 };
 
@@ -273,15 +278,74 @@ int ortho_few_rows(const OrthoPlan &p, OrthoStartArgs o, int steps, const float 
     return status;
 }
 
-int launch_ortho(const OrthoArgs &a, const OrthoCall &c, int cus, hipStream_t s)
+// How a product runs: tiles and workgroups, and what that takes, about, in us.
+struct OrthoChoice {
+    enum Kind { SMALL, WIDE, MIDDLE, LARGE } kind;     // 64 x 64 and 64 x 128 a workgroup each; 128 and 256 in the pipeline
+    double us;
+    int64_t wgs, whole;                                // tiles [0, whole) a workgroup's each, the others shared
+};
+
+// The fastest by a model of what was measured on one MI355X (us; slabs of 64 in the
+// contraction; "shared" with the launch that joins):
+//   product             tiles of 64 / 64 x 128 / 128, shared / 256, shared
+//   1024^2, 48          21   -   49 24   79 33   (symmetric)
+//                       23  30   52 26   66 34
+//   2048^2, 96          83   -   90 61  132 57   (symmetric)
+//                      101  77   93 86  123 73
+//   4096^2, 192        488   -  379 284 272 256  (symmetric)
+//                      705 560  475  -  330  -
+//   16 x 2048^2, 64    580   -  380 376 328 320  (symmetric)
+//   1088 x 5056, 34     60  52   47 58   56 56
+// A slab costs more the more CUs are at work (the clock falls); a tile of 256 has 6 us
+// besides, 13 where it is stored on both sides of the diagonal; shares are written and
+// read.
+OrthoChoice ortho_choose(const OrthoArgs &a, int cus, bool may_share)
 {
+    const int64_t slabs = (int64_t)a.segments * (a.k / 64);
     const auto tiles = [&](int64_t bm, int64_t bn) {
-        return (int64_t)a.batch * ((a.rows + bm - 1) / bm) * ((a.cols + bn - 1) / bn);
+        const int64_t tm = (a.rows + bm - 1) / bm, tn = (a.cols + bn - 1) / bn;
+        return a.batch * (a.symmetric ? tm * (tm + 1) / 2 : tm * tn);
     };
-    if (tiles(64, 64) <= cus) return launch_ortho_64_square(a, c, s);
-    if (tiles(64, 128) <= 2 * cus) return launch_ortho_64(a, c, s);
-    if (tiles(256, 256) >= cus) return launch_ortho_256(a, c, s);
-    return launch_ortho_128(a, c, s);
+    const auto rounds = [](int64_t n, int64_t slots) { return (double)((n + slots - 1) / slots); };
+    const auto busy = [](int64_t n, int64_t slots) { return n < slots ? (double)n / slots : 1.0; };
+    OrthoChoice best{OrthoChoice::SMALL, 0.0, 0, 0};
+    const int64_t n64 = tiles(64, 64);
+    best.us = 2.0 + slabs * (n64 <= cus ? 0.43 : rounds(n64, 2 * cus) * 0.52);
+    const auto take = [&](OrthoChoice::Kind kind, double us, int64_t wgs, int64_t whole) {
+        if (us < best.us) best = OrthoChoice{kind, us, wgs, whole};
+    };
+    if (!a.symmetric) {
+        const int64_t n = tiles(64, 128);
+        take(OrthoChoice::WIDE, 2.0 + slabs * (n <= cus ? 0.62 : rounds(n, 2 * cus) * 0.75), 0, 0);
+    }
+    for (const int64_t side : {128, 256}) {
+        const bool large = side == 256;
+        const OrthoChoice::Kind kind = large ? OrthoChoice::LARGE : OrthoChoice::MIDDLE;
+        const int64_t n = tiles(side, side), slots = cus / a.num_xcd * a.num_xcd * (large ? 1 : 2), left = n % slots;
+        const double more = (a.symmetric ? 13.0 : 6.0) * (large ? 1.0 : 0.5);
+        const double slab = large ? 1.15 + 0.55 * busy(n, slots) : 0.75 + 0.5 * busy(n, slots);
+        take(kind, rounds(n, slots) * (slabs * slab + more), n < slots ? (n + a.num_xcd - 1) / a.num_xcd * a.num_xcd : slots, n);
+        // (A part of fewer than four slabs is all start and end.)
+        if (!may_share || left == 0 || (slots + left) * side * side * 4 > kOrthoShares || left * slabs < 4 * slots) continue;
+        const double full = large ? 1.7 : 1.25, share_mb = (slots + left) * side * side * 4 * 1e-6;
+        const double result_mb = left * side * side * 2e-6 * a.c_planes * (a.symmetric ? 2 : 1);
+        take(kind, n / slots * (slabs * full + more) + (double)(left * slabs) / slots * full + 8.0 + share_mb / 5.0 + 7.0 +
+                       share_mb / 7.0 + result_mb / 5.0, slots, n - left);
+    }
+    return best;
+}
+
+int launch_ortho(OrthoArgs a, const OrthoCall &c, int cus, hipStream_t s)
+{
+    const OrthoChoice o = ortho_choose(a, cus, a.shares && (c.what == kOrthoGram || c.what == kOrthoStep));
+    a.whole = (int)o.whole;
+    a.shared_wgs = (int)o.wgs;
+    switch (o.kind) {
+    case OrthoChoice::SMALL: return launch_ortho_64_square(a, c, s);
+    case OrthoChoice::WIDE: return launch_ortho_64(a, c, s);
+    case OrthoChoice::MIDDLE: return launch_ortho_128(a, c, o.wgs, s);
+    default: return launch_ortho_256(a, c, o.wgs, s);
+    }
 }
 
 }  // namespace
@@ -718,7 +782,7 @@ int64_t expert_orthogonalize_workspace(int dtype, int64_t batch, int64_t rows, i
 {
     if (!ortho_sizes_ok(dtype, batch, rows, cols) || batch == 0) return 0;
     const OrthoPlan p(dtype, batch, rows, cols);
-    return p.chunk * p.matrix;
+    return p.shares + p.chunk * p.matrix;
 }
 
 int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, const void *X, int64_t ldx,
@@ -733,7 +797,7 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
     if (batch > 1 && (stride_y < (rows - 1) * ldy + cols)) return GEMM_F32_ERR_INVALID_VALUE;
     if (batch > 0 && (!here(X, size) || !here(Y, size))) return GEMM_F32_ERR_INVALID_VALUE;
     const OrthoPlan p(dtype, batch, rows, cols);
-    // Workgroups, of 64 x 64 at least, are counted in 32 bits.
+    // Workgroups, of 64 x 64 at least, and slabs are counted in 32 bits.
     if (p.m_pad / 64 > kMaxInt / (p.n_pad / 64) || p.m_pad / 64 * (p.n_pad / 64) > kMaxInt / (p.chunk ? p.chunk : 1))
         return GEMM_F32_ERR_INVALID_VALUE;
     const int64_t need = expert_orthogonalize_workspace(dtype, batch, rows, cols);
@@ -746,7 +810,7 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
     const bool bf16 = dtype == EXPERT_BF16, turned = rows > cols;
     for (int64_t first = 0; first < batch; first += p.chunk) {
         const int64_t here_ = batch - first < p.chunk ? batch - first : p.chunk;
-        char *const x0 = static_cast<char *>(workspace), *const x1 = x0 + p.chunk * 2 * p.x_plane;
+        char *const x0 = static_cast<char *>(workspace) + p.shares, *const x1 = x0 + p.chunk * 2 * p.x_plane;
         char *const g0 = x1 + p.chunk * 2 * p.x_plane, *const g1 = g0 + p.chunk * p.planes * p.g_plane;
         OrthoStartArgs o{};
         o.x = static_cast<const char *>(X) + first * stride_x * size;
@@ -769,6 +833,8 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
             continue;
         }
         o.sums = reinterpret_cast<double *>(g1 + p.chunk * p.planes * p.g_plane);
+        // bfloat16: X times a power of two is exact in one plane.
+        if (p.planes == 1) o.factors = reinterpret_cast<float *>(o.sums + p.chunk * kOrthoParts);
         int status = launch_ortho_start(o, bf16, (int)here_, s);
         if (status != GEMM_F32_SUCCESS) return status;
 
@@ -783,12 +849,15 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
         gram.batch = (int)here_;
         gram.num_xcd = num_xcd;
         gram.segments = p.planes == 2 ? 3 : 1;
-        gram.b_second = gram.a_third = p.x_plane;
+        gram.a_low = gram.b_low = p.x_plane;
+        gram.a_at = 2;
         gram.C = g0;
         gram.ldc = p.m_pad * 2;
         gram.c_plane = p.g_plane;
         gram.c_planes = p.planes;
         gram.c = kPlaneBack;
+        gram.symmetric = 1;
+        gram.shares = p.shares ? static_cast<float *>(workspace) : nullptr;
 
         OrthoArgs poly = gram;                                               // B = a I + b A + c A A
         poly.A = poly.B = poly.G = g0;
@@ -796,18 +865,19 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
         poly.lda = poly.ldb = (int)(p.m_pad * 2);
         poly.a_bytes = poly.b_bytes = p.planes * p.g_plane;
         poly.k = (int)p.m_pad;
-        poly.b_second = poly.a_third = p.g_plane;
+        poly.a_low = poly.b_low = p.g_plane;
         poly.C = g1;
         poly.order = (int)p.m;
 
         OrthoArgs step = poly;                                               // B X
         step.G = nullptr;
+        step.symmetric = 0;
         step.A = g1;
         step.b_stride = step.c_stride = 2 * p.x_plane;
         step.ldb = (int)(p.n_pad * 2);
         step.b_bytes = 2 * p.x_plane;
         step.segments = p.planes == 2 ? 3 : 2;
-        step.b_second = p.x_plane;
+        step.b_low = p.x_plane;
         step.cols = (int)p.n_pad;
         step.ldc = p.n_pad * 2;
         step.c_plane = p.x_plane;
@@ -818,6 +888,9 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
         for (int i = 0; i < steps; ++i) {
             const float *const f = coefficients + 3 * i;
             gram.A = gram.B = now;
+            gram.factors = step.factors = i == 0 ? o.factors : nullptr;
+            gram.power = 2;
+            step.power = 1;
             status = launch_ortho(gram, OrthoCall{kOrthoGram, bf16, true}, cus, s);
             if (status != GEMM_F32_SUCCESS) return status;
             poly.a = f[0] * kPlaneScale;
@@ -825,9 +898,12 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
             poly.c = f[2] * kPlaneBack;
             status = launch_ortho(poly, OrthoCall{kOrthoGram, bf16, true}, cus, s);
             if (status != GEMM_F32_SUCCESS) return status;
+            // (One plane of X in the first step and in the last: see orthogonal.hpp.)
+            if (p.planes == 1) step.segments = i == 0 || i + 1 == steps ? 1 : 2;
             if (i + 1 < steps) {
                 step.B = now;
                 step.C = then;
+                step.c_planes = p.planes == 1 && i + 2 == steps ? 1 : 2;
                 status = launch_ortho(step, OrthoCall{kOrthoStep, bf16, true}, cus, s);
                 if (status != GEMM_F32_SUCCESS) return status;
                 char *const t = now;
@@ -848,8 +924,7 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
                 last.a_stride = step.b_stride, last.lda = step.ldb, last.a_bytes = step.b_bytes;
                 last.B = g1;
                 last.b_stride = step.a_stride, last.ldb = step.lda, last.b_bytes = step.a_bytes;
-                last.a_second = step.b_second, last.a_third = step.b_third;
-                last.b_second = step.a_second, last.b_third = step.a_third;
+                last.a_low = step.b_low, last.b_low = step.a_low, last.a_at = 1;
             } else {
                 last.B = now;
             }

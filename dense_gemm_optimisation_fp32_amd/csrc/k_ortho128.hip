@@ -3,9 +3,9 @@
 
 namespace gemmf32 {
 
-int launch_ortho_128(const OrthoArgs &a, const OrthoCall &c, hipStream_t s)
+int launch_ortho_128(const OrthoArgs &a, const OrthoCall &c, long long wgs, hipStream_t s)
 {
-    return launch_ortho_tiles<LpTile<128, 128, 2, 2, 2>>(a, c, s);
+    return launch_ortho_pipe<LpTile<128, 128, 2, 2, 2>>(a, c, wgs, s);
 }
 
 int launch_ortho_squares(const OrthoStartArgs &a, bool bf16, int batch, hipStream_t s)

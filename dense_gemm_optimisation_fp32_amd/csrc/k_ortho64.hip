@@ -1,4 +1,4 @@
-// Kernel translation unit: orthogonalising, small tiles.
+// Kernel translation unit: orthogonalising, a workgroup a small tile.
 #include "ortho_launch.hpp"
 
 namespace gemmf32 {

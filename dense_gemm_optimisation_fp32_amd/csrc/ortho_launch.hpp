@@ -3,37 +3,45 @@
 #pragma once
 
 #include "expert_launch.hpp"
-#include "orthogonal.hpp"
+#include "ortho_pipe.hpp"
 
 namespace gemmf32 {
 
-template <class T, bool A_KS, bool B_KS, class E, bool WIDE>
-int launch_ortho_kernel(const OrthoArgs &a, hipStream_t s)
-{
-    return launch(ortho_kernel<T, A_KS, B_KS, E, WIDE>, (long long)a.tiles_m * a.tiles_n * a.batch, T::THREADS, 0, s, a);
-}
+// KERNEL<T, A_KS, B_KS, E, WIDE> for what a call asks for.
+#define ORTHO_KERNELS(KERNEL, T, c)                                                                              \
+    ((c).what == kOrthoGram   ? KERNEL<T, false, false, _Float16, true>                                          \
+     : (c).what == kOrthoStep ? KERNEL<T, false, true, _Float16, true>                                           \
+     : (c).what == kOrthoLast                                                                                    \
+         ? ((c).bf16 ? ((c).wide ? KERNEL<T, false, true, __bf16, true> : KERNEL<T, false, true, __bf16, false>) \
+                     : ((c).wide ? KERNEL<T, false, true, float, true> : KERNEL<T, false, true, float, false>))  \
+         : ((c).bf16 ? ((c).wide ? KERNEL<T, true, false, __bf16, true> : KERNEL<T, true, false, __bf16, false>) \
+                     : ((c).wide ? KERNEL<T, true, false, float, true> : KERNEL<T, true, false, float, false>)))
 
 template <class T>
-int launch_ortho_tiles(OrthoArgs a, const OrthoCall &c, hipStream_t s)
+void ortho_count_tiles(OrthoArgs &a)
 {
     a.tiles_m = (a.rows + T::BM - 1) / T::BM;
     a.tiles_n = (a.cols + T::BN - 1) / T::BN;
-    switch (c.what) {
-    case kOrthoGram: return launch_ortho_kernel<T, false, false, _Float16, true>(a, s);
-    case kOrthoStep: return launch_ortho_kernel<T, false, true, _Float16, true>(a, s);
-    case kOrthoLast:
-        if (c.bf16)
-            return c.wide ? launch_ortho_kernel<T, false, true, __bf16, true>(a, s)
-                          : launch_ortho_kernel<T, false, true, __bf16, false>(a, s);
-        return c.wide ? launch_ortho_kernel<T, false, true, float, true>(a, s)
-                      : launch_ortho_kernel<T, false, true, float, false>(a, s);
-    default:
-        if (c.bf16)
-            return c.wide ? launch_ortho_kernel<T, true, false, __bf16, true>(a, s)
-                          : launch_ortho_kernel<T, true, false, __bf16, false>(a, s);
-        return c.wide ? launch_ortho_kernel<T, true, false, float, true>(a, s)
-                      : launch_ortho_kernel<T, true, false, float, false>(a, s);
-    }
+}
+
+// A workgroup a tile.
+template <class T>
+int launch_ortho_tiles(OrthoArgs a, const OrthoCall &c, hipStream_t s)
+{
+    ortho_count_tiles<T>(a);
+    return launch(ORTHO_KERNELS(ortho_kernel, T, c), (long long)ortho_tiles(a) * a.batch, T::THREADS, 0, s, a);
+}
+
+// The pipeline on `wgs` workgroups (a multiple of the XCDs), with tiles from
+// a.whole on shared, and those tiles' sums.
+template <class T>
+int launch_ortho_pipe(OrthoArgs a, const OrthoCall &c, long long wgs, hipStream_t s)
+{
+    ortho_count_tiles<T>(a);
+    const int st = launch(ORTHO_KERNELS(ortho_pipe_kernel, T, c), wgs, T::THREADS, 0, s, a);
+    const long long shared = (long long)ortho_tiles(a) * a.batch - a.whole;
+    if (st != GEMM_F32_SUCCESS || shared == 0) return st;
+    return launch(ortho_join_kernel<T>, shared * (T::BM / 32) * (T::BN / 32) / 4, 256, 0, s, a);
 }
 
 }  // namespace gemmf32

@@ -16,9 +16,10 @@
 // factor 2^11 keeps lo above the subnormals; entries stay below 2^15.9 / 2^11 = 31,
 // which the host derives from the coefficients.
 // bfloat16 results are rounded to 2^-9 at the end: for them A and B = a I + b A +
-// c A A are one plane and X two; A = hi hi^T, A A one product, B X two.  Measured in
-// the 2-norm against 64 bits: 0.0017 off with all planes (what the last rounding
-// gives), 0.0018 to 0.0024 so.
+// c A A are one plane and X two; A = hi hi^T, A A one product, B X two (in the first
+// step, where X is exact in one plane, and in the last, whose roundings no step
+// follows, one).  Measured in the 2-norm against 64 bits: 0.0017 off with all planes
+// (what the last rounding gives), 0.0018 to 0.0024 so.
 //
 // A plane is rows of whole 64 columns, rows a multiple of 64, zeros outside the
 // matrix; a matrix's planes lie one after the other.  The contraction goes over the
@@ -40,7 +41,10 @@ struct OrthoArgs {
     int lda, ldb;                      // bytes from row to row
     long long a_bytes, b_bytes;        // of a matrix's planes
     int segments, k;                   // pairs of planes; contraction of each, whole slabs
-    long long a_second, a_third, b_second, b_third;     // where the second and third pair lie
+    // Where the lo planes lie, and in which pairs they take part: A's in pair
+    // a_at, B's in the other one of 1 and 2 (pair 0 is hi hi).
+    long long a_low, b_low;
+    int a_at;
     int rows, cols;                    // of C
     int tiles_m, tiles_n, group_m, batch, num_xcd;
     // What becomes of the sums.
@@ -50,7 +54,57 @@ struct OrthoArgs {
     const char *G;                     // A's planes in B = a I + b A + c A A (else NULL)
     int order;                         // rows of the matrix that I has
     float a, b, c;                     // (c: the factor of the sums in every product)
+    // C is symmetric: the tiles on and below its diagonal are computed, and stored
+    // on both sides.
+    int symmetric;
+    // X / |X| of bfloat16 values is held as X times a power of two, exactly; what is
+    // left of 1 / |X|, a factor a matrix, goes to A squared (power 2) and to B X (1).
+    const float *factors;              // or NULL
+    int power;
+    // The pipelined kernel: tiles [0, whole) are a workgroup's each, the others'
+    // slabs are shared out evenly (see ortho_pipe.hpp).
+    int whole, shared_wgs;
+    float *shares;
 };
+
+// What the sums of a matrix's product are multiplied by.
+__device__ __forceinline__ float ortho_factor(const OrthoArgs &g, int matrix)
+{
+    if (!g.factors) return g.c;
+    const float f = g.factors[matrix];
+    return g.power == 2 ? g.c * (f * f) : g.c * f;
+}
+
+// Tiles of one matrix, and the place of tile `t`.
+__device__ __host__ __forceinline__ int ortho_tiles(const OrthoArgs &g)
+{
+    return g.symmetric ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n;
+}
+
+struct OrthoTile {
+    int matrix, tm, tn;
+};
+
+// (In scalar registers: the copies' descriptors come from them.)
+__device__ __forceinline__ OrthoTile ortho_tile(const OrthoArgs &g, int logical)
+{
+    const int tiles = ortho_tiles(g), in = logical % tiles;
+    int tm, tn;
+    if (g.symmetric) {
+        // Row by row: tm (tm + 1) / 2 <= in.
+        tm = (int)((sqrtf(8.0f * (float)in + 1.0f) - 1.0f) * 0.5f);
+        tm += (tm + 1) * (tm + 2) / 2 <= in ? 1 : 0;
+        tm -= tm * (tm + 1) / 2 > in ? 1 : 0;
+        tn = in - tm * (tm + 1) / 2;
+    } else {
+        const int width = g.group_m * g.tiles_n, first = in / width * g.group_m;
+        const int size = min(g.tiles_m - first, g.group_m);
+        tm = first + in % width % size;
+        tn = in % width / size;
+    }
+    return OrthoTile{__builtin_amdgcn_readfirstlane(logical / tiles), __builtin_amdgcn_readfirstlane(tm),
+                     __builtin_amdgcn_readfirstlane(tn)};
+}
 
 struct OrthoStartArgs {
     const char *x;
@@ -60,6 +114,7 @@ struct OrthoStartArgs {
     int turned;                        // planes of the transposed
     int parts;
     double *sums;                      // (batch, parts): squares
+    float *factors;                    // (batch), or NULL: X / |X| whole, in two planes
     char *planes;
     long long plane, matrix;           // bytes
 };
@@ -110,7 +165,8 @@ struct Planes {
     }
 };
 
-// x / |x| as planes, a block of 64 x 64 a workgroup.
+// x / |x| as planes, a block of 64 x 64 a workgroup; with factors x times a power
+// of two, in one.
 template <class E>
 __global__ __launch_bounds__(256) void ortho_start_kernel(OrthoStartArgs a)
 {
@@ -124,8 +180,16 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(OrthoStartArgs a)
         for (int i = threadIdx.x; i < a.parts; i += 64) sum += a.sums[(long long)matrix * a.parts + i];
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
-        // (A matrix of zeros stays one.)
-        if (threadIdx.x == 0) factor_of = sum == 0.0 ? 0.0 : (double)kPlaneScale / sqrt(sum);
+        if (threadIdx.x == 0) {
+            // (A matrix of zeros stays one.)
+            double whole = sum == 0.0 ? 0.0 : 1.0 / sqrt(sum);
+            if (a.factors) {
+                const double power = __builtin_bit_cast(double, __builtin_bit_cast(long long, whole) & 0x7ff0000000000000ll);
+                if (tile == 0) a.factors[matrix] = sum == 0.0 ? 0.0f : (float)(whole / power);
+                whole = power;
+            }
+            factor_of = whole * (double)kPlaneScale;
+        }
     }
     const E *const x = reinterpret_cast<const E *>(a.x) + matrix * a.stride;
     const int r0 = a.turned ? col0 : row0, c0 = a.turned ? row0 : col0;      // in x
@@ -160,53 +224,82 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(OrthoStartArgs a)
         }
         char *const q = out + ((long long)(row0 + r) * a.n_pad + col0 + c) * 2;
         *reinterpret_cast<f16x8 *>(q) = hi;
-        *reinterpret_cast<f16x8 *>(q + a.plane) = lo;
+        if (!a.factors) *reinterpret_cast<f16x8 *>(q + a.plane) = lo;
     }
 }
 
-// The sums' planes, whole runs of eight columns.  G: a I + b G + c sums.
+// Four lanes' four halves each, turned: of the lanes' halves number lane % 4.
+__device__ __forceinline__ u32x2 turn4(unsigned p01, unsigned p23, int lane)
+{
+    // (All lanes take part in each exchange: none of them behind a condition.)
+    unsigned x[4] = {mx_lane<0x00>(p01), mx_lane<0x55>(p01), mx_lane<0xaa>(p01), mx_lane<0xff>(p01)};
+    const unsigned y[4] = {mx_lane<0x00>(p23), mx_lane<0x55>(p23), mx_lane<0xaa>(p23), mx_lane<0xff>(p23)};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = lane & 2 ? y[k] : x[k];
+    const unsigned pick = lane & 1 ? 0x07060302u : 0x05040100u;
+    return u32x2{__builtin_amdgcn_perm(x[1], x[0], pick), __builtin_amdgcn_perm(x[3], x[2], pick)};
+}
+
+// A 32 x 32 block of the sums as planes, in runs of eight columns.  G: a I + b G +
+// c sums.  mirror: also at the place across the diagonal, where the lane's values
+// are a column: four lanes turn theirs, for runs of four.
+__device__ __forceinline__ void ortho_block(const OrthoArgs &g, int matrix, int row0, int col0, int lane, const f32x16 &acc,
+                                            bool mirror)
+{
+    const int l32 = lane & 31, half = lane >> 5, row = row0 + l32;
+    const float factor = ortho_factor(g, matrix);
+#pragma unroll
+    for (int v0 = 0; v0 < 16; v0 += 8) {
+        const int col = col0 + half * 8 + v0 * 2;
+        const long long at = row * g.ldc + (long long)col * 2;
+        float t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = acc[v0 + i] * factor;
+        if (g.G) {
+            const char *const p = g.G + matrix * g.c_stride + at;
+            const f16x8 hi = *reinterpret_cast<const f16x8 *>(p);
+            f16x8 lo = {};
+            if (g.c_planes > 1) lo = *reinterpret_cast<const f16x8 *>(p + g.c_plane);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                t[i] += g.b * ((float)hi[i] + (float)lo[i]);
+                if (col + i == row && row < g.order) t[i] += g.a;
+            }
+        }
+        f16x8 plane[2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const Planes p(t[i]);
+            plane[0][i] = p.hi;
+            plane[1][i] = p.lo;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (j >= g.c_planes) break;
+            char *const q = g.C + matrix * g.c_stride + j * g.c_plane;
+            *reinterpret_cast<f16x8 *>(q + at) = plane[j];
+            if (mirror) {
+                const u32x4 w = __builtin_bit_cast(u32x4, plane[j]);
+                const long long across = (long long)(row0 + (l32 & ~3)) * 2;
+                *reinterpret_cast<u32x2 *>(q + (col + (lane & 3)) * g.ldc + across) = turn4(w.x, w.y, lane);
+                *reinterpret_cast<u32x2 *>(q + (col + 4 + (lane & 3)) * g.ldc + across) = turn4(w.z, w.w, lane);
+            }
+        }
+    }
+}
+
+// The tile's.
 template <class T>
-__device__ __forceinline__ void ortho_store(const OrthoArgs &g, int matrix, int row0, int col0, int wr, int wc, int lane,
+__device__ __forceinline__ void ortho_store(const OrthoArgs &g, const OrthoTile &t, int wr, int wc, int lane,
                                             f32x16 (&acc)[T::MB][T::NB])
 {
-    const int l32 = lane & 31, half = lane >> 5;
 #pragma unroll
-    for (int mb = 0; mb < T::MB; ++mb) {
-        const int row = row0 + wr * T::WM + mb * 32 + l32;
-        if (row >= g.rows) continue;
+    for (int mb = 0; mb < T::MB; ++mb)
 #pragma unroll
-        for (int nb = 0; nb < T::NB; ++nb)
-#pragma unroll
-            for (int v0 = 0; v0 < 16; v0 += 8) {
-                const int col = col0 + wc * T::WN + nb * 32 + half * 8 + v0 * 2;
-                if (col >= g.cols) continue;
-                const long long at = row * g.ldc + (long long)col * 2;
-                float t[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) t[i] = acc[mb][nb][v0 + i] * g.c;
-                if (g.G) {
-                    const char *const p = g.G + matrix * g.c_stride + at;
-                    const f16x8 hi = *reinterpret_cast<const f16x8 *>(p);
-                    f16x8 lo = {};
-                    if (g.c_planes > 1) lo = *reinterpret_cast<const f16x8 *>(p + g.c_plane);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        t[i] += g.b * ((float)hi[i] + (float)lo[i]);
-                        if (col + i == row && row < g.order) t[i] += g.a;
-                    }
-                }
-                f16x8 hi, lo;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const Planes p(t[i]);
-                    hi[i] = p.hi;
-                    lo[i] = p.lo;
-                }
-                char *const q = g.C + matrix * g.c_stride + at;
-                *reinterpret_cast<f16x8 *>(q) = hi;
-                if (g.c_planes > 1) *reinterpret_cast<f16x8 *>(q + g.c_plane) = lo;
-            }
-    }
+        for (int nb = 0; nb < T::NB; ++nb) {
+            const int row0 = t.tm * T::BM + wr * T::WM + mb * 32, col0 = t.tn * T::BN + wc * T::WN + nb * 32;
+            if (row0 < g.rows && col0 < g.cols) ortho_block(g, t.matrix, row0, col0, lane, acc[mb][nb], g.symmetric && t.tm != t.tn);
+        }
 }
 
 // E: what C holds, planes (_Float16) or the result's type.
@@ -217,14 +310,8 @@ __global__ __launch_bounds__(T::THREADS) void ortho_kernel(OrthoArgs g)
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave % T::WAVES_M, wc = wave / T::WAVES_M;
-    const int tiles = g.tiles_m * g.tiles_n;
-    const int logical = xcd_contiguous(blockIdx.x, tiles * g.batch, g.num_xcd);
-    // (In scalar registers: the copies' descriptors come from them.)
-    const int matrix = __builtin_amdgcn_readfirstlane(logical / tiles), in = logical % tiles;
-    const int width = g.group_m * g.tiles_n, first = in / width * g.group_m;
-    const int size = min(g.tiles_m - first, g.group_m);
-    const int row = __builtin_amdgcn_readfirstlane((first + in % width % size) * T::BM);
-    const int col = __builtin_amdgcn_readfirstlane(in % width / size * T::BN);
+    const OrthoTile t = ortho_tile(g, xcd_contiguous(blockIdx.x, ortho_tiles(g) * g.batch, g.num_xcd));
+    const int matrix = t.matrix, row = t.tm * T::BM, col = t.tn * T::BN;
     LpProblem q{};
     const long long skip_a = A_KS ? (long long)row * 2 : (long long)row * g.lda;
     const long long skip_b = B_KS ? (long long)col * 2 : (long long)col * g.ldb;
@@ -232,8 +319,8 @@ __global__ __launch_bounds__(T::THREADS) void ortho_kernel(OrthoArgs g)
     q.b = {g.B + matrix * g.b_stride + skip_b, g.b_bytes - skip_b, g.ldb, g.cols - col};
     q.k = g.segments * g.k;
     q.segment = g.k / 64;
-    q.a_second = g.a_second, q.a_third = g.a_third;
-    q.b_second = g.b_second, q.b_third = g.b_third;
+    q.a_second = g.a_at == 1 ? g.a_low : 0, q.a_third = g.a_at == 2 ? g.a_low : 0;
+    q.b_second = g.a_at == 2 ? g.b_low : 0, q.b_third = g.a_at == 1 ? g.b_low : 0;
     f32x16 acc[T::MB][T::NB];
 #pragma unroll
     for (int mb = 0; mb < T::MB; ++mb)
@@ -242,12 +329,13 @@ __global__ __launch_bounds__(T::THREADS) void ortho_kernel(OrthoArgs g)
     LpLoop<T, kF16, A_KS, B_KS, 16 / sizeof(E)> loop{q, lds, tid, lane, wave, wr, wc};
     loop.run(acc);
     if constexpr (sizeof(E) == 2 && __is_same(E, _Float16)) {
-        ortho_store<T>(g, matrix, row, col, wr, wc, lane, acc);
+        ortho_store<T>(g, t, wr, wc, lane, acc);
     } else {
+        const float factor = ortho_factor(g, matrix);
 #pragma unroll
         for (int mb = 0; mb < T::MB; ++mb)
 #pragma unroll
-            for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] *= g.c;
+            for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] *= factor;
         lp_store<T, E, WIDE>(g.C + matrix * g.c_stride + row * g.ldc + (long long)col * sizeof(E), g.ldc, g.rows - row,
                              g.cols - col, nullptr, 0, wr, wc, lane, acc);
     }

@@ -23,7 +23,7 @@ def normal(shape, dtype, seed, scale=1.0):
 
 
 def definition(x, steps=5, coefficients=COEFFICIENTS, scale=1.0):
-    x = x.double().cpu()
+    x = x.double()
     if x.dim() == 3:
         return torch.stack([definition(v, steps, coefficients, scale) for v in x])
     if x.shape[0] > x.shape[1]:
@@ -44,7 +44,7 @@ def room(dtype):
 
 
 def off(got, want):
-    return ((got.double().cpu() - want).norm() / want.norm()).item()
+    return ((got.double() - want).norm() / want.norm()).item()
 
 
 SHAPES = [(1, 1), (1, 5), (7, 1), (2, 3), (16, 16), (31, 65), (64, 64), (65, 64), (64, 192), (100, 333), (129, 127), (200, 1000),
@@ -59,6 +59,21 @@ def test_one_matrix(rows, cols, dtype):
     got = g.orthogonalize(x)
     assert got.shape == x.shape and got.dtype == dtype
     assert off(got, definition(x)) <= room(dtype)
+
+
+# Whole rounds of large tiles, tiles shared by workgroups, both, and sizes that fit none.
+LARGE = [(1, 1500, 1600), (1, 2118, 2081), (1, 1027, 5003), (1, 5003, 1027), (3, 1100, 2300), (24, 520, 530), (70, 300, 280), (2, 2048, 2048),
+         (5, 1536, 1024)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("batch,rows,cols", LARGE)
+def test_large(batch, rows, cols, dtype):
+    x = normal((batch, rows, cols), dtype, rows)
+    got = g.orthogonalize(x)
+    assert torch.equal(got, g.orthogonalize(x))
+    for i in {0, batch // 2, batch - 1}:
+        assert off(got[i], definition(x[i])) <= room(dtype), i
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -130,7 +145,7 @@ def test_strides_out_and_in_place(rows, cols, dtype):
     want = g.orthogonalize(x.contiguous())
     assert torch.equal(g.orthogonalize(x), want)
     turned = g.orthogonalize(x.contiguous().transpose(1, 2).contiguous().transpose(1, 2))
-    assert off(turned, want.double().cpu()) <= room(dtype)
+    assert off(turned, want.double()) <= room(dtype)
     out = torch.full((3, rows + 1, cols + 1), 9.0, dtype=dtype, device="cuda")
     g.orthogonalize(x, out=out[:, 1:, 1:])
     assert torch.equal(out[:, 1:, 1:], want) and (out[:, 0] == 9).all() and (out[:, :, 0] == 9).all()
