@@ -141,6 +141,12 @@ bool counts_ok(int64_t m, int64_t groups)
 // Longest contraction of 8-bit products: 127 * 127 * k stays below 2^31.
 constexpr int64_t kInt8MaxK = 131072;
 
+// Up to this many values of X an expert, and so many bytes of LDS for a tile's
+// codes, the few-row kernel quantises them in every workgroup.  Measured, us, so / by
+// a launch of their own: 1 row of 4096, 4096 columns 7.2 / 8.0, 14336 columns 13.9 / 14.5;
+// 2 rows of 1024 over 8 experts 5.2 / 7.4; 4 rows of 4096 16.2 / 14.8, 16 of 1024 14 / 7.7.
+constexpr int64_t kInt8FewValues = 4096, kInt8FewBytes = 66 * 1024;
+
 int64_t padded16(int64_t k) { return (k + 15) / 16 * 16; }
 
 // The 8-bit tiles of `rows` rows an expert, by launch_tiles' rules (an
@@ -770,10 +776,16 @@ int expert_int8_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t group
     const hipStream_t s = stream_of(stream);
     const bool bf16 = dtype == EXPERT_BF16;
     const int64_t rows = mean_rows(m, groups);
+    const bool few = few_rows(false, true, rows, n, groups, cus);
+    if (few && rows * kpx <= kInt8FewValues && (m < 16 ? m : 16) * (kpx + 16) <= kInt8FewBytes) {
+        a.A = static_cast<const char *>(X);
+        a.lda = ldx * size;
+        return launch_int8_few(a, bf16, true, cus, s);
+    }
     const int quantised =
         launch_int8_quantize(Int8Args{static_cast<const char *>(X), xc, xs, ldx, (int)m, (int)k, (int)kpx}, bf16, false, s);
     if (quantised != GEMM_F32_SUCCESS) return quantised;
-    if (few_rows(false, true, rows, n, groups, cus)) return launch_int8_few(a, bf16, cus, s);
+    if (few) return launch_int8_few(a, bf16, false, cus, s);
     const LpCall c{false, bf16, true, false, wide_rows(Y, a.ldc, n, size), cus};
     return launch_int8_tiles(a, c, rows, s);
 }
