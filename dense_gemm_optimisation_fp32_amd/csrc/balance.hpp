@@ -390,19 +390,24 @@ __global__ __launch_bounds__(kRouteThreads) void balance_place_kernel(RouteArgs 
     route_place_part<TOKENS>(a, lds);
 }
 
-template <class E, int V>
+// Floats of a token's row: whole 16-byte pieces, rows on different banks.
+__device__ __host__ constexpr int balance_grad_row(int groups) { return (groups + 3) / 4 * 4 + 4; }
+
+// A token's gradient is put together in LDS: what every expert has
+// (0, or softmax's share), then the chosen ones' on top, a lane a slot; then it is
+// stored 16 bytes a lane.
+template <class E>
 __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(BalanceArgs b)
 {
-    // What each slot adds to its expert's gradient, for the 16 lanes that
-    // hold the token.
-    __shared__ Choice adds[kGradThreads / 16][kRouteMaxChoices];
+    extern __shared__ float all[];
     const RouteArgs &a = b.route;
     const int sub = threadIdx.x & 15;
     const int token = blockIdx.x * (kGradThreads / 16) + (threadIdx.x >> 4);
     if (token >= a.tokens) return;
-    Choice *const mine = adds[threadIdx.x >> 4];
+    const int row = balance_grad_row(a.groups);
+    float *const mine = all + (threadIdx.x >> 4) * row;
     const long long s0 = (long long)token * a.choices;
-    const E *const row = reinterpret_cast<const E *>(a.logits) + (long long)token * a.ld;
+    const E *const logits = reinterpret_cast<const E *>(a.logits) + (long long)token * a.ld;
     float w[2] = {}, g[2] = {};
     int e[2] = {-1, -1};
 #pragma unroll
@@ -416,61 +421,50 @@ __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(BalanceArgs 
         }
     }
     const float dot = row_sum(w[0] * g[0] + w[1] * g[1]);        // scale times the mean gradient
+    if (b.softmax && !a.normalize) {
+        float top = -__builtin_inff(), sum = 0.0f;
+        for (int i = sub; i < a.groups; i += 16) {
+            const float v = to_f32(logits[i]);
+            mine[i] = v;
+            top = fmaxf(top, v);
+        }
+        top = row_max(top);
+        top = top > -__builtin_inff() ? top : 0.0f;
+        for (int i = sub; i < a.groups; i += 16) {
+            const float v = mine[i], p = v == v ? expf(v - top) : 0.0f;
+            mine[i] = p;
+            sum += p;
+        }
+        sum = row_sum(sum);
+        const float each = sum > 0.0f ? -dot / sum : 0.0f;
+        for (int i = sub; i < a.groups; i += 16) mine[i] *= each;
+    } else {
+        for (int i = sub * 4; i < row; i += 64) *reinterpret_cast<f32x4 *>(mine + i) = f32x4{};
+    }
+    wave_sync();
     const float mean = a.normalize ? dot / b.scale : 0.0f;
 #pragma unroll
     for (int q = 0; q < 2; ++q)
-        if (sub + 16 * q < a.choices) {
+        if (e[q] >= 0) {
             float d = w[q] * (g[q] - mean);
             // 1 - s = sigmoid(-x), without the difference of two near ones.
-            if (!b.softmax && e[q] >= 0) d /= 1.0f + expf(to_f32(row[e[q]]));
-            mine[sub + 16 * q] = Choice{d, e[q]};
+            if (!b.softmax) d /= 1.0f + expf(to_f32(logits[e[q]]));
+            mine[e[q]] += d;
         }
-    float d[V];
-    if (b.softmax && !a.normalize) {
-        float x[V], top = -__builtin_inff(), sum = 0.0f;
-        route_load<E, V>(a, token, sub, x);
-#pragma unroll
-        for (int i = 0; i < V; ++i) top = fmaxf(top, x[i]);
-        top = row_max(top);
-        top = top > -__builtin_inff() ? top : 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            x[i] = expf(x[i] - top);
-            sum += x[i];
-        }
-        sum = row_sum(sum);
-        const float each = sum > 0.0f ? dot / sum : 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = -x[i] * each;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = 0.0f;
-    }
     wave_sync();
-    for (int j = 0; j < a.choices; ++j) {
-        const Choice c = mine[j];
-        const int i0 = c.expert - sub * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (c.expert >= 0 && i == i0) d[i] += c.logit;
-    }
-    E *p = reinterpret_cast<E *>(a.dlogits) + (long long)token * a.ldd + sub * V;
-    const int left = a.groups - sub * V;
+    E *const p = reinterpret_cast<E *>(a.dlogits) + (long long)token * a.ldd;
     constexpr int N = 16 / sizeof(E);                       // elements of a 16-byte store
     struct __attribute__((packed, aligned(sizeof(E)))) Some {
         E e[N];
     };
-#pragma unroll
-    for (int i0 = 0; i0 < V; i0 += N) {
-        if (V % N == 0 && left >= i0 + N) {
+    for (int i = sub * N; i < a.groups; i += 16 * N) {
+        if (i + N <= a.groups) {
             Some t;
 #pragma unroll
-            for (int i = 0; i < N; ++i) t.e[i] = (E)d[(i0 + i) % V];
-            *reinterpret_cast<Some *>(p + i0) = t;
+            for (int j = 0; j < N; ++j) t.e[j] = (E)mine[i + j];
+            *reinterpret_cast<Some *>(p + i) = t;
         } else {
-#pragma unroll
-            for (int i = i0; i < i0 + N && i < V; ++i)
-                if (i < left) p[i] = (E)d[i];
+            for (int j = i; j < a.groups; ++j) p[j] = (E)mine[j];
         }
     }
 }

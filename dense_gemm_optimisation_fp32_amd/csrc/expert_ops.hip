@@ -150,12 +150,14 @@ constexpr int64_t kInt8FewValues = 4096, kInt8FewBytes = 66 * 1024;
 int64_t padded16(int64_t k) { return (k + 15) / 16 * 16; }
 
 // The 8-bit tiles of `rows` rows an expert, by launch_tiles' rules (an
-// instruction takes as long, and a slab has as many bytes).
+// instruction takes as long, and a slab has as many bytes), but for 64 x 128 tiles
+// up to 72 rows: 32 experts of 65 rows, 32-bit results, 128 / 64, us: 4096 x 2048 85 / 89,
+// 4099 x 2048 95 / 87, 4099 x 2049 118 / 110.
 int launch_int8_tiles(const GroupedArgs &a, const LpCall &c, int64_t rows, hipStream_t s)
 {
     if (tiles_of(a, rows, 64, 64) <= c.cu_count) return launch_int8_64_square(a, c, s);
     if (tiles_of(a, rows, 64, 128) <= 2 * c.cu_count) return launch_int8_64_ring(a, c, s);
-    if (rows <= kSmallTileRows) return launch_int8_64(a, c, s);
+    if (rows <= kSmallTileRows + 8) return launch_int8_64(a, c, s);
     if (large_tiles(rows, a.m, a.n, a.groups, c.cu_count)) return launch_int8_256(a, c, s);
     return launch_int8_128(a, c, s);
 }

@@ -63,15 +63,8 @@ int launch_choose_e(BalanceArgs b, hipStream_t s)
 template <class E>
 int launch_grad_e(const BalanceArgs &b, hipStream_t s)
 {
-    const long long grid = (b.route.tokens + 15ll) / 16;
-    const int groups = b.route.groups;
-    if (groups <= 16) return launch(balance_grad_kernel<E, 1>, grid, kGradThreads, 0, s, b);
-    if (groups <= 32) return launch(balance_grad_kernel<E, 2>, grid, kGradThreads, 0, s, b);
-    if (groups <= 64) return launch(balance_grad_kernel<E, 4>, grid, kGradThreads, 0, s, b);
-    if (groups <= 128) return launch(balance_grad_kernel<E, 8>, grid, kGradThreads, 0, s, b);
-    if (groups <= 256) return launch(balance_grad_kernel<E, 16>, grid, kGradThreads, 0, s, b);
-    if (groups <= 512) return launch(balance_grad_kernel<E, 32>, grid, kGradThreads, 0, s, b);
-    return launch(balance_grad_kernel<E, 64>, grid, kGradThreads, 0, s, b);
+    return launch(balance_grad_kernel<E>, (b.route.tokens + 15ll) / 16, kGradThreads,
+                  (size_t)16 * balance_grad_row(b.route.groups) * 4, s, b);
 }
 
 }  // namespace
