@@ -811,8 +811,10 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
     if (batch > 1 && (stride_y < (rows - 1) * ldy + cols)) return GEMM_F32_ERR_INVALID_VALUE;
     if (batch > 0 && (!here(X, size) || !here(Y, size))) return GEMM_F32_ERR_INVALID_VALUE;
     const OrthoPlan p(dtype, batch, rows, cols);
-    // Workgroups, of 64 x 64 at least, and slabs are counted in 32 bits.
-    if (p.m_pad / 64 > kMaxInt / (p.n_pad / 64) || p.m_pad / 64 * (p.n_pad / 64) > kMaxInt / (p.chunk ? p.chunk : 1))
+    // A launch over the blocks of 64 x 64 holds less than 2^32 threads (256 each).
+    constexpr int64_t kMostBlocks = (1 << 24) - 1;
+    if (!p.strips && (p.m_pad / 64 > kMostBlocks / (p.n_pad / 64) ||
+                      (p.chunk && p.m_pad / 64 * (p.n_pad / 64) > kMostBlocks / p.chunk)))
         return GEMM_F32_ERR_INVALID_VALUE;
     const int64_t need = expert_orthogonalize_workspace(dtype, batch, rows, cols);
     if (need > 0 && !here(workspace, 16)) return GEMM_F32_ERR_INVALID_VALUE;

@@ -48,11 +48,17 @@ class ExpertLayer:
         self.b1 = torch.zeros((experts, hidden), device=device)
         self.w2 = normal(experts, hidden, width, scale=hidden ** -0.5)
 
+    def _route(self, logits):
+        return g.route(logits, self.choices)
+
+    def _route_grad(self, logits, r, grad):
+        return g.route_grad(logits, r, grad)
+
     def _dispatch(self, x, masked=None):
         logits = g.matmul(x.float(), self.router.float())
         if masked is not None:                       # (tokens, experts): experts a token may not use
             logits = logits.masked_fill(masked, float("-inf"))
-        r = g.route(logits, self.choices)
+        r = self._route(logits)
         # Slots without an expert follow the last expert's; their rows are zeros.
         used = (r.order >= 0).unsqueeze(1)
         token = (r.order.clamp(min=0) // self.choices).long()
@@ -83,7 +89,7 @@ class ExpertLayer:
         dz = (weight * dy_rows).to(x.dtype)
         slot_grad = torch.zeros(r.weights.numel(), device=x.device)
         slot_grad.index_add_(0, r.order.clamp(min=0).long(), (dy_rows * z.float()).sum(1) * used.squeeze(1))
-        dlogits = g.route_grad(logits, r, slot_grad.view_as(r.weights))
+        dlogits = self._route_grad(logits, r, slot_grad.view_as(r.weights))
 
         dw2 = g.grouped_weight_grad(h, dz, r.offsets)
         dh = g.grouped_linear(dz, self.w2.transpose(1, 2), r.offsets)

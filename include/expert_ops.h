@@ -34,7 +34,9 @@
  *    (GEMM_F32_ERR_INVALID_VALUE): route takes up to 2^29 - 128 tokens, its
  *    gradient 2^28 - 16; a 4-bit operand of rows of k columns has
  *    rows ceil(k / 512) up to 2^26 - 4; an 8-bit operand up to 2^26 - 4 rows of
- *    2048 columns, 2^24 - 1 longer ones; a product's tiles of 16 rows (up to 16
+ *    up to 2048 columns, 2^24 - 1 longer ones, rows ceil(k / 256) up to 2^26 - 4 back to
+ *    values, and tiles of 16 x 16 below 2^23 where its experts have 16 rows or fewer; a
+ *    product's tiles of 16 rows (up to 16
  *    rows an expert on average, else 64 or 128) and 32 to 128 columns, those
  *    of empty experts among them, are below 2^24.
  *  - Errors: GEMM_F32_ERR_INVALID_VALUE (an argument outside the above),
