@@ -83,6 +83,7 @@ int launch_ortho_strips(const OrthoStripArgs &a, int blocks, bool bf16, bool fir
 int launch_ortho_squares(const OrthoStartArgs &a, bool bf16, int batch, hipStream_t s);
 int launch_ortho_start(const OrthoStartArgs &a, bool bf16, int batch, hipStream_t s);
 int launch_ortho_64_square(const OrthoArgs &a, const OrthoCall &c, hipStream_t s);
+int launch_ortho_64_parts(const OrthoArgs &a, const OrthoCall &c, hipStream_t s);     // two parts of a workgroup share the slabs
 int launch_ortho_64(const OrthoArgs &a, const OrthoCall &c, hipStream_t s);
 int launch_ortho_128(const OrthoArgs &a, const OrthoCall &c, long long wgs, hipStream_t s);
 int launch_ortho_256(const OrthoArgs &a, const OrthoCall &c, long long wgs, hipStream_t s);

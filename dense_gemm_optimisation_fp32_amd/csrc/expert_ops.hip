@@ -288,22 +288,25 @@ int ortho_few_rows(const OrthoPlan &p, OrthoStartArgs o, int steps, const float 
 
 // How a product runs: tiles and workgroups, and what that takes, about, in us.
 struct OrthoChoice {
-    enum Kind { SMALL, WIDE, MIDDLE, LARGE } kind;     // 64 x 64 and 64 x 128 a workgroup each; 128 and 256 in the pipeline
+    // 64 x 64 (in two parts, in one) and 64 x 128 a workgroup each; 128 and 256 in the pipeline.
+    enum Kind { PARTS, SMALL, WIDE, MIDDLE, LARGE } kind;
     double us;
     int64_t wgs, whole;                                // tiles [0, whole) a workgroup's each, the others shared
 };
 
 // The fastest by a model of what was measured on one MI355X (us; slabs of 64 in the
 // contraction; "shared" with the launch that joins):
-//   product             tiles of 64 / 64 x 128 / 128, shared / 256, shared
-//   1024^2, 48          21   -   49 24   79 33   (symmetric)
-//                       23  30   52 26   66 34
-//   2048^2, 96          83   -   90 61  132 57   (symmetric)
-//                      101  77   93 86  123 73
-//   4096^2, 192        488   -  379 284 272 256  (symmetric)
-//                      705 560  475  -  330  -
-//   16 x 2048^2, 64    580   -  380 376 328 320  (symmetric)
-//   1088 x 5056, 34     60  52   47 58   56 56
+//   product             tiles of 64, in parts / 64 x 128 / 128, shared / 256, shared
+//   1024^2, 48          22 17   -   49 24   79 33   (symmetric)
+//                       23 18  30   52 26   66 34
+//   1536^2, 72          40 45   -   70 38  109 42   (symmetric)
+//   2048^2, 96          83  -   -   90 61  132 57   (symmetric)
+//                      101  -  77   93 86  123 73
+//   4096^2, 192        488  -   -  379 284 272 256  (symmetric)
+//                      705  - 560  475  -  330  -
+//   16 x 2048^2, 64    580  -   -  380 376 328 320  (symmetric)
+//   1088 x 5056, 34     60  -  52   47 58   56 56
+//   1088^2, 79          32 25   -   72 30  103 39   (symmetric)
 // A slab costs more the more CUs are at work (the clock falls); a tile of 256 has 6 us
 // besides, 13 where it is stored on both sides of the diagonal; shares are written and
 // read.
@@ -316,9 +319,9 @@ OrthoChoice ortho_choose(const OrthoArgs &a, int cus, bool may_share)
     };
     const auto rounds = [](int64_t n, int64_t slots) { return (double)((n + slots - 1) / slots); };
     const auto busy = [](int64_t n, int64_t slots) { return n < slots ? (double)n / slots : 1.0; };
-    OrthoChoice best{OrthoChoice::SMALL, 0.0, 0, 0};
     const int64_t n64 = tiles(64, 64);
-    best.us = 2.0 + slabs * (n64 <= cus ? 0.43 : rounds(n64, 2 * cus) * 0.52);
+    OrthoChoice best{n64 <= cus ? OrthoChoice::PARTS : OrthoChoice::SMALL,
+                     2.0 + slabs * (n64 <= cus ? 0.33 : rounds(n64, 2 * cus) * 0.52), 0, 0};
     const auto take = [&](OrthoChoice::Kind kind, double us, int64_t wgs, int64_t whole) {
         if (us < best.us) best = OrthoChoice{kind, us, wgs, whole};
     };
@@ -349,6 +352,7 @@ int launch_ortho(OrthoArgs a, const OrthoCall &c, int cus, hipStream_t s)
     a.whole = (int)o.whole;
     a.shared_wgs = (int)o.wgs;
     switch (o.kind) {
+    case OrthoChoice::PARTS: return launch_ortho_64_parts(a, c, s);
     case OrthoChoice::SMALL: return launch_ortho_64_square(a, c, s);
     case OrthoChoice::WIDE: return launch_ortho_64(a, c, s);
     case OrthoChoice::MIDDLE: return launch_ortho_128(a, c, o.wgs, s);

@@ -318,6 +318,9 @@ struct LpProblem {
     // slabs each; where the second and the third lie from p on.
     int segment;
     long long a_second, a_third, b_second, b_third;
+    // Planes: of every `share` neighbouring slabs this workgroup's part of the
+    // wavefronts multiplies number `turn`.
+    int share, turn;
 };
 
 // REG: operands whose rows are not 4-byte aligned (bfloat16 rows of odd
@@ -361,6 +364,7 @@ struct LpLoop {
         }
         slabs = (q.k + KSLAB - 1) / KSLAB;
         tail = q.k % KSLAB;
+        if constexpr (KIND == kF16) slabs = (slabs + q.share - 1) / q.share;
     }
 
     // Copies of slab kt: descriptors of the operands from the slab's first k on.
@@ -375,15 +379,18 @@ struct LpLoop {
         c.st = stage(kt % T::STAGES);
         c.left = q.k - kt * KSLAB;
         int at = kt;
-        long long pa = 0, pb = 0;
+        long long pa = 0, pb = 0, none = 0;
         if constexpr (KIND == kF16) {
+            at = kt * q.share + q.turn;
+            // (Past the last slab, where they are not whole shares: no bytes, zeros.)
+            none = at * KSLAB >= q.k ? 1ll << 62 : 0;
             if (at >= q.segment) at -= q.segment, pa = q.a_second, pb = q.b_second;
             if (at >= q.segment) at -= q.segment, pa = q.a_third, pb = q.b_third;
         }
         const long long sa = pa + (A_KS ? (long long)at * KSLAB * q.a.ld : (long long)at * (T::CPR * 16));
         const long long sb = pb + (B_KS ? (long long)at * KSLAB * q.b.ld : (long long)at * (T::CPR * 16));
-        c.a = lp_rsrc(q.a.p + sa, q.a.bytes - sa);
-        c.b = lp_rsrc(q.b.p + sb, q.b.bytes - sb);
+        c.a = lp_rsrc(q.a.p + sa, q.a.bytes - sa - none);
+        c.b = lp_rsrc(q.b.p + sb, q.b.bytes - sb - none);
         if constexpr (KIND == kFp4) {
             const long long k = (long long)(T::KBLOCKS * kt) * (s_is_a ? q.a_scale_step : q.b_scale_step);
             c.s = lp_rsrc(reinterpret_cast<const char *>(s_is_a ? q.a_scales : q.b_scales) + k,

@@ -7,15 +7,15 @@
 
 namespace gemmf32 {
 
-// KERNEL<T, A_KS, B_KS, E, WIDE> for what a call asks for.
-#define ORTHO_KERNELS(KERNEL, T, c)                                                                              \
-    ((c).what == kOrthoGram   ? KERNEL<T, false, false, _Float16, true>                                          \
-     : (c).what == kOrthoStep ? KERNEL<T, false, true, _Float16, true>                                           \
+// KERNEL<..., A_KS, B_KS, E, WIDE> for what a call asks for.
+#define ORTHO_KERNELS(c, KERNEL, ...)                                                                              \
+    ((c).what == kOrthoGram   ? KERNEL<__VA_ARGS__, false, false, _Float16, true>                                          \
+     : (c).what == kOrthoStep ? KERNEL<__VA_ARGS__, false, true, _Float16, true>                                           \
      : (c).what == kOrthoLast                                                                                    \
-         ? ((c).bf16 ? ((c).wide ? KERNEL<T, false, true, __bf16, true> : KERNEL<T, false, true, __bf16, false>) \
-                     : ((c).wide ? KERNEL<T, false, true, float, true> : KERNEL<T, false, true, float, false>))  \
-         : ((c).bf16 ? ((c).wide ? KERNEL<T, true, false, __bf16, true> : KERNEL<T, true, false, __bf16, false>) \
-                     : ((c).wide ? KERNEL<T, true, false, float, true> : KERNEL<T, true, false, float, false>)))
+         ? ((c).bf16 ? ((c).wide ? KERNEL<__VA_ARGS__, false, true, __bf16, true> : KERNEL<__VA_ARGS__, false, true, __bf16, false>) \
+                     : ((c).wide ? KERNEL<__VA_ARGS__, false, true, float, true> : KERNEL<__VA_ARGS__, false, true, float, false>))  \
+         : ((c).bf16 ? ((c).wide ? KERNEL<__VA_ARGS__, true, false, __bf16, true> : KERNEL<__VA_ARGS__, true, false, __bf16, false>) \
+                     : ((c).wide ? KERNEL<__VA_ARGS__, true, false, float, true> : KERNEL<__VA_ARGS__, true, false, float, false>)))
 
 template <class T>
 void ortho_count_tiles(OrthoArgs &a)
@@ -24,12 +24,12 @@ void ortho_count_tiles(OrthoArgs &a)
     a.tiles_n = (a.cols + T::BN - 1) / T::BN;
 }
 
-// A workgroup a tile.
-template <class T>
+// A workgroup a tile, in K parts.
+template <class T, int K>
 int launch_ortho_tiles(OrthoArgs a, const OrthoCall &c, hipStream_t s)
 {
     ortho_count_tiles<T>(a);
-    return launch(ORTHO_KERNELS(ortho_kernel, T, c), (long long)ortho_tiles(a) * a.batch, T::THREADS, 0, s, a);
+    return launch(ORTHO_KERNELS(c, ortho_kernel, T, K), (long long)ortho_tiles(a) * a.batch, T::THREADS * K, 0, s, a);
 }
 
 // The pipeline on `wgs` workgroups (a multiple of the XCDs), with tiles from
@@ -38,7 +38,7 @@ template <class T>
 int launch_ortho_pipe(OrthoArgs a, const OrthoCall &c, long long wgs, hipStream_t s)
 {
     ortho_count_tiles<T>(a);
-    const int st = launch(ORTHO_KERNELS(ortho_pipe_kernel, T, c), wgs, T::THREADS, 0, s, a);
+    const int st = launch(ORTHO_KERNELS(c, ortho_pipe_kernel, T), wgs, T::THREADS, 0, s, a);
     const long long shared = (long long)ortho_tiles(a) * a.batch - a.whole;
     if (st != GEMM_F32_SUCCESS || shared == 0) return st;
     return launch(ortho_join_kernel<T>, shared * (T::BM / 32) * (T::BN / 32) / 4, 256, 0, s, a);

@@ -302,12 +302,16 @@ __device__ __forceinline__ void ortho_store(const OrthoArgs &g, const OrthoTile 
         }
 }
 
-// E: what C holds, planes (_Float16) or the result's type.
-template <class T, bool A_KS, bool B_KS, class E, bool WIDE>
-__global__ __launch_bounds__(T::THREADS) void ortho_kernel(OrthoArgs g)
+// A workgroup a tile.  E: what C holds, planes (_Float16) or the result's type.
+// K: parts of the workgroup that share the slabs, each with a ring of its own; their
+// sums meet in LDS.  A part of four wavefronts, one a SIMD, waits most of a slab for
+// LDS and its own products.
+template <class T, int K, bool A_KS, bool B_KS, class E, bool WIDE>
+__global__ __launch_bounds__(T::THREADS * K) void ortho_kernel(OrthoArgs g)
 {
-    __shared__ i32x4 lds[T::STAGES * T::stage_chunks(kF16)];
-    const int tid = threadIdx.x, lane = tid & 63;
+    __shared__ i32x4 lds[K * T::STAGES * T::stage_chunks(kF16)];
+    const int part = K > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / T::THREADS) : 0;
+    const int tid = threadIdx.x % T::THREADS, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave % T::WAVES_M, wc = wave / T::WAVES_M;
     const OrthoTile t = ortho_tile(g, xcd_contiguous(blockIdx.x, ortho_tiles(g) * g.batch, g.num_xcd));
@@ -321,14 +325,38 @@ __global__ __launch_bounds__(T::THREADS) void ortho_kernel(OrthoArgs g)
     q.segment = g.k / 64;
     q.a_second = g.a_at == 1 ? g.a_low : 0, q.a_third = g.a_at == 2 ? g.a_low : 0;
     q.b_second = g.a_at == 2 ? g.b_low : 0, q.b_third = g.a_at == 1 ? g.b_low : 0;
+    q.share = K;
+    q.turn = part;
     f32x16 acc[T::MB][T::NB];
 #pragma unroll
     for (int mb = 0; mb < T::MB; ++mb)
 #pragma unroll
         for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] = f32x16{};
-    LpLoop<T, kF16, A_KS, B_KS, 16 / sizeof(E)> loop{q, lds, tid, lane, wave, wr, wc};
+    LpLoop<T, kF16, A_KS, B_KS, 16 / sizeof(E)> loop{q, lds + part * T::STAGES * T::stage_chunks(kF16), tid, lane, wave, wr, wc};
     loop.run(acc);
-    if constexpr (sizeof(E) == 2 && __is_same(E, _Float16)) {
+    if constexpr (K > 1) {
+        constexpr int SUMS = T::MB * T::NB * 4;              // of four, a lane
+        static_assert((K - 1) * T::THREADS * SUMS <= K * T::STAGES * T::stage_chunks(kF16), "the sums fit the rings");
+        f32x4 *const sums = reinterpret_cast<f32x4 *>(lds) + tid;
+        __syncthreads();
+        if (part > 0)
+#pragma unroll
+            for (int i = 0; i < SUMS; ++i) {
+                const f32x16 &x = acc[i / 4 / T::NB][i / 4 % T::NB];
+                sums[((part - 1) * SUMS + i) * T::THREADS] = f32x4{x[i % 4 * 4], x[i % 4 * 4 + 1], x[i % 4 * 4 + 2], x[i % 4 * 4 + 3]};
+            }
+        __syncthreads();
+        if (part > 0) return;
+#pragma unroll
+        for (int p = 0; p < K - 1; ++p)
+#pragma unroll
+            for (int i = 0; i < SUMS; ++i) {
+                const f32x4 x = sums[(p * SUMS + i) * T::THREADS];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i / 4 / T::NB][i / 4 % T::NB][i % 4 * 4 + j] += x[j];
+            }
+    }
+    if constexpr (__is_same(E, _Float16)) {
         ortho_store<T>(g, t, wr, wc, lane, acc);
     } else {
         const float factor = ortho_factor(g, matrix);
