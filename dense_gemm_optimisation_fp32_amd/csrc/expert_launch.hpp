@@ -78,7 +78,8 @@ int launch_int8_64_ring(const GroupedArgs &a, const LpCall &c, hipStream_t s);
 int launch_int8_64_square(const GroupedArgs &a, const LpCall &c, hipStream_t s);
 // quantise: A holds the rows of X, which every workgroup quantises for itself.
 int launch_int8_few(const GroupedArgs &a, bool bf16, bool quantise, int cu_count, hipStream_t s);
-// Matrices of few rows: strips of `blocks` x 64 columns (1, 2 or 4; one strip: 1 to 4).
+// Matrices of few rows: strips of `blocks` x 64 columns (1, 2 or 4; one strip: 1 to 4; of
+// more than 64 rows 1 or 2).
 int launch_ortho_strips(const OrthoStripArgs &a, int blocks, bool bf16, bool first, int batch, hipStream_t s);
 int launch_ortho_squares(const OrthoStartArgs &a, bool bf16, int batch, hipStream_t s);
 int launch_ortho_start(const OrthoStartArgs &a, bool bf16, int batch, hipStream_t s);

@@ -141,10 +141,11 @@ bool counts_ok(int64_t m, int64_t groups)
 // Longest contraction of 8-bit products: 127 * 127 * k stays below 2^31.
 constexpr int64_t kInt8MaxK = 131072;
 
-// Up to this many values of X an expert, and so many bytes of LDS for a tile's
-// codes, the few-row kernel quantises them in every workgroup.  Measured, us, so / by
+// Up to two rows and this many values of X an expert, and so many bytes of LDS for
+// a tile's codes, the few-row kernel quantises them in every workgroup.  Measured, us, so / by
 // a launch of their own: 1 row of 4096, 4096 columns 7.2 / 8.0, 14336 columns 13.9 / 14.5;
-// 2 rows of 1024 over 8 experts 5.2 / 7.4; 4 rows of 4096 16.2 / 14.8, 16 of 1024 14 / 7.7.
+// 2 rows of 1024 over 8 experts 5.2 / 7.4; 4 rows of 4096 16.2 / 14.8, 16 of 1024 14 / 7.7, 11 of
+// 256 for each of 42 experts 79 / 20.
 constexpr int64_t kInt8FewValues = 4096, kInt8FewBytes = 66 * 1024;
 
 int64_t padded16(int64_t k) { return (k + 15) / 16 * 16; }
@@ -177,7 +178,7 @@ struct OrthoPlan {
     int64_t m, n, m_pad, n_pad;            // m <= n
     int planes;                            // of A and B
     int64_t x_plane, g_plane;              // bytes
-    int64_t blocks, strips;                // up to 64 rows: 64-column blocks of a strip, strips (else 0)
+    int64_t blocks, strips;                // few rows: 64-column blocks of a strip, strips (else 0)
     int64_t matrix;                        // bytes of workspace a matrix
     int64_t chunk;
     int64_t shares;                        // bytes for shared tiles' sums
@@ -192,15 +193,18 @@ struct OrthoPlan {
         x_plane = m_pad * n_pad * 2;
         g_plane = m_pad * m_pad * 2;
         matrix = 4 * x_plane + 2 * planes * g_plane + kOrthoParts * 8 + 8;
+        // Few rows: one strip (up to 256 columns, of 128 rows 128), else sixteen at most
+        // up to 4096 columns, of 128 rows eight.  Measured, us: four of 64 x 192 25, by the
+        // tiles 82; 64 x 384 in one strip 40.4, in six, a launch a step, 40; 128 x 128 in 32
+        // bits 56, by the tiles 102, in bfloat16 56 / 80; 128 x 512 86 / about 120 and 86 / 87, 128 x 1024
+        // 107 / about 150 and 107 / 96.
+        const int64_t all = n_pad / 64;
         blocks = strips = 0;
-        if (m <= kStripRows) {
-            // One strip (up to 256 columns), else sixteen at most up to 4096 columns.
-            // Measured in 32 bits, us: 64 x 256 in one strip 28.8, 64 x 384 in one 40.4 and in
-            // six, a launch a step, 40; by the tiles 82 for four of 64 x 192 (23.9 here).
-            const int64_t all = n_pad / 64;
-            blocks = all <= 4 ? all : all <= 16 ? 1 : all <= 32 ? 2 : 4;
+        if (m <= 64) blocks = all <= 4 ? all : all <= 16 ? 1 : all <= 32 ? 2 : 4;
+        else if (m <= 128 && all <= (dtype == EXPERT_BF16 ? 8 : 16)) blocks = all <= 2 ? all : all <= 8 ? 1 : 2;
+        if (blocks) {
             strips = (all + blocks - 1) / blocks;
-            matrix = strips == 1 ? 0 : 2 * x_plane + 2 * strips * kStripRows * kStripRows * 4 + kOrthoParts * 8;
+            matrix = strips == 1 ? 0 : 2 * x_plane + 2 * strips * m_pad * m_pad * 4 + kOrthoParts * 8;
         }
         chunk = matrix ? kOrthoSpace / matrix : batch;
         chunk = chunk < 1 ? 1 : chunk > batch ? batch : chunk;
@@ -249,7 +253,7 @@ bool ortho_bounded(const float *coefficients, int steps)
     return true;
 }
 
-// `batch` matrices of up to 64 rows; o: x and the planes at the workspace's start.
+// `batch` matrices of few rows; o: x and the planes at the workspace's start.
 int ortho_few_rows(const OrthoPlan &p, OrthoStartArgs o, int steps, const float *coefficients, float scale, bool bf16,
                    int batch, char *y, int64_t ldy, int64_t stride_y, hipStream_t s)
 {
@@ -267,7 +271,7 @@ int ortho_few_rows(const OrthoPlan &p, OrthoStartArgs o, int steps, const float 
         for (int i = 0; i < 3 * steps; ++i) a.f[i] = coefficients[i];
         return launch_ortho_strips(a, (int)p.blocks, bf16, false, batch, s);
     }
-    const int64_t shares = p.strips * kStripRows * kStripRows;       // floats a matrix
+    const int64_t shares = p.strips * p.m_pad * p.m_pad;             // floats a matrix
     float *const g0 = reinterpret_cast<float *>(o.planes + p.chunk * 2 * p.x_plane), *const g1 = g0 + p.chunk * shares;
     o.sums = reinterpret_cast<double *>(g1 + p.chunk * shares);
     int status = launch_ortho_squares(o, bf16, batch, s);
@@ -783,7 +787,7 @@ int expert_int8_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t group
     const bool bf16 = dtype == EXPERT_BF16;
     const int64_t rows = mean_rows(m, groups);
     const bool few = few_rows(false, true, rows, n, groups, cus);
-    if (few && rows * kpx <= kInt8FewValues && (m < 16 ? m : 16) * (kpx + 16) <= kInt8FewBytes) {
+    if (few && rows <= 2 && rows * kpx <= kInt8FewValues && (m < 16 ? m : 16) * (kpx + 16) <= kInt8FewBytes) {
         a.A = static_cast<const char *>(X);
         a.lda = ldx * size;
         return launch_int8_few(a, bf16, true, cus, s);

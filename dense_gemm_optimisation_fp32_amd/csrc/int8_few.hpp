@@ -1,8 +1,9 @@
 // 8-bit products where an expert has few rows (decoding): bound by the bytes of
 // the experts' codes, each read once.
 //
-// A workgroup takes 16 rows of one expert and a strip of columns, its
-// wavefronts split k, as in grouped_few.hpp.  Codes go straight from memory into
+// A workgroup takes 16 rows of one expert and a strip of columns, KW of its
+// wavefronts split k, as in grouped_few.hpp, and CW of them the strip (short k: a
+// workgroup has to have work for all).  Codes go straight from memory into
 // registers, 16 bytes a lane, one iteration's loads ahead of the products
 // (v_mfma_i32_16x16x64_i8: four lanes share a column's 64 bytes).  The
 // wavefronts' sums meet in LDS as integers: any order gives the same bits.
@@ -17,11 +18,11 @@
 
 namespace gemmf32 {
 
-template <class X, int WAVES_, int NB_>
+template <class X, int KW_, int CW_, int NB_>
 struct Int8FewTile {
     using E = X;
-    static constexpr int WAVES = WAVES_, THREADS = WAVES * 64, NB = NB_;
-    static constexpr int BM = 16, BN = 16 * NB, KI = 256;       // k of an iteration
+    static constexpr int KW = KW_, CW = CW_, WAVES = KW * CW, THREADS = WAVES * 64, NB = NB_;
+    static constexpr int BM = 16, WN = 16 * NB, BN = WN * CW, KI = 256;       // k of an iteration
 };
 
 template <class T>
@@ -87,7 +88,7 @@ __global__ __launch_bounds__(T::THREADS) void int8_few_kernel(GroupedArgs g)
 {
     using E = typename T::E;
     constexpr int BM = T::BM, BN = T::BN, ROW = BN + 4;
-    __shared__ int red[T::WAVES][BM * ROW];
+    __shared__ int red[T::KW][BM * ROW];
     __shared__ float row_scales[BM];
     __shared__ unsigned tops[T::WAVES][4];
     extern __shared__ i32x4 codes_lds[];
@@ -100,6 +101,7 @@ __global__ __launch_bounds__(T::THREADS) void int8_few_kernel(GroupedArgs g)
     const int col0 = tn * BN;
     const int l16 = lane & 15, grp = lane >> 4;
     const int rows = min(rt.rows, BM);
+    const int kw = wave % T::KW, strip = wave / T::KW * T::WN;       // the wavefront's part of k, and of the columns
     // What the thread's first result is scaled by, loaded ahead of all else.
     const float *const sa = reinterpret_cast<const float *>(g.a_scales) + rt.row;
     const float *const sb = reinterpret_cast<const float *>(g.b_scales) + (long long)max(rt.expert, 0) * g.n + col0;
@@ -117,7 +119,7 @@ __global__ __launch_bounds__(T::THREADS) void int8_few_kernel(GroupedArgs g)
         const char *const bx = g.B + rt.expert * g.expert_stride + grp * 16;
         const char *pb[T::NB];
 #pragma unroll
-        for (int nb = 0; nb < T::NB; ++nb) pb[nb] = bx + min(col0 + nb * 16 + l16, g.n - 1) * g.ldb;
+        for (int nb = 0; nb < T::NB; ++nb) pb[nb] = bx + min(col0 + strip + nb * 16 + l16, g.n - 1) * g.ldb;
         const int held = (int)g.ldb - grp * 16;               // bytes of B's rows from this lane's first on
         const int kp = g.a_kblocks * 128;                     // of A's rows
         auto load_a = [&](int it, Int8FewRegs<T> &r) {
@@ -146,36 +148,36 @@ __global__ __launch_bounds__(T::THREADS) void int8_few_kernel(GroupedArgs g)
         };
         const int its = (g.k + T::KI - 1) / T::KI;
         Int8FewRegs<T> r[2];
-        if (wave < its) load(wave, r[0]);
+        if (kw < its) load(kw, r[0]);
         if constexpr (QUANTISE) {
-            if (wave + T::WAVES < its) load(wave + T::WAVES, r[1]);
+            if (kw + T::KW < its) load(kw + T::KW, r[1]);
             int8_few_quantise<T>(g, rt.row, rows, codes, row_scales, tops);
         }
-        int it = wave;
+        int it = kw;
         while (it < its) {
-            if (it + T::WAVES < its && !(QUANTISE && it == wave)) load(it + T::WAVES, r[1]);
+            if (it + T::KW < its && !(QUANTISE && it == kw)) load(it + T::KW, r[1]);
             if constexpr (QUANTISE) load_a(it, r[0]);
             multiply(r[0]);
-            it += T::WAVES;
+            it += T::KW;
             if (it >= its) continue;
-            if (it + T::WAVES < its) load(it + T::WAVES, r[0]);
+            if (it + T::KW < its) load(it + T::KW, r[0]);
             if constexpr (QUANTISE) load_a(it, r[1]);
             multiply(r[1]);
-            it += T::WAVES;
+            it += T::KW;
         }
     }
     // Lane (l16, grp) holds row l16 and columns 4 grp + v of each block.
 #pragma unroll
     for (int nb = 0; nb < T::NB; ++nb)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) red[wave][l16 * ROW + nb * 16 + 4 * grp + v] = acc[nb][v];
+        for (int v = 0; v < 4; ++v) red[kw][l16 * ROW + strip + nb * 16 + 4 * grp + v] = acc[nb][v];
     __syncthreads();
     for (int e = tid; e < rows * BN; e += T::THREADS) {
         const int row = e / BN, col = e % BN;
         if (col0 + col >= g.n) continue;
         int sum = 0;
 #pragma unroll
-        for (int w = 0; w < T::WAVES; ++w) sum += red[w][row * ROW + col];
+        for (int w = 0; w < T::KW; ++w) sum += red[w][row * ROW + col];
         float x = 0.0f;
         if (rt.expert >= 0) {
             const bool first = e == tid;

@@ -154,7 +154,8 @@ def offsets_of(sizes):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("sizes,n,k", [
     ([2, 0, 1, 0], 70, 40), ([0, 0, 3], 33, 130), ([16, 17, 15, 1, 0, 31], 200, 260), ([100, 0, 1, 37, 64, 65], 300, 200),
-    ([300, 260, 0, 250, 1], 600, 384), ([129] * 20, 513, 100), ([700, 400, 600], 4100, 260), ([900, 1101, 0, 700, 1], 8200, 260), ([0] * 70 + [5] + [0] * 9, 48, 33)])
+    ([300, 260, 0, 250, 1], 600, 384), ([129] * 20, 513, 100), ([700, 400, 600], 4100, 260), ([900, 1101, 0, 700, 1], 8200, 260), ([0] * 70 + [5] + [0] * 9, 48, 33),
+    ([0] * 30 + [41] + [0] * 20 + [1], 100, 700), ([1, 2, 2, 3], 4500, 1500), ([8, 9, 1, 16] * 15, 600, 300)])
 def test_linear_by_expert(sizes, n, k, dtype):
     m = sum(sizes)
     x, w, off = normal((m, k), dtype, m), weights(len(sizes), n, k, n), offsets_of(sizes)

@@ -49,7 +49,8 @@ def off(got, want):
 
 SHAPES = [(1, 1), (1, 5), (7, 1), (2, 3), (16, 16), (31, 65), (64, 64), (65, 64), (64, 192), (100, 333), (129, 127), (200, 1000),
           (1000, 70), (64, 128), (40, 250), (64, 384), (300, 64), (64, 385), (450, 33), (50, 1024), (1100, 64), (64, 2050), (20, 4200),
-          (5000, 64), (256, 256), (320, 640), (513, 300), (700, 1100), (1300, 520)]
+          (5000, 64), (65, 66), (128, 64), (90, 128), (128, 128), (129, 130), (100, 400), (512, 128), (128, 513), (70, 1024), (1024, 127),
+          (128, 1025), (256, 256), (320, 640), (513, 300), (700, 1100), (1300, 520)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -77,7 +78,7 @@ def test_large(batch, rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("batch,rows,cols", [(0, 8, 8), (1, 20, 30), (5, 64, 96), (33, 70, 40), (6, 64, 500), (3, 300, 200), (9, 260, 513), (70, 256, 256)])
+@pytest.mark.parametrize("batch,rows,cols", [(0, 8, 8), (1, 20, 30), (5, 64, 96), (33, 70, 40), (6, 64, 500), (40, 120, 100), (5, 100, 700), (3, 300, 200), (9, 260, 513), (70, 256, 256)])
 def test_stacks(batch, rows, cols, dtype):
     x = normal((batch, rows, cols), dtype, batch) * torch.exp(3 * normal((batch, 1, 1), torch.float32, 1)).to(dtype)
     got = g.orthogonalize(x, scale=0.5)
@@ -157,15 +158,15 @@ def test_strides_out_and_in_place(rows, cols, dtype):
     assert torch.equal(g.orthogonalize(one), want[:1].expand(4, rows, cols))
 
 
-@pytest.mark.parametrize("rows,cols", [(70, 200), (30, 100), (60, 900)])
+@pytest.mark.parametrize("rows,cols", [(70, 200), (30, 100), (60, 900), (128, 1000), (200, 300)])
 def test_turned_matrices_agree(rows, cols):
     x = normal((rows, cols), torch.float32, 9)
     assert off(g.orthogonalize(x.t().contiguous()).t(), definition(x)) <= 1e-5
 
 
-@pytest.mark.parametrize("cols", [60, 350, 800])
-def test_few_rows_zeros_magnitudes_and_strides(cols):
-    x = normal((5, 40, cols), torch.float32, 6)
+@pytest.mark.parametrize("rows,cols", [(40, 60), (40, 350), (40, 800), (100, 100), (100, 800)])
+def test_few_rows_zeros_magnitudes_and_strides(rows, cols):
+    x = normal((5, rows, cols), torch.float32, 6)
     x[1] = 0
     x[2, 3, 4] = float("inf")
     x[3] *= 1e-30
@@ -174,13 +175,13 @@ def test_few_rows_zeros_magnitudes_and_strides(cols):
     assert (got[1] == 0).all() and got[2].isnan().any()
     for i in (0, 3, 4):
         assert off(got[i], definition(x[i])) <= 1e-5
-    full = normal((3, 42, cols + 5), torch.bfloat16, 8)
-    part = full[:, 1:41, 3:3 + cols]
+    full = normal((3, rows + 2, cols + 5), torch.bfloat16, 8)
+    part = full[:, 1:1 + rows, 3:3 + cols]
     want = g.orthogonalize(part.contiguous())
     before = full.clone()
     g.orthogonalize(part, out=part)
     assert torch.equal(part, want)
-    full[:, 1:41, 3:3 + cols] = before[:, 1:41, 3:3 + cols]
+    full[:, 1:1 + rows, 3:3 + cols] = before[:, 1:1 + rows, 3:3 + cols]
     assert torch.equal(full, before)
     for steps in (1, 2, 3, 6):
         assert off(g.orthogonalize(x[0], steps=steps), definition(x[0], steps)) <= 1e-5
@@ -209,7 +210,7 @@ def test_refusals():
         g.orthogonalize(x.expand(2, 8, 8), out=torch.empty((8, 8), device="cuda").expand(2, 8, 8))
 
 
-@pytest.mark.parametrize("rows,cols", [(96, 200), (40, 100), (600, 50)])
+@pytest.mark.parametrize("rows,cols", [(96, 200), (40, 100), (600, 50), (200, 300), (100, 90)])
 def test_captured_replayed_and_on_two_streams(rows, cols):
     x = normal((2, rows, cols), torch.float32, 3)
     want = g.orthogonalize(x)
