@@ -30,8 +30,8 @@ QUANT = dict(dtype=0, rows=8, k=32, X=OK, layout=0, ld=32, codes=OK, scales=OK, 
 DEQUANT = dict(dtype=0, rows=8, k=32, codes=OK, scales=OK, X=OK, ld=32, stream=None)
 LINEAR = dict(dtype=0, m=80, n=16, k=32, groups=2, X=OK, ldx=32, codes=OK, scales=OK, offsets=OK, bias=None, act=0, Y=OK, ldy=16,
               work=OK, work_bytes=1 << 20, stream=None)
-ORTHO = dict(dtype=0, batch=2, rows=80, cols=100, X=OK, ldx=100, stride_x=8000, steps=5, f=ctypes.addressof(COEFFICIENTS),
-             scale=1.0, Y=OK, ldy=100, stride_y=8000, work=OK, work_bytes=1 << 31, stream=None)
+ORTHO = dict(dtype=0, batch=2, rows=180, cols=200, X=OK, ldx=200, stride_x=36000, steps=5, f=ctypes.addressof(COEFFICIENTS),
+             scale=1.0, Y=OK, ldy=200, stride_y=36000, work=OK, work_bytes=1 << 31, stream=None)
 
 REFUSALS = [
     ("expert_route_balanced", BALANCE, [
@@ -56,8 +56,8 @@ REFUSALS = [
         dict(scales=None), dict(X=None), dict(Y=None), dict(work=None), dict(work=OK + 4), dict(bias=OK + 2), dict(ldx=1 << 21),
         dict(m=1 << 29, groups=1000)]),
     ("expert_orthogonalize", ORTHO, [
-        dict(dtype=2), dict(batch=-1), dict(rows=0), dict(cols=0), dict(ldx=99), dict(ldy=99), dict(stride_x=-1),
-        dict(stride_y=7999), dict(steps=0), dict(steps=65), dict(f=None), dict(scale=INF), dict(scale=NAN), dict(X=None),
+        dict(dtype=2), dict(batch=-1), dict(rows=0), dict(cols=0), dict(ldx=199), dict(ldy=199), dict(stride_x=-1),
+        dict(stride_y=35999), dict(steps=0), dict(steps=65), dict(f=None), dict(scale=INF), dict(scale=NAN), dict(X=None),
         dict(Y=None), dict(X=OK + 2), dict(work=None), dict(work=OK + 8), dict(cols=1 << 22, ldx=1 << 22, ldy=1 << 22),
         dict(ldx=1 << 21)]),
 ]
@@ -85,9 +85,9 @@ def test_workspaces():
     assert f["expert_int8_workspace"](80, 130) == 80 * (256 + 4) and f["expert_int8_workspace"](0, 130) == 0
     assert f["expert_int8_linear"](*{**LINEAR, "work_bytes": 80 * 132 - 1}.values()) == SMALL
     space = f["expert_orthogonalize_workspace"]
-    assert space(0, 5, 64, 256) == 0                       # one strip of columns: none
+    assert space(0, 5, 64, 256) == 0 and space(1, 5, 100, 128) == 0       # one strip of columns: none
     assert space(0, 5, 300, 60) > 0 and space(0, 0, 300, 300) == 0 and space(3, 1, 300, 300) == 0
-    need = space(0, 2, 80, 100)
+    need = space(0, 2, 180, 200)
     assert f["expert_orthogonalize"](*{**ORTHO, "work_bytes": need - 1}.values()) == SMALL
     # A stack's matrices are worked on as many at a time as 2 GiB hold.
     assert space(1, 1000, 2048, 4096) < (5 << 29) and space(1, 1000, 2048, 4096) == space(1, 2000, 2048, 4096)
