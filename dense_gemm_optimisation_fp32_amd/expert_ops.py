@@ -26,6 +26,7 @@ the calls below.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 import torch
 
@@ -328,9 +329,12 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
     if isinstance(x, torch.Tensor) and x.dim() in (2, 3) and x.stride(-1) != 1 and x.shape[-1] > 1 and x.stride(-2) == 1:
         turned = orthogonalize(x.transpose(-1, -2), steps, coefficients, scale, None if out is None else out.transpose(-1, -2))
         return turned.transpose(-1, -2) if out is None else out
+    steps = operator.index(steps)
+    if not 1 <= steps <= 64:
+        raise ValueError("steps must be from 1 to 64")
     flat = tuple(coefficients)
     if flat and not isinstance(flat[0], (int, float)):
         flat = tuple(v for step in flat for v in step)
-    elif len(flat) == 3 and isinstance(steps, int):
+    elif len(flat) == 3:
         flat = flat * steps
     return _checked((_module or _binding()).orthogonalize(x, steps, flat, scale, out, _stream(x, "x")), "expert_orthogonalize")

@@ -251,3 +251,38 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             assert torch.equal(a.order, b.order) and torch.equal(a.weights, b.weights)
+
+
+def test_refusals():
+    x = normal(5, 12, torch.float32, 1)
+    for bad in (dict(sets=5), dict(sets=0), dict(sets=3, kept_sets=4), dict(sets=3, kept_sets=0), dict(scale=0.0),
+                dict(scale=float("nan")), dict(bias=torch.zeros(11, device="cuda")), dict(bias=torch.zeros(12)),
+                dict(bias=torch.zeros(12, device="cuda").double()), dict(bias=torch.zeros(24, device="cuda")[::2])):
+        with pytest.raises(ValueError):
+            g.route_balanced(x, 2, **bad)
+    for choices in (0, 13):
+        with pytest.raises(ValueError):
+            g.route_balanced(x, choices)
+    with pytest.raises(ValueError):
+        g.route_balanced(x, 5, sets=3, kept_sets=1)           # four experts are left
+    with pytest.raises(g.GemmF32Error):
+        g.route_balanced(normal(5, 64, torch.float32, 1), 33)
+    with pytest.raises(ValueError):
+        g.route_balanced(x.t(), 2)
+    r = g.route_balanced(x, 2)
+    for grad in (torch.zeros((5, 3), device="cuda"), torch.zeros((5, 2)), torch.zeros((5, 2), device="cuda").double()):
+        with pytest.raises(ValueError):
+            g.route_balanced_grad(x, r, grad)
+    with pytest.raises(ValueError):
+        g.route_balanced_grad(x[:4], r, torch.zeros((5, 2), device="cuda"))
+
+
+def test_experts_outside_the_range_are_left_out():
+    """A gradient of experts that there are not (a list that the caller changed) stays inside."""
+    x = normal(40, 12, torch.float32, 1)
+    r = g.route_balanced(x, 3)
+    r.experts[::2, 1] = 12
+    r.experts[1::2, 0] = -7
+    wide = torch.full((42, 12), 3.0, device="cuda")
+    wide[1:41] = g.route_balanced_grad(x, r, torch.ones((40, 3), device="cuda"))
+    assert wide.isfinite().all() and (wide[0] == 3).all() and (wide[41] == 3).all()

@@ -235,3 +235,39 @@ def test_same_bits_each_time_on_two_streams_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(held, g.int8_linear(x, w, activation="gelu")) and torch.equal(few, g.int8_linear(x[:3], w))
+
+
+def test_refusals():
+    x, w = normal((6, 40), torch.float32, 1), weights(0, 5, 40, 1)
+    many, off = weights(3, 5, 40, 1), offsets_of([2, 2, 2])
+    for bad in (dict(w=weights(0, 5, 41, 1)), dict(w=many), dict(offsets=off), dict(w=many, offsets=off[:3]),
+                dict(w=many, offsets=off.long()), dict(bias=torch.zeros(4, device="cuda")), dict(bias=torch.zeros(5)),
+                dict(out=torch.empty((6, 6), device="cuda")), dict(out=torch.empty((6, 5), device="cuda").bfloat16()),
+                dict(w=g.Int8Tensor(w.codes.cpu(), w.scales.cpu(), 40))):
+        with pytest.raises(ValueError):
+            g.int8_linear(**{"x": x, "w": w, **bad})
+    with pytest.raises(TypeError):
+        g.int8_linear(x.half(), w)
+    with pytest.raises(ValueError):
+        g.int8_linear(x[:, ::2], weights(0, 5, 20, 1))
+    with pytest.raises(ValueError):
+        g.int8_quantize(normal((4, 6, 8), torch.float32, 1))
+    with pytest.raises(ValueError):
+        g.int8_quantize(normal((8, 16), torch.float32, 1)[::2, ::2])
+    with pytest.raises(ValueError):
+        g.int8_dequantize(many)
+    # Codes that do not begin at 16 bytes: refused by the library.
+    base = torch.zeros(5 * 48 + 4, dtype=torch.int8, device="cuda")
+    with pytest.raises(g.GemmF32Error):
+        g.int8_linear(x, g.Int8Tensor(base[4:].view(5, 48), torch.ones(5, device="cuda"), 40))
+
+
+@pytest.mark.parametrize("offset", [1, 2, 3])
+def test_rows_at_any_address(offset):
+    """x and the result at addresses of their type's alignment, rows of odd length."""
+    base = normal((70 * 333 + 8,), torch.bfloat16, 3)
+    x = base[offset:offset + 70 * 333].view(70, 333)
+    out = torch.empty(70 * 77 + 8, dtype=torch.bfloat16, device="cuda")[offset:offset + 70 * 77].view(70, 77)
+    check_product(x, weights(0, 77, 333, 4), out=out)
+    check_product(x[:3], weights(0, 77, 333, 5), out=out[:3])
+    check_codes(x)

@@ -117,8 +117,10 @@ def test_magnitudes_of_any_size():
     assert off(g.orthogonalize((x * 1e-41)), definition(x * 1e-41)) <= 1e-5
 
 
-def test_zeros_and_values_that_are_not_finite():
-    x = normal((4, 70, 90), torch.float32, 6)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols", [(70, 90), (170, 200), (300, 150)])
+def test_zeros_and_values_that_are_not_finite(rows, cols, dtype):
+    x = normal((4, rows, cols), dtype, 6)
     x[1] = 0
     x[2, 3, 4] = float("inf")
     x[3, 69, 89] = float("nan")
@@ -187,6 +189,28 @@ def test_few_rows_zeros_magnitudes_and_strides(rows, cols):
         assert off(g.orthogonalize(x[0], steps=steps), definition(x[0], steps)) <= 1e-5
 
 
+@pytest.mark.parametrize("batch,rows,cols", [(40, 2048, 2048), (1400, 64, 4096)])
+def test_stacks_that_are_worked_on_in_parts(batch, rows, cols):
+    """More matrices than 2 GiB of workspace hold: two rounds, also in place."""
+    x = normal((batch, rows, cols), torch.float32, 1)
+    got = g.orthogonalize(x)
+    for i in (0, batch * 3 // 4, batch * 4 // 5, batch - 1):
+        assert off(got[i], definition(x[i])) <= 1e-5, i
+    g.orthogonalize(x, out=x)
+    assert torch.equal(x, got)
+
+
+@pytest.mark.parametrize("rows,cols", [(100, 100), (300, 200)])
+def test_bfloat16_magnitudes(rows, cols):
+    x = normal((rows, cols), torch.bfloat16, 2)
+    want = g.orthogonalize(x)
+    # A power of two gives the same bits, where it is exact: entries of 2^-13 and more times
+    # 2^-120 would be subnormal, with fewer bits.
+    for power in (-100, -40, 60, 100):
+        assert torch.equal(x * 2.0 ** power * 2.0 ** -power, x)
+        assert torch.equal(g.orthogonalize(x * 2.0 ** power), want)
+
+
 def test_refusals():
     x = normal((8, 8), torch.float32, 1)
     for f in ((40.0, 0.0, 0.0), (float("nan"), 0.0, 0.0), (3.0, float("inf"), 0.0), (8.0, 0.0, 0.0)):
@@ -196,6 +220,10 @@ def test_refusals():
         g.orthogonalize(x, steps=0)
     with pytest.raises(ValueError):
         g.orthogonalize(x, steps=65)
+    with pytest.raises(ValueError):
+        g.orthogonalize(x, steps=10 ** 12)
+    with pytest.raises(TypeError):
+        g.orthogonalize(x, steps=2.0)
     with pytest.raises(ValueError):
         g.orthogonalize(x, coefficients=(1.0, 2.0))
     with pytest.raises(ValueError):
