@@ -157,24 +157,20 @@ __device__ __forceinline__ int sets_before(K value, int set, int lanes)
     return n;
 }
 
-// One token's choice: its experts to `mine`.  K: float or double.  x: the lane's
-// logits, `count` of them from expert e0 on.  False: keys or sets whose order
-// decides are nearer than their errors (never for double).
+// The lane's keys.  K: float or double.  x: its logits, `count` of them from
+// expert e0 on; top: the token's largest (softmax).  Returns twice the error that a
+// 32-bit score may have.
 //
 // Errors of 32-bit keys.  sigmoid: e = 2^(-x log2 e) is off by (1.5 |x| + 2)
 // 2^-24 of itself, the sum and the reciprocal add 1.5 2^-23: the score's error is
 // below 2^-21 (|x| s (1 - s) stays below 0.3).  softmax: e^(x - top) as much, the sum of
 // up to 32 of them a lane and of 6 lane by lane 38 2^-24 more: below 2^-18 of the
 // score, which is at most 1 / sum.  The bias adds a rounding, 2^-24 of the key.
-// Twice that for two keys, four times for two sets of two.
 template <class K, int LANES, int V>
-__device__ __forceinline__ bool balance_pick(const BalanceArgs &b, const float (&x)[V], float top, int sub, int group, int set,
-                                             int e0, int count, int *mine)
+__device__ __forceinline__ float balance_keys(const BalanceArgs &b, const float (&x)[V], float top, int e0, int count, K (&c)[V])
 {
     constexpr bool kWide = sizeof(K) == 8;
-    const K none = -__builtin_inff();
-    K c[V];
-    float near = 0x1p-20f;                                // twice a score's error
+    float near = 0x1p-20f;
     if (b.softmax) {
         K sum = 0;
 #pragma unroll
@@ -206,31 +202,182 @@ __device__ __forceinline__ bool balance_pick(const BalanceArgs &b, const float (
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         if (b.bias) c[i] += (K)(i < count ? b.bias[eb + i] : 0.0f);
-        c[i] = x[i] > -__builtin_inff() && c[i] == c[i] ? c[i] : none;
+        c[i] = x[i] > -__builtin_inff() && c[i] == c[i] ? c[i] : (K)-__builtin_inff();
     }
+    return near;
+}
+
+// How many sets of the token come before this lane's, whose two largest keys are
+// `two`, joined over its lanes.
+template <class K, int LANES>
+__device__ __forceinline__ int balance_sets(const BalanceArgs &b, Two<K> &two, int set, K &value)
+{
+    const K none = -__builtin_inff();
+    if (b.lanes > 1) two.template join<1>();
+    if (b.lanes > 2) two.template join<2>();
+    if (b.lanes > 4) two.template join<4>();
+    if (b.lanes > 8) two.template join<8>();
+    if constexpr (LANES == 64) {
+        if (b.lanes > 16) two.template join<16>();
+        if (b.lanes > 32) two.template join<32>();
+    }
+    value = two.second > none ? two.first + two.second : two.first;
+    if constexpr (LANES == 16) return sets_before<1>(value, set, b.lanes);
+    int before = 0;
+    for (int u = 0; u < b.sets; ++u) {
+        const K v = __shfl(value, u * b.lanes);
+        before += v > value || (v == value && u < set) ? 1 : 0;
+    }
+    return before;
+}
+
+// The lane of the token's that holds its largest, among those with `hit`.
+template <int LANES>
+__device__ __forceinline__ int first_lane(bool hit, int group)
+{
+    const unsigned long long lanes = __ballot(hit);
+    if constexpr (LANES == 16) return __builtin_ctz((unsigned)(lanes >> (16 * group)) & 0xffffu);
+    else return __builtin_ctzll(lanes);
+}
+
+template <int LANES>
+__device__ __forceinline__ int lanes_max_int(int x)
+{
+    x = max(x, (int)mx_lane<0xb1>((unsigned)x));
+    x = max(x, (int)mx_lane<0x4e>((unsigned)x));
+    x = max(x, (int)mx_lane<0x141>((unsigned)x));
+    x = max(x, (int)mx_lane<0x140>((unsigned)x));
+    if constexpr (LANES == 64) {
+        x = max(x, __shfl_xor(x, 16));
+        x = max(x, __shfl_xor(x, 32));
+    }
+    return x;
+}
+
+__device__ __forceinline__ void order(int &a, int &b)
+{
+    const int most = max(a, b);
+    b = min(a, b);
+    a = most;
+}
+
+// Eight in falling order: nineteen comparisons, and twelve of two sorted runs,
+// the second turned round.
+__device__ __forceinline__ void sort8(int *p)
+{
+    order(p[0], p[2]), order(p[1], p[3]), order(p[4], p[6]), order(p[5], p[7]);
+    order(p[0], p[4]), order(p[1], p[5]), order(p[2], p[6]), order(p[3], p[7]);
+    order(p[0], p[1]), order(p[2], p[3]), order(p[4], p[5]), order(p[6], p[7]);
+    order(p[2], p[4]), order(p[3], p[5]), order(p[1], p[4]), order(p[3], p[6]);
+    order(p[1], p[2]), order(p[3], p[4]), order(p[5], p[6]);
+}
+
+__device__ __forceinline__ void merge8(int *p)
+{
+    order(p[0], p[4]), order(p[1], p[5]), order(p[2], p[6]), order(p[3], p[7]);
+    order(p[0], p[2]), order(p[1], p[3]), order(p[4], p[6]), order(p[5], p[7]);
+    order(p[0], p[1]), order(p[2], p[3]), order(p[4], p[5]), order(p[6], p[7]);
+}
+
+// A key and its place in the lane as one number in the keys' order: the key's bits
+// but the last four (2^-19 of it), and 15 - i.
+constexpr int kNoKey = (int)0x80000000, kLeastKey = (int)0x80800000;
+
+__device__ __forceinline__ int packed_key(float c, int i)
+{
+    const int u = __float_as_int(c);
+    return c > -__builtin_inff() ? ((u ^ (u >> 31 & 0x7fffffff)) & ~15) | (15 - i) : kNoKey;
+}
+
+__device__ __forceinline__ float unpacked_key(int p)
+{
+    const int s = p & ~15;
+    return p < kLeastKey ? -__builtin_inff() : __int_as_float(s ^ (s >> 31 & 0x7fffffff));
+}
+
+// One token's choice, its experts to `mine`, for up to eight choices or up to eight
+// experts a lane: every lane sorts its keys once (minima and maxima of integers, no
+// comparison waits for another lane) and keeps the eight largest and the ninth, and
+// a choice takes the largest of the lanes' first.  False: keys or sets whose order
+// decides are nearer than their errors.
+template <int LANES, int V>
+__device__ __forceinline__ bool balance_pick_packed(const BalanceArgs &b, const float (&x)[V], float top, int sub, int group,
+                                                    int set, int e0, int count, int *mine)
+{
+    static_assert(V <= 16, "places of four bits");
+    constexpr int KEPT = V < 8 ? V : 8;
+    int q[KEPT + 1];
+    float near;
+    {
+        float c[V];
+        near = balance_keys<float, LANES, V>(b, x, top, e0, count, c);
+        int p[V < 8 ? 8 : V];
+#pragma unroll
+        for (int i = 0; i < (V < 8 ? 8 : V); ++i) p[i] = i < V ? packed_key(c[i < V ? i : 0], i) : kNoKey;
+        sort8(p);
+        q[KEPT] = kNoKey;
+        if constexpr (V == 16) {
+            sort8(p + 8);
+            int rest = kNoKey;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) rest = max(rest, min(p[i], p[15 - i]));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = max(p[i], p[15 - i]);
+            merge8(p);
+            q[KEPT] = rest;
+        }
+#pragma unroll
+        for (int i = 0; i < KEPT; ++i) q[i] = p[i];
+    }
+    bool sure = true;
+    const float none = -__builtin_inff();
+    if (b.kept < b.sets) {
+        Two<float> two{unpacked_key(q[0]), unpacked_key(q[1])};
+        float value;
+        const int before = balance_sets<float, LANES>(b, two, set, value);
+        const bool out = before >= b.kept;
+        const float least = -lanes_max<LANES>(out ? none : -value), most = lanes_max<LANES>(out ? value : none);
+        const float size = lanes_max<LANES>(fabsf(two.first > none ? two.first : 0.0f) + fabsf(two.second > none ? two.second : 0.0f));
+        sure = most == none || least - most > 2.0f * near + 0x1p-17f * size;
+        if (out)
+#pragma unroll
+            for (int i = 0; i <= KEPT; ++i) q[i] = kNoKey;
+    }
+    float last = none;
+    for (int j = 0;; ++j) {
+        const int m = lanes_max_int<LANES>(q[0]);
+        const bool used = m >= kLeastKey;
+        const float key = unpacked_key(m);
+        if (j > 0) sure = sure && (!used || last - key > near + 0x1p-18f * (fabsf(last) + fabsf(key)));
+        last = key;
+        if (j == b.route.choices) break;
+        if (sub == first_lane<LANES>(q[0] == m, group)) {
+            mine[j] = used ? e0 + 15 - (m & 15) : -1;
+#pragma unroll
+            for (int i = 0; i < KEPT; ++i) q[i] = q[i + 1];
+            q[KEPT] = kNoKey;
+        }
+    }
+    return sure;
+}
+
+// The same for any number of choices, key by key.  K: float or double, which is
+// always sure.
+template <class K, int LANES, int V>
+__device__ __forceinline__ bool balance_pick(const BalanceArgs &b, const float (&x)[V], float top, int sub, int group, int set,
+                                             int e0, int count, int *mine)
+{
+    constexpr bool kWide = sizeof(K) == 8;
+    const K none = -__builtin_inff();
+    K c[V];
+    const float near = balance_keys<K, LANES, V>(b, x, top, e0, count, c);
     bool sure = true;
     if (b.kept < b.sets) {
         Two<K> two{none, none};
 #pragma unroll
         for (int i = 0; i < V; ++i) two.add(c[i]);
-        if (b.lanes > 1) two.template join<1>();
-        if (b.lanes > 2) two.template join<2>();
-        if (b.lanes > 4) two.template join<4>();
-        if (b.lanes > 8) two.template join<8>();
-        if constexpr (LANES == 64) {
-            if (b.lanes > 16) two.template join<16>();
-            if (b.lanes > 32) two.template join<32>();
-        }
-        const K value = two.second > none ? two.first + two.second : two.first;
-        int before = 0;
-        if constexpr (LANES == 16) {
-            before = sets_before<1>(value, set, b.lanes);
-        } else {
-            for (int u = 0; u < b.sets; ++u) {
-                const K v = __shfl(value, u * b.lanes);
-                before += v > value || (v == value && u < set) ? 1 : 0;
-            }
-        }
+        K value;
+        const int before = balance_sets<K, LANES>(b, two, set, value);
         const bool out = before >= b.kept;
         if constexpr (!kWide) {
             const float least = -lanes_max<LANES>(out ? none : -value), most = lanes_max<LANES>(out ? value : none);
@@ -257,11 +404,7 @@ __device__ __forceinline__ bool balance_pick(const BalanceArgs &b, const float (
             last = m;
         }
         if (j == b.route.choices) break;
-        const unsigned long long hit = __ballot(best == m);
-        int who;
-        if constexpr (LANES == 16) who = __builtin_ctz((unsigned)(hit >> (16 * group)) & 0xffffu);
-        else who = __builtin_ctzll(hit);
-        if (sub == who) {
+        if (sub == first_lane<LANES>(best == m, group)) {
             mine[j] = used ? e0 + at : -1;
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -311,7 +454,10 @@ __device__ __forceinline__ void balance_choose(const BalanceArgs &b, int first, 
             top = lanes_max<LANES>(top);
             top = top > -__builtin_inff() ? top : 0.0f;
         }
-        const bool sure = balance_pick<float, LANES, V>(b, x, top, sub, group, set, e0, count, mine);
+        bool sure;
+        if constexpr (V > 16) sure = balance_pick<float, LANES, V>(b, x, top, sub, group, set, e0, count, mine);
+        else if (V <= 8 || a.choices <= 8) sure = balance_pick_packed<LANES, V>(b, x, top, sub, group, set, e0, count, mine);
+        else sure = balance_pick<float, LANES, V>(b, x, top, sub, group, set, e0, count, mine);
         if (__ballot(!sure)) balance_pick<double, LANES, V>(b, x, top, sub, group, set, e0, count, mine);
         double sum = 1.0;
         if (b.softmax && !a.normalize) {

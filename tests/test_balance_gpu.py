@@ -151,6 +151,20 @@ def test_ties_go_to_the_lowest(sets, kept):
     check(logits, 6, torch.zeros(48, device="cuda"), "softmax", sets, kept)
 
 
+@pytest.mark.parametrize("groups", [16, 64, 120, 256, 384, 1024])
+@pytest.mark.parametrize("choices", [1, 7, 8, 9, 16])
+def test_neighbours_hold_all_choices(groups, choices):
+    """Every choice from neighbouring experts, from either end, and keys of both signs."""
+    up = torch.linspace(-3.0, 3.0, groups).repeat(6, 1)
+    up[1] = up[1].flip(0)
+    up[2, : groups // 2] = up[2, : groups // 2].flip(0)
+    up[3:] = up[3:].roll(groups // 3, 1)
+    bias = torch.full((groups,), -0.5)
+    for kind in ("sigmoid", "softmax"):
+        for dtype in (torch.float32, torch.bfloat16):       # (in 16 bits many are equal)
+            check(up.to(dtype).cuda(), choices, bias.cuda(), kind)
+
+
 def test_choice_goes_by_64_bits():
     """Keys that 32 bits cannot tell apart: sigmoids of neighbouring 32-bit logits
     near 9, a bias that all but makes up for their difference."""
