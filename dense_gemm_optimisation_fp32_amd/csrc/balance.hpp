@@ -26,6 +26,13 @@
 // (`lanes`), each `each` neighbouring experts, so that a set's two largest are
 // found by exchanges between its own lanes whatever its size; the lanes hold
 // the experts in order.
+//
+// What bounds it is the vector unit, not memory.  One MI355X, 32768 tokens of 256
+// bfloat16 logits, 8 choices from 4 of 8 sets: 37.5 us to choose (vector
+// instructions in 62 % of the issue slots; its bytes would take 4), 11.4 to place.
+// With keys compared lane by lane at every choice, instead of sorted ones, choosing
+// took 42.3.  5003 tokens of 60 32-bit logits, 6 choices: 13.3 and 4.7; 16 tokens of
+// 64, chosen and placed in one launch: 6.4, the launch and one chain of latencies.
 #pragma once
 
 #include "route.hpp"
@@ -541,7 +548,8 @@ __device__ __host__ constexpr int balance_grad_row(int groups) { return (groups 
 
 // A token's gradient is put together in LDS: what every expert has
 // (0, or softmax's share), then the chosen ones' on top, a lane a slot; then it is
-// stored 16 bytes a lane.
+// stored 16 bytes a lane.  Bound by memory: 32768 tokens of 256 bfloat16 logits, 8
+// choices: 6.8 us, 5 TB/s read and written.
 template <class E>
 __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(BalanceArgs b)
 {

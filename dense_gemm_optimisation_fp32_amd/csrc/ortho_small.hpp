@@ -10,6 +10,10 @@
 // share of the next X X^T.
 //
 // Products run on hi hi + hi lo + lo hi in both types: three times little.
+//
+// One MI355X: four matrices of 64 x 192, five steps, one launch of 25.6 us, 4 of them a step
+// and barrier after barrier (fifteen products of few instructions that wait for each
+// other through LDS); as tiles, 17 launches, 82.
 // LDS: row r of a block, 16-byte chunk c at [r][c ^ (r / 2) % 8], as the tiles have
 // it; X is read along its columns (X X^T) as it is, along its rows (B X) by the
 // transposing read.

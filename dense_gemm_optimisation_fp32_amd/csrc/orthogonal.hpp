@@ -11,8 +11,9 @@
 // are 1 to 30 % off, in half precision 0.2 to 4 % (the more, the faster the
 // singular values fall).  Every matrix is therefore held as two half-precision
 // planes, v * 2^11 = hi + lo: 22 bits, and products run on the matrix cores as
-// hi hi + hi lo + lo hi, accumulated in 32 bits (v_mfma_f32_32x32x16_f16, three
-// times the work of one plane, yet 5 times the rate of 32-bit products).  The
+// hi hi + hi lo + lo hi, accumulated in 32 bits (v_mfma_f32_32x32x16_f16: three
+// times the work of one plane, and still 2.5 times the rate of 32-bit instructions:
+// large products reach 1139 TFLOPS in half precision, 153 in 32 bits).  The
 // factor 2^11 keeps lo above the subnormals; entries stay below 2^15.9 / 2^11 = 31,
 // which the host derives from the coefficients.
 // bfloat16 results are rounded to 2^-9 at the end: for them A and B = a I + b A +
@@ -120,6 +121,7 @@ struct OrthoStartArgs {
 };
 
 // Sums of squares, in 64 bits: neither leaves the range for any 32-bit values.
+// Bound by memory from large matrices on: 16 of 2048 x 4096 in bfloat16 64 us, 4.2 TB/s.
 template <class E>
 __global__ __launch_bounds__(256) void ortho_squares_kernel(OrthoStartArgs a)
 {
@@ -166,7 +168,8 @@ struct Planes {
 };
 
 // x / |x| as planes, a block of 64 x 64 a workgroup; with factors x times a power
-// of two, in one.
+// of two, in one.  Bound by memory: 16 of 2048 x 4096 in bfloat16 134 us, 4.0 TB/s read and
+// written.
 template <class E>
 __global__ __launch_bounds__(256) void ortho_start_kernel(OrthoStartArgs a)
 {
@@ -321,7 +324,9 @@ __device__ __forceinline__ void ortho_store(const OrthoArgs &g, const OrthoTile 
 // A workgroup a tile.  E: what C holds, planes (_Float16) or the result's type.
 // K: parts of the workgroup that share the slabs, each with a ring of its own; their
 // sums meet in LDS.  A part of four wavefronts, one a SIMD, waits most of a slab for
-// LDS and its own products.
+// LDS and its own products.  X X^T of 1088 x 5056, 153 tiles of 64 x 64 (one MI355X): 25 us in
+// two parts, 32 in one (0.24 and 0.19 PFLOPS): the ring of a tile alone on its CU runs at the
+// latency of its slabs.
 template <class T, int K, bool A_KS, bool B_KS, class E, bool WIDE>
 __global__ __launch_bounds__(T::THREADS * K) void ortho_kernel(OrthoArgs g)
 {
