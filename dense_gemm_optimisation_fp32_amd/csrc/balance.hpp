@@ -28,10 +28,9 @@
 // the experts in order.
 //
 // What bounds it is the vector unit, not memory.  One MI355X, 32768 tokens of 256
-// bfloat16 logits, 8 choices from 4 of 8 sets: 37.5 us to choose (vector
-// instructions in 62 % of the issue slots; its bytes would take 4), 11.4 to place.
-// With keys compared lane by lane at every choice, instead of sorted ones, choosing
-// took 42.3.  5003 tokens of 60 32-bit logits, 6 choices: 13.3 and 4.7; 16 tokens of
+// bfloat16 logits, 8 choices from 4 of 8 sets: 30 us to choose (its bytes would take
+// 4), 11.4 to place.  With keys compared lane by lane at every choice, instead of sorted
+// ones, choosing took 5 more.  5003 tokens of 60 32-bit logits, 6 choices: 13.3 and 4.7; 16 tokens of
 // 64, chosen and placed in one launch: 6.4, the launch and one chain of latencies.
 #pragma once
 
@@ -164,7 +163,7 @@ __device__ __forceinline__ int sets_before(K value, int set, int lanes)
     return n;
 }
 
-// The lane's keys.  K: float or double.  x: its logits, `count` of them from
+// The lane's keys.  x: its logits, `count` of them from
 // expert e0 on; top: the token's largest (softmax).  Returns twice the error that a
 // 32-bit score may have.
 //
@@ -173,45 +172,76 @@ __device__ __forceinline__ int sets_before(K value, int set, int lanes)
 // below 2^-21 (|x| s (1 - s) stays below 0.3).  softmax: e^(x - top) as much, the sum of
 // up to 32 of them a lane and of 6 lane by lane 38 2^-24 more: below 2^-18 of the
 // score, which is at most 1 / sum.  The bias adds a rounding, 2^-24 of the key.
-template <class K, int LANES, int V>
-__device__ __forceinline__ float balance_keys(const BalanceArgs &b, const float (&x)[V], float top, int e0, int count, K (&c)[V])
+template <int LANES, int V>
+__device__ __forceinline__ float balance_keys(const BalanceArgs &b, const float (&x)[V], float top, int e0, int count,
+                                              float (&c)[V])
 {
-    constexpr bool kWide = sizeof(K) == 8;
     float near = 0x1p-20f;
     if (b.softmax) {
-        K sum = 0;
+        float sum = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if constexpr (kWide) c[i] = exp((double)x[i] - (double)top);
-            else c[i] = __builtin_amdgcn_exp2f((x[i] - top) * 1.44269504088896341f);
-            sum += x[i] == x[i] ? c[i] : (K)0;
+            c[i] = __builtin_amdgcn_exp2f((x[i] - top) * 1.44269504088896341f);
+            sum += x[i] == x[i] ? c[i] : 0.0f;
         }
         sum = lanes_sum<LANES>(sum);
-        if constexpr (kWide) {
+        const float each = __builtin_amdgcn_rcpf(sum);
+        near = 0x1p-17f * each;
 #pragma unroll
-            for (int i = 0; i < V; ++i) c[i] /= sum;
-        } else {
-            const float each = __builtin_amdgcn_rcpf(sum);
-            near = 0x1p-17f * each;
-#pragma unroll
-            for (int i = 0; i < V; ++i) c[i] *= each;
-        }
+        for (int i = 0; i < V; ++i) c[i] *= each;
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if constexpr (kWide) c[i] = sigmoid64((double)x[i]);
-            else c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[i] * -1.44269504088896341f));
-        }
+        for (int i = 0; i < V; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[i] * -1.44269504088896341f));
     }
     // (Opaque: the biases would else be held in registers for all tokens.)
     int eb = e0;
     asm volatile("" : "+v"(eb));
+    if (b.bias) {
+        if constexpr (V % 8 == 0) {
+            // (One by one, each with its bound: 36.6 us instead of 30 for 32768 tokens of 256.)
+#pragma unroll
+            for (int i = 0; i < V; i += 8) {
+                float v[8];
+                load8(b.bias + eb + i, count - i, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) c[i + j] += v[j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) c[i] += i < count ? b.bias[eb + i] : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = x[i] > -__builtin_inff() && c[i] == c[i] ? c[i] : -__builtin_inff();
+    return near;
+}
+
+// The same in 64 bits, one after the other: each takes a logit's place in the
+// registers.
+template <int LANES, int V>
+__device__ __forceinline__ float balance_keys(const BalanceArgs &b, const float (&x)[V], float top, int e0, int count,
+                                              double (&c)[V])
+{
+    double sum = 1.0;
+    if (b.softmax) {
+        sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            sum += x[i] == x[i] ? exp((double)x[i] - (double)top) : 0.0;
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        sum = lanes_sum<LANES>(sum);
+    }
+    int eb = e0;
+    asm volatile("" : "+v"(eb));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        if (b.bias) c[i] += (K)(i < count ? b.bias[eb + i] : 0.0f);
-        c[i] = x[i] > -__builtin_inff() && c[i] == c[i] ? c[i] : (K)-__builtin_inff();
+        double s = b.softmax ? exp((double)x[i] - (double)top) / sum : sigmoid64((double)x[i]);
+        if (b.bias) s += (double)(i < count ? b.bias[eb + i] : 0.0f);
+        c[i] = x[i] > -__builtin_inff() && s == s ? s : -__builtin_inf();
+        __builtin_amdgcn_sched_barrier(0);
     }
-    return near;
+    return 0.0f;
 }
 
 // How many sets of the token come before this lane's, whose two largest keys are
@@ -287,7 +317,9 @@ __device__ __forceinline__ void merge8(int *p)
 }
 
 // A key and its place in the lane as one number in the keys' order: the key's bits
-// but the last four (2^-19 of it), and 15 - i.
+// but the last four, and 15 - i.  Dropping them takes a key down, by up to 15 units in
+// its last place: below 2^-19 of what is left.  So of two, the larger one's packed key
+// less the smaller one's is at most 2^-19 of the latter more than the keys' difference.
 constexpr int kNoKey = (int)0x80000000, kLeastKey = (int)0x80800000;
 
 __device__ __forceinline__ int packed_key(float c, int i)
@@ -317,7 +349,7 @@ __device__ __forceinline__ bool balance_pick_packed(const BalanceArgs &b, const 
     float near;
     {
         float c[V];
-        near = balance_keys<float, LANES, V>(b, x, top, e0, count, c);
+        near = balance_keys<LANES, V>(b, x, top, e0, count, c);
         int p[V < 8 ? 8 : V];
 #pragma unroll
         for (int i = 0; i < (V < 8 ? 8 : V); ++i) p[i] = i < V ? packed_key(c[i < V ? i : 0], i) : kNoKey;
@@ -345,7 +377,7 @@ __device__ __forceinline__ bool balance_pick_packed(const BalanceArgs &b, const 
         const bool out = before >= b.kept;
         const float least = -lanes_max<LANES>(out ? none : -value), most = lanes_max<LANES>(out ? value : none);
         const float size = lanes_max<LANES>(fabsf(two.first > none ? two.first : 0.0f) + fabsf(two.second > none ? two.second : 0.0f));
-        sure = most == none || least - most > 2.0f * near + 0x1p-17f * size;
+        sure = most == none || least - most > 2.0f * near + 0x1.2p-19f * size;      // (with the sums' rounding)
         if (out)
 #pragma unroll
             for (int i = 0; i <= KEPT; ++i) q[i] = kNoKey;
@@ -355,7 +387,7 @@ __device__ __forceinline__ bool balance_pick_packed(const BalanceArgs &b, const 
         const int m = lanes_max_int<LANES>(q[0]);
         const bool used = m >= kLeastKey;
         const float key = unpacked_key(m);
-        if (j > 0) sure = sure && (!used || last - key > near + 0x1p-18f * (fabsf(last) + fabsf(key)));
+        if (j > 0) sure = sure && (!used || last - key > near + 0x1.1p-19f * fabsf(key));
         last = key;
         if (j == b.route.choices) break;
         if (sub == first_lane<LANES>(q[0] == m, group)) {
@@ -377,7 +409,7 @@ __device__ __forceinline__ bool balance_pick(const BalanceArgs &b, const float (
     constexpr bool kWide = sizeof(K) == 8;
     const K none = -__builtin_inff();
     K c[V];
-    const float near = balance_keys<K, LANES, V>(b, x, top, e0, count, c);
+    const float near = balance_keys<LANES, V>(b, x, top, e0, count, c);
     bool sure = true;
     if (b.kept < b.sets) {
         Two<K> two{none, none};
@@ -424,6 +456,23 @@ __device__ __forceinline__ bool balance_pick(const BalanceArgs &b, const float (
 
 // Chooses for the workgroup's TOKENS tokens and counts the experts in LDS.
 // `found` (LDS): `choices` experts for every LANES lanes.
+template <class E, int V>
+__device__ __forceinline__ void balance_load(const E *p, int count, float (&x)[V])
+{
+    if constexpr (V % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 8) {
+            float v[8];
+            load8(p + i, count - i, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[i + j] = i + j < count ? v[j] : -__builtin_inff();
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = i < count ? to_f32(p[i]) : -__builtin_inff();
+    }
+}
+
 template <class E, int LANES, int V, int THREADS, int TOKENS>
 __device__ __forceinline__ void balance_choose(const BalanceArgs &b, int first, int *counts, int *found)
 {
@@ -441,18 +490,7 @@ __device__ __forceinline__ void balance_choose(const BalanceArgs &b, int first, 
         const bool live = token < last;
         const E *const row = reinterpret_cast<const E *>(a.logits) + (long long)(live ? token : last - 1) * a.ld;
         float x[V];
-        if constexpr (V % 8 == 0) {
-#pragma unroll
-            for (int i = 0; i < V; i += 8) {
-                float v[8];
-                load8(row + e0 + i, count - i, v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[i + j] = i + j < count ? v[j] : -__builtin_inff();
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[i] = i < count ? to_f32(row[e0 + i]) : -__builtin_inff();
-        }
+        balance_load<E, V>(row + e0, count, x);
         float top = 0.0f;
         if (b.softmax) {
             top = -__builtin_inff();
@@ -466,9 +504,16 @@ __device__ __forceinline__ void balance_choose(const BalanceArgs &b, int first, 
         else if (V <= 8 || a.choices <= 8) sure = balance_pick_packed<LANES, V>(b, x, top, sub, group, set, e0, count, mine);
         else sure = balance_pick<float, LANES, V>(b, x, top, sub, group, set, e0, count, mine);
         if (__ballot(!sure)) balance_pick<double, LANES, V>(b, x, top, sub, group, set, e0, count, mine);
+        // (Opaque, and the logits loaded again: what follows from these would be held in
+        // registers through the choice.)
+        int again = live ? token : last - 1;
+        float scale = b.scale;
+        asm volatile("" : "+v"(again), "+v"(scale));
+        const E *const logits = reinterpret_cast<const E *>(a.logits) + (long long)again * a.ld;
         double sum = 1.0;
         if (b.softmax && !a.normalize) {
             sum = 0.0;
+            balance_load<E, V>(logits + e0, count, x);
 #pragma unroll
             for (int i = 0; i < V; ++i) sum += x[i] == x[i] ? exp((double)x[i] - (double)top) : 0.0;
             sum = lanes_sum<LANES>(sum);
@@ -482,7 +527,7 @@ __device__ __forceinline__ void balance_choose(const BalanceArgs &b, int first, 
             if (sub + LANES * q < a.choices) {
                 e[q] = mine[sub + LANES * q];
                 if (e[q] >= 0) {
-                    const double v = (double)to_f32(row[e[q]]);
+                    const double v = (double)to_f32(logits[e[q]]);
                     w[q] = b.softmax ? exp(v - (double)top) / sum : sigmoid64(v);
                 }
             }
@@ -492,7 +537,7 @@ __device__ __forceinline__ void balance_choose(const BalanceArgs &b, int first, 
             const int j = sub + LANES * q;
             if (live && j < a.choices) {
                 const long long s = (long long)token * a.choices + j;
-                a.weights[s] = w[q] > 0.0 ? (float)(w[q] / total * (double)b.scale) : 0.0f;
+                a.weights[s] = w[q] > 0.0 ? (float)(w[q] / total * (double)scale) : 0.0f;
                 a.experts[s] = e[q];
                 if (e[q] >= 0) atomicAdd(counts + e[q], 1);
             }
