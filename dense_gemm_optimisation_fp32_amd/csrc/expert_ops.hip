@@ -176,32 +176,29 @@ constexpr double kOrthoMost = 31.0;        // of a plane's entries
 // hold (one at least).
 struct OrthoPlan {
     int64_t m, n, m_pad, n_pad;            // m <= n
-    int planes;                            // of A and B
     int64_t x_plane, g_plane;              // bytes
     int64_t blocks, strips;                // few rows: 64-column blocks of a strip, strips (else 0)
     int64_t matrix;                        // bytes of workspace a matrix
     int64_t chunk;
     int64_t shares;                        // bytes for shared tiles' sums
 
-    OrthoPlan(int dtype, int64_t batch, int64_t rows, int64_t cols)
+    OrthoPlan(int64_t batch, int64_t rows, int64_t cols)
     {
         m = rows < cols ? rows : cols;
         n = rows < cols ? cols : rows;
         m_pad = padded64(m);
         n_pad = padded64(n);
-        planes = dtype == EXPERT_BF16 ? 1 : 2;
         x_plane = m_pad * n_pad * 2;
         g_plane = m_pad * m_pad * 2;
-        matrix = 4 * x_plane + 2 * planes * g_plane + kOrthoParts * 8 + 8;
+        matrix = 4 * x_plane + 4 * g_plane + kOrthoParts * 8 + 8;
         // Few rows: one strip (up to 256 columns, of 128 rows 128), else sixteen at most
         // up to 4096 columns, of 128 rows eight.  Measured, us: four of 64 x 192 25, by the
-        // tiles 82; 64 x 384 in one strip 40.4, in six, a launch a step, 40; 128 x 128 in 32
-        // bits 56, by the tiles 102, in bfloat16 56 / 80; 128 x 512 86 / about 120 and 86 / 87, 128 x 1024
-        // 107 / about 150 and 107 / 96.
+        // tiles 82; 64 x 384 in one strip 40.4, in six, a launch a step, 40; 128 x 128 56, by the
+        // tiles 102, 128 x 512 86 / about 120, 128 x 1024 107 / about 150.
         const int64_t all = n_pad / 64;
         blocks = strips = 0;
         if (m <= 64) blocks = all <= 4 ? all : all <= 16 ? 1 : all <= 32 ? 2 : 4;
-        else if (m <= 128 && all <= (dtype == EXPERT_BF16 ? 8 : 16)) blocks = all <= 2 ? all : all <= 8 ? 1 : 2;
+        else if (m <= 128 && all <= 16) blocks = all <= 2 ? all : all <= 8 ? 1 : 2;
         if (blocks) {
             strips = (all + blocks - 1) / blocks;
             matrix = strips == 1 ? 0 : 2 * x_plane + 2 * strips * m_pad * m_pad * 4 + kOrthoParts * 8;
@@ -343,7 +340,7 @@ OrthoChoice ortho_choose(const OrthoArgs &a, int cus, bool may_share)
         // (A part of fewer than four slabs is all start and end.)
         if (!may_share || left == 0 || (slots + left) * side * side * 4 > kOrthoShares || left * slabs < 4 * slots) continue;
         const double full = large ? 1.7 : 1.25, share_mb = (slots + left) * side * side * 4 * 1e-6;
-        const double result_mb = left * side * side * 2e-6 * a.c_planes * (a.symmetric ? 2 : 1);
+        const double result_mb = left * side * side * 4e-6 * (a.symmetric ? 2 : 1);
         take(kind, n / slots * (slabs * full + more) + (double)(left * slabs) / slots * full + 8.0 + share_mb / 5.0 + 7.0 +
                        share_mb / 7.0 + result_mb / 5.0, slots, n - left);
     }
@@ -803,7 +800,7 @@ int expert_int8_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t group
 int64_t expert_orthogonalize_workspace(int dtype, int64_t batch, int64_t rows, int64_t cols)
 {
     if (!ortho_sizes_ok(dtype, batch, rows, cols) || batch == 0) return 0;
-    const OrthoPlan p(dtype, batch, rows, cols);
+    const OrthoPlan p(batch, rows, cols);
     return p.shares + p.chunk * p.matrix;
 }
 
@@ -818,7 +815,7 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
     if (ldx * size >= kMaxRowBytes || ldy * size >= kMaxRowBytes) return GEMM_F32_ERR_INVALID_VALUE;
     if (batch > 1 && (stride_y < (rows - 1) * ldy + cols)) return GEMM_F32_ERR_INVALID_VALUE;
     if (batch > 0 && (!here(X, size) || !here(Y, size))) return GEMM_F32_ERR_INVALID_VALUE;
-    const OrthoPlan p(dtype, batch, rows, cols);
+    const OrthoPlan p(batch, rows, cols);
     // A launch over the blocks of 64 x 64 holds less than 2^32 threads (256 each).
     constexpr int64_t kMostBlocks = (1 << 24) - 1;
     if (!p.strips && (p.m_pad / 64 > kMostBlocks / (p.n_pad / 64) ||
@@ -835,7 +832,7 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
     for (int64_t first = 0; first < batch; first += p.chunk) {
         const int64_t here_ = batch - first < p.chunk ? batch - first : p.chunk;
         char *const x0 = static_cast<char *>(workspace) + p.shares, *const x1 = x0 + p.chunk * 2 * p.x_plane;
-        char *const g0 = x1 + p.chunk * 2 * p.x_plane, *const g1 = g0 + p.chunk * p.planes * p.g_plane;
+        char *const g0 = x1 + p.chunk * 2 * p.x_plane, *const g1 = g0 + p.chunk * 2 * p.g_plane;
         OrthoStartArgs o{};
         o.x = static_cast<const char *>(X) + first * stride_x * size;
         o.ld = ldx;
@@ -856,15 +853,15 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
             if (status != GEMM_F32_SUCCESS) return status;
             continue;
         }
-        o.sums = reinterpret_cast<double *>(g1 + p.chunk * p.planes * p.g_plane);
+        o.sums = reinterpret_cast<double *>(g1 + p.chunk * 2 * p.g_plane);
         // bfloat16: X times a power of two is exact in one plane.
-        if (p.planes == 1) o.factors = reinterpret_cast<float *>(o.sums + p.chunk * kOrthoParts);
+        if (bf16) o.factors = reinterpret_cast<float *>(o.sums + p.chunk * kOrthoParts);
         int status = launch_ortho_start(o, bf16, (int)here_, s);
         if (status != GEMM_F32_SUCCESS) return status;
 
         OrthoArgs gram{};                                                    // A = X X^T
         gram.a_stride = gram.b_stride = 2 * p.x_plane;
-        gram.c_stride = p.planes * p.g_plane;
+        gram.c_stride = 2 * p.g_plane;
         gram.lda = gram.ldb = (int)(p.n_pad * 2);
         gram.a_bytes = gram.b_bytes = 2 * p.x_plane;
         gram.k = (int)p.n_pad;
@@ -872,26 +869,25 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
         gram.group_m = 8;
         gram.batch = (int)here_;
         gram.num_xcd = num_xcd;
-        gram.segments = p.planes == 2 ? 3 : 1;
         gram.a_low = gram.b_low = p.x_plane;
         gram.a_at = 2;
         gram.C = g0;
         gram.ldc = p.m_pad * 2;
         gram.c_plane = p.g_plane;
-        gram.c_planes = p.planes;
         gram.c = kPlaneBack;
         gram.symmetric = 1;
         gram.shares = p.shares ? static_cast<float *>(workspace) : nullptr;
 
         OrthoArgs poly = gram;                                               // B = a I + b A + c A A
         poly.A = poly.B = poly.G = g0;
-        poly.a_stride = poly.b_stride = p.planes * p.g_plane;
+        poly.a_stride = poly.b_stride = 2 * p.g_plane;
         poly.lda = poly.ldb = (int)(p.m_pad * 2);
-        poly.a_bytes = poly.b_bytes = p.planes * p.g_plane;
+        poly.a_bytes = poly.b_bytes = 2 * p.g_plane;
         poly.k = (int)p.m_pad;
         poly.a_low = poly.b_low = p.g_plane;
         poly.C = g1;
         poly.order = (int)p.m;
+        poly.segments = 3;
 
         OrthoArgs step = poly;                                               // B X
         step.G = nullptr;
@@ -900,12 +896,10 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
         step.b_stride = step.c_stride = 2 * p.x_plane;
         step.ldb = (int)(p.n_pad * 2);
         step.b_bytes = 2 * p.x_plane;
-        step.segments = p.planes == 2 ? 3 : 2;
         step.b_low = p.x_plane;
         step.cols = (int)p.n_pad;
         step.ldc = p.n_pad * 2;
         step.c_plane = p.x_plane;
-        step.c_planes = 2;
         step.c = kPlaneBack;
 
         char *now = x0, *then = x1;
@@ -913,6 +907,10 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
             const float *const f = coefficients + 3 * i;
             gram.A = gram.B = now;
             gram.factors = step.factors = i == 0 ? o.factors : nullptr;
+            // (One plane of X: its product with itself is one pair, B X two.)
+            gram.segments = gram.factors ? 1 : 3;
+            step.segments = step.factors ? 2 : 3;
+            step.a_at = step.factors ? 1 : 2;
             gram.power = 2;
             step.power = 1;
             status = launch_ortho(gram, OrthoCall{kOrthoGram, bf16, true}, cus, s);
@@ -922,12 +920,9 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
             poly.c = f[2] * kPlaneBack;
             status = launch_ortho(poly, OrthoCall{kOrthoGram, bf16, true}, cus, s);
             if (status != GEMM_F32_SUCCESS) return status;
-            // (One plane of X in the first step and in the last: see orthogonal.hpp.)
-            if (p.planes == 1) step.segments = i == 0 || i + 1 == steps ? 1 : 2;
             if (i + 1 < steps) {
                 step.B = now;
                 step.C = then;
-                step.c_planes = p.planes == 1 && i + 2 == steps ? 1 : 2;
                 status = launch_ortho(step, OrthoCall{kOrthoStep, bf16, true}, cus, s);
                 if (status != GEMM_F32_SUCCESS) return status;
                 char *const t = now;
@@ -948,7 +943,7 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
                 last.a_stride = step.b_stride, last.lda = step.ldb, last.a_bytes = step.b_bytes;
                 last.B = g1;
                 last.b_stride = step.a_stride, last.ldb = step.lda, last.b_bytes = step.a_bytes;
-                last.a_low = step.b_low, last.b_low = step.a_low, last.a_at = 1;
+                last.a_low = step.b_low, last.b_low = step.a_low, last.a_at = 3 - step.a_at;
             } else {
                 last.B = now;
             }

@@ -16,11 +16,10 @@
 // large products reach 1139 TFLOPS in half precision, 153 in 32 bits).  The
 // factor 2^11 keeps lo above the subnormals; entries stay below 2^15.9 / 2^11 = 31,
 // which the host derives from the coefficients.
-// bfloat16 results are rounded to 2^-9 at the end: for them A and B = a I + b A +
-// c A A are one plane and X two; A = hi hi^T, A A one product, B X two (in the first
-// step, where X is exact in one plane, and in the last, whose roundings no step
-// follows, one).  Measured in the 2-norm against 64 bits: 0.0017 off with all planes
-// (what the last rounding gives), 0.0018 to 0.0024 so.
+// bfloat16 matrices take the same products, for the result is rounded to them once
+// (with A and B = a I + b A + c A A in one plane half the products would do, and 26 to
+// 30 % of the entries came out a step off the rounded one; 0.2 % do).  In their first step X is exact in one plane:
+// A = hi hi^T, one product, B X two.
 //
 // A plane is rows of whole 64 columns, rows a multiple of 64, zeros outside the
 // matrix; a matrix's planes lie one after the other.  The contraction goes over the
@@ -51,7 +50,6 @@ struct OrthoArgs {
     // What becomes of the sums.
     char *C;                           // planes, or the result
     long long ldc, c_plane;            // bytes; from hi to lo
-    int c_planes;
     const char *G;                     // A's planes in B = a I + b A + c A A (else NULL)
     int order;                         // rows of the matrix that I has
     float a, b, c;                     // (c: the factor of the sums in every product)
@@ -262,8 +260,7 @@ __device__ __forceinline__ void ortho_block(const OrthoArgs &g, int matrix, int 
         if (g.G) {
             const char *const p = g.G + matrix * g.c_stride + at;
             const f16x8 hi = *reinterpret_cast<const f16x8 *>(p);
-            f16x8 lo = {};
-            if (g.c_planes > 1) lo = *reinterpret_cast<const f16x8 *>(p + g.c_plane);
+            const f16x8 lo = *reinterpret_cast<const f16x8 *>(p + g.c_plane);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 t[i] += g.b * ((float)hi[i] + (float)lo[i]);
@@ -279,7 +276,6 @@ __device__ __forceinline__ void ortho_block(const OrthoArgs &g, int matrix, int 
         if (mirror)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                if (j >= g.c_planes) break;
                 char *const q = g.C + matrix * g.c_stride + j * g.c_plane;
                 const u32x4 w = __builtin_bit_cast(u32x4, plane[v0 / 8][j]);
                 const long long across = (long long)(row0 + (l32 & ~3)) * 2;
@@ -294,7 +290,6 @@ __device__ __forceinline__ void ortho_block(const OrthoArgs &g, int matrix, int 
     const long long to = (row0 + (lane & 15)) * g.ldc + (long long)(col0 + half * 8 + (lane & 16)) * 2;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        if (j >= g.c_planes) break;
         char *const q = g.C + matrix * g.c_stride + j * g.c_plane;
         u32x4 x = __builtin_bit_cast(u32x4, plane[0][j]), y = __builtin_bit_cast(u32x4, plane[1][j]);
 #pragma unroll

@@ -224,14 +224,14 @@ int expert_int8_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t group
  * step's three coefficients a, b, c (in host memory, 3 * steps floats, read before
  * the call returns),
  *   X <- (a I + b A + c A A) X      (of a matrix with rows > cols its transposed),
- * which takes every singular value s to a s + b s^3 + c s^5.  Held in 22 bits between
- * the steps (bfloat16: A and a I + b A + c A A in 11), sums in 32.  Y may be X.
+ * which takes every singular value s to a s + b s^3 + c s^5.  X, A and a I + b A + c A A
+ * are held in 22 bits between the products, whatever the type, sums in 32; a result of
+ * dtype EXPERT_BF16 is rounded once.  Y may be X.
  *   steps 1 .. 64; coefficients that could let an entry of A, a I + b A + c A A or,
  *   before the last step, X pass 31 are refused; cols and rows below 2^22 - 64, and workgroups of 64 x 64
  *   in all below 2^24.
  * workspace: expert_orthogonalize_workspace bytes (for as many matrices at a time as
- * 2 GiB hold, one at least: about 8 bytes an entry, and of the smaller square 8, in
- * bfloat16 4).
+ * 2 GiB hold, one at least: about 8 bytes an entry, and of the smaller square 8).
  */
 int64_t expert_orthogonalize_workspace(int dtype, int64_t batch, int64_t rows, int64_t cols);
 int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, const void *X, int64_t ldx,
