@@ -420,7 +420,9 @@ __device__ __forceinline__ bool balance_pick(const BalanceArgs &b, const float (
         const bool out = before >= b.kept;
         if constexpr (!kWide) {
             const float least = -lanes_max<LANES>(out ? none : -value), most = lanes_max<LANES>(out ? value : none);
-            sure = most == none || least - most > 2.0f * near + 0x1p-21f * (fabsf(least) + fabsf(most));
+            // (By the keys' size, not the sums': keys of both signs cancel, their roundings do not.)
+            const float size = lanes_max<LANES>(fabsf(two.first > none ? two.first : 0.0f) + fabsf(two.second > none ? two.second : 0.0f));
+            sure = most == none || least - most > 2.0f * near + 0x1p-21f * size;
         }
         if (out)
 #pragma unroll

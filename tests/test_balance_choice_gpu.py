@@ -1,0 +1,83 @@
+"""Balanced routing of many tokens against the definition in 64 bits, all tokens at once:
+experts, offsets and order exactly, weights and gradients within their roundings
+(derived in test_balance_gpu.py: weights 2^-24; gradients (2 choices + 90) 2^-24 of the
+magnitudes of their terms, and half a step of the logits' type)."""
+import pytest
+import torch
+
+import dense_gemm_optimisation_fp32_amd as g
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+def definition(logits, choices, bias, kind, sets, kept, normalize, scale):
+    """Experts, weights and scores (tokens, groups), on the CPU."""
+    x = logits.double().cpu()
+    x = torch.where(x == x, x, torch.full_like(x, -INF))
+    tokens, groups = x.shape
+    if kind == "sigmoid":
+        s = 1.0 / (1.0 + torch.exp(-x))
+    else:
+        top = x.max(1, keepdim=True)[0]
+        p = torch.exp(x - torch.where(top > -INF, top, torch.zeros_like(top)))
+        s = p / p.sum(1, keepdim=True).clamp(min=1e-300)
+    key = torch.where(x > -INF, s if bias is None else s + bias.double().cpu(), torch.full_like(x, -INF))
+    of_set = key.view(tokens, sets, -1)
+    two = of_set.topk(min(2, of_set.shape[2]), dim=2)[0]
+    value = torch.where(two > -INF, two, torch.zeros_like(two)).sum(2)
+    value = torch.where(two[:, :, 0] > -INF, value, torch.full_like(value, -INF))
+    stays = torch.zeros((tokens, sets), dtype=torch.bool)
+    stays.scatter_(1, torch.sort(value, dim=1, descending=True, stable=True)[1][:, :kept], True)
+    key = torch.where(stays.unsqueeze(2), of_set, torch.full_like(of_set, -INF)).view(tokens, groups)
+    best, at = torch.sort(key, dim=1, descending=True, stable=True)
+    used, at = best[:, :choices] > -INF, at[:, :choices]
+    w = torch.where(used, s.gather(1, at), torch.zeros((), dtype=torch.float64))
+    if normalize:
+        total = w.sum(1, keepdim=True)
+        w = torch.where(total > 0, w / total, torch.zeros_like(w))
+    return torch.where(used, at, torch.full_like(at, -1)), scale * w, s
+
+
+def check(logits, choices, bias=None, kind="sigmoid", sets=1, kept=1, normalize=True, scale=1.0):
+    tokens, groups = logits.shape
+    r = g.route_balanced(logits, choices, bias=bias, scores=kind, sets=sets, kept_sets=kept, normalize=normalize, scale=scale)
+    experts, weights, s = definition(logits, choices, bias, kind, sets, kept, normalize, scale)
+    wrong = (r.experts.cpu().long() != experts).any(1)
+    assert not wrong.any(), (int(wrong.sum()), int(wrong.nonzero()[0]))
+    assert ((r.weights.double().cpu() - weights).abs() <= weights * 2.0 ** -24 * 1.001).all()
+    flat = torch.where(experts < 0, torch.full_like(experts, groups), experts).reshape(-1)
+    order, ends = torch.sort(flat, stable=True)[1], torch.bincount(flat, minlength=groups + 1)[:groups].cumsum(0)
+    assert torch.equal(r.order.cpu().long(), torch.where(torch.arange(flat.numel()) < ends[-1], order, torch.full_like(order, -1)))
+    assert torch.equal(r.offsets.cpu().long(), torch.cat((torch.zeros(1, dtype=torch.long), ends)))
+
+    grad = torch.randn((tokens, choices), generator=torch.Generator().manual_seed(tokens))
+    got = g.route_balanced_grad(logits, r, grad.cuda()).double().cpu()
+    used = experts >= 0
+    at, wg = experts.clamp(min=0), torch.where(used, weights * grad.double(), torch.zeros_like(weights))
+    dot, much = wg.sum(1, keepdim=True), wg.abs().sum(1, keepdim=True)
+    mean, size = (dot / scale, much / scale) if normalize else (torch.zeros_like(dot), torch.zeros_like(much))
+    slope = 1.0 / (1.0 + torch.exp(logits.double().cpu().gather(1, at))) if kind == "sigmoid" else torch.ones_like(weights)
+    slope = torch.where(used, slope * weights, torch.zeros_like(weights))
+    d = torch.zeros_like(s).scatter_add_(1, at, slope * (grad.double() - mean))
+    size = torch.zeros_like(s).scatter_add_(1, at, slope * (grad.double().abs() + size))
+    if kind == "softmax" and not normalize:
+        d, size = d - s * dot, size + s * much
+    room = (2 * choices + 90) * 2.0 ** -24 * size + torch.finfo(logits.dtype).eps / 2 * d.abs() + 1e-38
+    assert ((got - d).abs() <= room * 1.001).all()
+
+
+def normal(tokens, groups, dtype, seed, scale=1.5):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn((tokens, groups), generator=gen, device="cuda") * scale).to(dtype)
+
+
+@pytest.mark.parametrize("groups,sets,choices", [(256, 8, 9), (256, 8, 12), (384, 12, 8), (1000, 40, 6)])
+@pytest.mark.parametrize("large", [1.0, 64.0, 1000.0, 4096.0, 2.0 ** 20])
+def test_biases_that_cancel_in_a_set(groups, sets, choices, large):
+    """A set's two largest keys are near +large and -large: their sum is of the scores' size, but
+    each key's rounding to 32 bits goes by `large`.  By 64-bit keys, so the choice asks for them."""
+    size = groups // sets
+    bias = torch.full((sets, size), -2.0 * large)
+    bias[:, 0], bias[:, size // 2] = large, -large
+    check(normal(20000, groups, torch.float32, groups), choices, bias.reshape(-1).cuda(), "sigmoid", sets, sets // 2)
