@@ -81,3 +81,37 @@ def test_biases_that_cancel_in_a_set(groups, sets, choices, large):
     bias = torch.full((sets, size), -2.0 * large)
     bias[:, 0], bias[:, size // 2] = large, -large
     check(normal(20000, groups, torch.float32, groups), choices, bias.reshape(-1).cuda(), "sigmoid", sets, sets // 2)
+
+
+# Tokens, experts, choices, sets, kept: every kind of kernel.  Up to 8192 tokens in parts of 32, then of 128; 16
+# lanes a token with 1, 2, 4, 8 and 16 experts a lane, 64 lanes with 8, 16 and 32; up to eight choices and more
+# (more than eight of more than eight experts a lane are chosen key by key).
+SHAPES = [
+    (129, 256, 8, 8, 4), (300, 256, 12, 8, 4), (200, 256, 8, 1, 1), (257, 250, 16, 5, 3), (8192, 256, 8, 8, 4), (4099, 144, 9, 1, 1),
+    (300, 16, 3, 1, 1), (300, 30, 5, 2, 1), (300, 64, 4, 8, 4), (1000, 128, 20, 4, 4), (300, 384, 8, 12, 5), (300, 512, 10, 1, 1),
+    (300, 1000, 8, 40, 30), (300, 1000, 17, 2, 1), (150, 1024, 32, 16, 8),
+    (8193, 256, 8, 8, 4), (9001, 256, 12, 8, 4), (9001, 256, 8, 1, 1), (8200, 255, 9, 15, 7), (20000, 16, 2, 4, 2), (9000, 32, 8, 8, 8),
+    (12345, 60, 6, 6, 3), (9001, 128, 8, 8, 4), (8321, 384, 8, 12, 6), (8195, 512, 9, 4, 2), (8257, 1000, 6, 40, 20),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind,normalize", [("sigmoid", True), ("softmax", False)])
+@pytest.mark.parametrize("tokens,groups,choices,sets,kept", SHAPES)
+def test_every_kernel(tokens, groups, choices, sets, kept, kind, normalize, dtype):
+    logits = normal(tokens, groups, dtype, tokens + groups)
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    masked = torch.rand((tokens, groups), generator=gen, device="cuda") < 0.25
+    masked |= torch.rand((tokens, 1), generator=gen, device="cuda") < 0.05
+    masked[-1] = False
+    logits.masked_fill_(masked, -INF)
+    bias = normal(1, groups, torch.float32, groups, 0.1 if kind == "sigmoid" else 0.3 / groups)[0]
+    check(logits, choices, bias, kind, sets, kept, normalize, 2.5)
+
+
+@pytest.mark.parametrize("tokens,groups,choices,sets,kept", [(200, 256, 8, 8, 4), (200, 256, 12, 8, 4), (8200, 256, 8, 8, 4),
+                                                             (8200, 256, 9, 1, 1), (8200, 1000, 8, 40, 20), (8200, 60, 6, 6, 3)])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_equal_logits_without_biases(tokens, groups, choices, sets, kept, zeros):
+    """bfloat16 logits, many of them equal, without a bias and with one of zeros."""
+    check(normal(tokens, groups, torch.bfloat16, 3), choices, torch.zeros(groups, device="cuda") if zeros else None, "sigmoid", sets, kept)
