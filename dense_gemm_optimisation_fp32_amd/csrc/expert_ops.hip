@@ -148,6 +148,9 @@ constexpr int64_t kInt8MaxK = 131072;
 // 256 for each of 42 experts 79 / 20.
 constexpr int64_t kInt8FewValues = 4096, kInt8FewBytes = 66 * 1024;
 
+// Most columns to quantise: counted in 32 bits up to the end of a piece of 2048.
+constexpr int64_t kInt8MaxColumns = kMaxInt - 2048;
+
 int64_t padded16(int64_t k) { return (k + 15) / 16 * 16; }
 
 // The 8-bit tiles of `rows` rows an expert, by launch_tiles' rules (an
@@ -706,7 +709,7 @@ int expert_route_balanced_grad(int dtype, int64_t tokens, int64_t groups, int64_
 int expert_int8_quantize(int dtype, int64_t rows, int64_t k, const void *X, int layout, int64_t ld, void *codes,
                          float *scales, void *stream)
 {
-    if (!dtype_ok(dtype) || !layout_ok(layout) || !size_ok(rows, 0) || !size_ok(k, 1) || k > kMaxInt - 1024 ||
+    if (!dtype_ok(dtype) || !layout_ok(layout) || !size_ok(rows, 0) || !size_ok(k, 1) || k > kInt8MaxColumns ||
         ld < (layout == GEMM_F32_COL_MAJOR ? rows : k))
         return GEMM_F32_ERR_INVALID_VALUE;
     if (rows > 0 && (!here(X, elem(dtype)) || !here(codes, 16) || !here(scales, 4))) return GEMM_F32_ERR_INVALID_VALUE;

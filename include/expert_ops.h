@@ -29,7 +29,7 @@
  *    may be larger.  Counted in 32 bits, so below 2^31: of a product
  *    (m / 64 + 1) (groups + 2), with m / 16 where an expert has 16 rows or fewer
  *    on average, and (m / 16 + groups + 2) ceil(n / 32); of a 4-bit operand
- *    rows ceil(k / 32).
+ *    rows ceil(k / 32).  A matrix to quantise to 8 bits has up to 2^31 - 2049 columns.
  *  - A launch holds less than 2^32 threads, or the call is refused
  *    (GEMM_F32_ERR_INVALID_VALUE): route takes up to 2^29 - 128 tokens, its
  *    gradient 2^28 - 16; a 4-bit operand of rows of k columns has
