@@ -235,16 +235,13 @@ bool ortho_bounded(const float *coefficients, int steps)
         const double turn = c != 0.0 ? -b / (2.0 * c) : -1.0;
         if (turn > 0.0 && turn < end) most = std::fmax(most, q(turn));
         // X: sqrt(u) (a + b u + c u^2), largest at the end or where a + 3 b u + 5 c u^2 = 0.
+        // (Each root in the form that takes no difference of near numbers, which a small c leaves.)
         double next = top * q(end);
         const double root = 9.0 * b * b - 20.0 * a * c;
-        if (c != 0.0 && root >= 0.0) {
-            for (double sign : {-1.0, 1.0}) {
-                const double u = (-3.0 * b + sign * std::sqrt(root)) / (10.0 * c);
+        if (root >= 0.0) {
+            const double half = -0.5 * (3.0 * b + std::copysign(std::sqrt(root), b));
+            for (const double u : {half / (5.0 * c), a / half})
                 if (u > 0.0 && u < end) next = std::fmax(next, std::sqrt(u) * q(u));
-            }
-        } else if (c == 0.0 && b != 0.0) {
-            const double u = -a / (3.0 * b);
-            if (u > 0.0 && u < end) next = std::fmax(next, std::sqrt(u) * q(u));
         }
         // (The last step's X is the result, in its own type.)
         if (!(end < kOrthoMost && most < kOrthoMost && (next < kOrthoMost || i + 1 == steps))) return false;
