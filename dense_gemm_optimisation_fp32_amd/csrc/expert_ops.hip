@@ -935,7 +935,8 @@ int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, c
             last.c_stride = stride_y * size;
             last.rows = (int)rows;
             last.cols = (int)cols;
-            last.c = scale * kPlaneBack * kPlaneBack;
+            last.c = kPlaneBack * kPlaneBack;
+            last.scale = scale;
             const bool wide = wide_rows(last.C, last.ldc, cols, size) && (here_ == 1 || last.c_stride % 16 == 0);
             if (turned) {
                 // X^T B: X is the first operand, along its rows.

@@ -259,7 +259,7 @@ struct OrthoPipe {
 #pragma unroll
                     for (int nb = 0; nb < T::NB; ++nb)
 #pragma unroll
-                        for (int v = 0; v < 16; ++v) acc[mb][nb][v] *= factor;
+                        for (int v = 0; v < 16; ++v) acc[mb][nb][v] = acc[mb][nb][v] * factor * g.scale;
                 const int row = j.tile.tm * T::BM, col = j.tile.tn * T::BN;
                 lp_store<T, E, WIDE>(g.C + j.tile.matrix * g.c_stride + row * g.ldc + (long long)col * (long long)sizeof(E), g.ldc,
                                      g.rows - row, g.cols - col, nullptr, 0, wr, wc, lane_e, acc);

@@ -302,13 +302,12 @@ __global__ __launch_bounds__(WAVES * 64) void ortho_strip_kernel(OrthoStripArgs 
             for (int j = 0; j < BLOCKS; ++j) {
                 const int b = wave + j * WAVES, row = b % SIDE * 16 + l16, c = b / SIDE * 16 + 4 * grp;
                 if (last) {
-                    const float back = g.scale * kPlaneBack * kPlaneBack;
                     E *const y = reinterpret_cast<E *>(g.y) + matrix * g.stride_y;
                     struct __attribute__((packed, aligned(sizeof(E)))) Run {
                         E e[4];
                     } t;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) t.e[i] = (E)(acc[j][i] * back);
+                    for (int i = 0; i < 4; ++i) t.e[i] = (E)(acc[j][i] * (kPlaneBack * kPlaneBack) * g.scale);
                     if (row >= g.order) continue;
                     if (!a.turned && col0 + c + 4 <= g.width) {
                         *reinterpret_cast<Run *>(y + row * g.ldy + col0 + c) = t;

@@ -53,6 +53,7 @@ struct OrthoArgs {
     const char *G;                     // A's planes in B = a I + b A + c A A (else NULL)
     int order;                         // rows of the matrix that I has
     float a, b, c;                     // (c: the factor of the sums in every product)
+    float scale;                       // of the result, a product of its own: c times a small one is subnormal
     // C is symmetric: the tiles on and below its diagonal are computed, and stored
     // on both sides.
     int symmetric;
@@ -379,7 +380,7 @@ __global__ __launch_bounds__(T::THREADS * K) void ortho_kernel(OrthoArgs g)
 #pragma unroll
         for (int mb = 0; mb < T::MB; ++mb)
 #pragma unroll
-            for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] *= factor;
+            for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] = acc[mb][nb] * factor * g.scale;
         lp_store<T, E, WIDE>(g.C + matrix * g.c_stride + row * g.ldc + (long long)col * sizeof(E), g.ldc, g.rows - row,
                              g.cols - col, nullptr, 0, wr, wc, lane, acc);
     }
