@@ -173,10 +173,11 @@ int64_t padded64(int64_t k) { return (k + 63) / 64 * 64; }
 constexpr int kOrthoParts = 512;           // workgroups that sum a matrix's squares, at most
 constexpr int64_t kOrthoSpace = (int64_t)2 << 30;
 constexpr int64_t kOrthoShares = (int64_t)512 * 256 * 256 * 4;      // bytes for shared tiles' sums
+constexpr int64_t kOrthoOneStrip = (1 << 22) - 1;       // matrices of one strip a launch (1024 threads each)
 constexpr double kOrthoMost = 31.0;        // of a plane's entries
 
 // How a batch is worked on: its planes, and as many matrices at a time as 2 GiB
-// hold (one at least).
+// hold (one at least), or a launch.
 struct OrthoPlan {
     int64_t m, n, m_pad, n_pad;            // m <= n
     int64_t x_plane, g_plane;              // bytes
@@ -206,7 +207,7 @@ struct OrthoPlan {
             strips = (all + blocks - 1) / blocks;
             matrix = strips == 1 ? 0 : 2 * x_plane + 2 * strips * m_pad * m_pad * 4 + kOrthoParts * 8;
         }
-        chunk = matrix ? kOrthoSpace / matrix : batch;
+        chunk = matrix ? kOrthoSpace / matrix : kOrthoOneStrip;
         chunk = chunk < 1 ? 1 : chunk > batch ? batch : chunk;
         // (As launch_ortho has it: small tiles a workgroup's each where they are few.)
         const int64_t side = m_pad / 64;
