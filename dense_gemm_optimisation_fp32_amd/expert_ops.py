@@ -26,6 +26,7 @@ the calls below.
 from __future__ import annotations
 
 import ctypes
+import numbers
 import operator
 
 import torch
@@ -317,6 +318,30 @@ def int8_linear(x: torch.Tensor, w: Int8Tensor, offsets: torch.Tensor | None = N
                                                         _stream(x, "x")), "expert_int8_linear")
 
 
+def _number(v):
+    if isinstance(v, numbers.Real) or (getattr(v, "ndim", None) == 0):
+        return float(v)
+    raise TypeError
+
+
+def _coefficients(coefficients, steps):
+    """(a, b, c) of every step, one after the other, from one triple or one a step."""
+    steps = operator.index(steps)
+    if not 1 <= steps <= 64:
+        raise ValueError("steps must be from 1 to 64")
+    try:
+        given = list(coefficients)
+        one = not given or isinstance(given[0], numbers.Real) or getattr(given[0], "ndim", None) == 0
+        flat = tuple(_number(v) for v in given) if one else tuple(_number(v) for step in given for v in step)
+    except TypeError:
+        raise TypeError("coefficients must be three numbers, or three for each step") from None
+    if one and len(flat) == 3:
+        return flat * steps
+    if len(flat) != 3 * steps:
+        raise ValueError(f"coefficients must be three numbers, or three for each of the {steps} steps")
+    return flat
+
+
 def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), scale: float = 1.0,
                   out: torch.Tensor | None = None) -> torch.Tensor:
     """scale * x with its singular values brought near one and its singular vectors
@@ -325,16 +350,21 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
 
     From x / |x|, ``steps`` times X <- (a I + b A + c A A) X with A = X X^T, which
     takes a singular value s to a s + b s^3 + c s^5.  ``coefficients``: (a, b, c), or
-    one such triple a step.  The result has x's type; out may be x."""
+    one such triple a step.  The result has x's type and unit stride along x's axis, as
+    out has to; out may be x."""
+    flat = _coefficients(coefficients, steps)
     if isinstance(x, torch.Tensor) and x.dim() in (2, 3) and x.stride(-1) != 1 and x.shape[-1] > 1 and x.stride(-2) == 1:
-        turned = orthogonalize(x.transpose(-1, -2), steps, coefficients, scale, None if out is None else out.transpose(-1, -2))
+        if out is not None:
+            if not isinstance(out, torch.Tensor):
+                raise TypeError("out must be a tensor")
+            if out.shape != x.shape:
+                raise ValueError(f"out must have x's shape {tuple(x.shape)}")
+            if out.shape[-2] > 1 and out.stride(-2) != 1:
+                raise ValueError("out needs unit stride along the same axis as x, its columns")
+        turned = _orthogonalize(x.transpose(-1, -2), flat, scale, None if out is None else out.transpose(-1, -2))
         return turned.transpose(-1, -2) if out is None else out
-    steps = operator.index(steps)
-    if not 1 <= steps <= 64:
-        raise ValueError("steps must be from 1 to 64")
-    flat = tuple(coefficients)
-    if flat and not isinstance(flat[0], (int, float)):
-        flat = tuple(v for step in flat for v in step)
-    elif len(flat) == 3:
-        flat = flat * steps
-    return _checked((_module or _binding()).orthogonalize(x, steps, flat, scale, out, _stream(x, "x")), "expert_orthogonalize")
+    return _orthogonalize(x, flat, scale, out)
+
+
+def _orthogonalize(x, flat, scale, out):
+    return _checked((_module or _binding()).orthogonalize(x, len(flat) // 3, flat, scale, out, _stream(x, "x")), "expert_orthogonalize")
