@@ -19,8 +19,11 @@
 // Which expert is chosen goes by differences of keys: in 32 bits the last bits
 // of an exponential decided one choice in about twenty thousand tokens (256
 // experts).  A choice is first made in 32 bits with bounds on their errors; where
-// two keys, or two sets, whose order matters are nearer than those (few tokens,
-// unless many logits are equal) the wavefront chooses again in 64 bits.
+// two keys, or two sets, whose order matters are nearer than those the wavefront
+// chooses again in 64 bits.  With biases that differ from expert to expert those are
+// few: 1 token in 1000.  Equal keys are nearer than any bound, and logits of 16 bits
+// with equal biases, or none, have many: of random ones (256 experts, 8 choices) 3 tokens
+// in 10, 3 of 4 wavefronts.
 //
 // A token is held by LANES lanes.  A set takes a power of two of them
 // (`lanes`), each `each` neighbouring experts, so that a set's two largest are
@@ -28,8 +31,9 @@
 // the experts in order.
 //
 // What bounds it is the vector unit, not memory.  One MI355X, 32768 tokens of 256
-// bfloat16 logits, 8 choices from 4 of 8 sets: 30 us to choose (its bytes would take
-// 4), 11.4 to place.  With keys compared lane by lane at every choice, instead of sorted
+// bfloat16 logits, 8 choices from 4 of 8 sets, random biases: 30 us to choose (its
+// bytes would take 4), 11.4 to place; both together 41, with biases of zeros 66, without
+// 62 (32-bit logits 39, 47 and 45).  With keys compared lane by lane at every choice, instead of sorted
 // ones, choosing took 5 more.  5003 tokens of 60 32-bit logits, 6 choices: 13.3 and 4.7; 16 tokens of
 // 64, chosen and placed in one launch: 6.4, the launch and one chain of latencies.
 #pragma once
@@ -456,8 +460,7 @@ __device__ __forceinline__ bool balance_pick(const BalanceArgs &b, const float (
     return sure;
 }
 
-// Chooses for the workgroup's TOKENS tokens and counts the experts in LDS.
-// `found` (LDS): `choices` experts for every LANES lanes.
+// `count` logits from p on, -inf past them.
 template <class E, int V>
 __device__ __forceinline__ void balance_load(const E *p, int count, float (&x)[V])
 {
@@ -475,6 +478,8 @@ __device__ __forceinline__ void balance_load(const E *p, int count, float (&x)[V
     }
 }
 
+// Chooses for the workgroup's TOKENS tokens and counts the experts in LDS.
+// `found` (LDS): `choices` experts for every LANES lanes.
 template <class E, int LANES, int V, int THREADS, int TOKENS>
 __device__ __forceinline__ void balance_choose(const BalanceArgs &b, int first, int *counts, int *found)
 {

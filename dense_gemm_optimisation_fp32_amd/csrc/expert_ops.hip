@@ -198,7 +198,10 @@ struct OrthoPlan {
         // Few rows: one strip (up to 256 columns, of 128 rows 128), else sixteen at most
         // up to 4096 columns, of 128 rows eight.  Measured, us: four of 64 x 192 25, by the
         // tiles 82; 64 x 384 in one strip 40.4, in six, a launch a step, 40; 128 x 128 56, by the
-        // tiles 102, 128 x 512 86 / about 120, 128 x 1024 107 / about 150.
+        // tiles 102, 128 x 512 86 / about 120, 128 x 1024 106 (bfloat16 107), 128 x 1088 by the
+        // tiles 152 (143).  Longer ones of 64 rows stay in strips of 256 columns, each of which
+        // adds up the shares of all in every step: 64 x 4096 69, 16384 107, 65536 263, 131072 843;
+        // the tiles have not been measured there.
         const int64_t all = n_pad / 64;
         blocks = strips = 0;
         if (m <= 64) blocks = all <= 4 ? all : all <= 16 ? 1 : all <= 32 ? 2 : 4;
@@ -209,7 +212,9 @@ struct OrthoPlan {
         }
         chunk = matrix ? kOrthoSpace / matrix : kOrthoOneStrip;
         chunk = chunk < 1 ? 1 : chunk > batch ? batch : chunk;
-        // (As launch_ortho has it: small tiles a workgroup's each where they are few.)
+        // (Small tiles are a workgroup's each where they are few, whatever their length.  From
+        // 4096 columns on sharing them would be faster, 32 bits, us, so / shared: 1024 x 1024 262 / 263,
+        // 1024 x 4096 547 / 525, 768 x 4096 482 / 434, 768 x 16384 1330 / 892, 512 x 32768 2192 / 869.)
         const int64_t side = m_pad / 64;
         shares = !strips && chunk * (side * (side + 1) / 2) > 256 ? kOrthoShares : 0;
     }

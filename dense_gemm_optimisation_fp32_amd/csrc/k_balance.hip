@@ -13,6 +13,11 @@ int launch_choose(const BalanceArgs &b, hipStream_t s)
     // Half the threads where a lane's keys would not fit the registers of all.
     constexpr int THREADS = V > 16 ? 512 : kRouteThreads;
     const int found = balance_found_words(LANES, THREADS, a.choices), place = route_place_words(a.groups);
+    // One launch, of one workgroup, as long as it holds all tokens, for it needs no
+    // workspace.  Measured, us, 8 choices, one launch / two (parts of 32 tokens): 64 experts, 16
+    // tokens 6.8 / 8.5, 64 9.7 / 10.4, 96 11.6 / 10.4, 128 15.0 / 10.4; 256 experts, 16 tokens
+    // 10.9 / 16.1, 48 24 / 27, 64 30 / 27, 128 57 / 27; 512 experts 16 9.8 / 14.4, 64 25.7 / 24.6,
+    // 128 49 / 27.
     if constexpr (V <= 16)
         if (a.tokens <= kRouteTokens)
             return launch(balance_one_kernel<E, LANES, V>, 1, kRouteThreads,

@@ -10,14 +10,14 @@
 // t is number w + t: along the run one of the two goes up from part to part.
 //
 // One MI355X, 256 x 256 tiles: B X of 4096 x 4096 in three pairs of planes, a tile a
-// workgroup, 350 us (1.18 PFLOPS; matrix cores 72 % busy).  X X^T of 136 such tiles, all
+// workgroup, 340 us (1.21 PFLOPS; matrix cores 71 % busy).  X X^T of 136 such tiles, all
 // shared, 214 and 39 for joining them (136 workgroups with a tile each: 330); what
 // the shares cost is their bytes, 64 MiB written and read.  B X of 16 matrices of 2048 x
-// 4096, two pairs, 1048 (1.05 PFLOPS, 58 % busy), eight tiles a workgroup: a tile's stores
+// 4096, three pairs, 1500 (1.10 PFLOPS, 62 % busy), eight tiles a workgroup: a tile's stores
 // leave in a burst of all CUs, and the next tile's first barrier waits for them too (vmcnt
 // counts loads and stores together): about 18 us a tile.  Tiles taken in an order rotated
 // from workgroup to workgroup, so that bursts do not meet, read more from beyond the L2
-// and took 1251; planes with rows 128 bytes longer than whole KiB made 1 % of it, and lost
+// and took 1251 us instead of 991 in two pairs; planes with rows 128 bytes longer than whole KiB made 1 % of it, and lost
 // as much at 4096 x 4096.
 #pragma once
 

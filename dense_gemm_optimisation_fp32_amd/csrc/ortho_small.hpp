@@ -28,7 +28,7 @@ constexpr int strip_chunks(int rows) { return rows * 8; }       // of a plane's 
 struct OrthoStripArgs {
     OrthoStartArgs start;              // x, its sums of squares (several strips), its shape; planes
     char *planes_out;                  // several strips: the next X
-    const float *shares;               // (batch, strips, 64, 64): of X X^T, and of the next one
+    const float *shares;               // (batch, strips, ROWS, ROWS): of X X^T, and of the next one
     float *shares_out;
     int strips, steps;
     int order, width;                  // rows of X, columns

