@@ -134,8 +134,8 @@ __global__ __launch_bounds__(256) void int8_quantize_rows_kernel(Int8Args a)
 // the columns 16 at a time; the second reading comes from the caches.  Far from
 // memory's rate: a lane loads one value at a time, and a CU has 64 rows, so that few
 // long rows go column after column on few CUs.  One MI355X, us, bfloat16 / 32 bits (rows
-// contiguous along k): 14336 rows of 4096 177 / 204 (33 / 56), 4096 of 14336 594 / 653
-// (27 / 42), 1024 of 4096 87 / 87 (4 / 4), 4096 of 1024 25 / 25 (4 / 4).
+// contiguous along k): 14336 rows of 4096 177 / 204 (27 / 42), 4096 of 14336 594 / 653
+// (33 / 56), 1024 of 4096 87 / 87 (4 / 4), 4096 of 1024 25 / 25 (4 / 4).
 template <class E>
 __global__ __launch_bounds__(1024) void int8_quantize_columns_kernel(Int8Args a)
 {
